@@ -8,6 +8,11 @@ pointers, sizes and the current HIP stream. Every step of the computation runs
 in the library's HIP kernels; there is no fallback. PyTorch provides device
 memory and streams.
 
+Around the step it has training operators that keep their activations in 8
+bits: activation checkpoints, layer norm / RMS norm and the gated
+feed-forward block, whose backward passes read a checkpoint and produce the
+binary32 gradients that the step's quantize takes.
+
 Layouts (MS-AMP "Optimization Level" page, sections O2/O3 and the table):
   O2: grad FP8 (per-tensor scale), exp_avg FP8 E4M3 (own scale), exp_avg_sq
       FP16, weight FP16.
@@ -38,6 +43,9 @@ __all__ = [
     "quantize_adamw_o2_step_devconst", "quantize_adamw_o3_step_devconst",
     # ablations
     "adamw_o2_step_delayed", "adamw_o2_step_scaled_v",
+    # training operators with 8-bit activation checkpoints
+    "Checkpoint", "new_checkpoint", "checkpoint_save", "checkpoint_load",
+    "layernorm_forward", "layernorm_backward", "gated_ffn_forward", "gated_ffn_backward", "ACTIVATIONS",
     # state helpers
     "new_meta", "allocate_state", "flat_views", "state_bytes_per_param",
     # measurement and test aids
@@ -58,7 +66,12 @@ PROBE_F16_TO_F32 = 5
 # kernel kinds of msamp_profile_read, in enum order
 KERNELS = ["amax", "quantize_fp8", "dequantize_fp8", "step_pass1", "o2_pass2", "o3_pass2",
            "o3_pass3", "finalize", "amax_finalize", "o2_delayed", "rmw_probe", "quantize_pass1",
-           "read_probe", "copy_probe", "qp1_probe"]
+           "read_probe", "copy_probe", "qp1_probe", "checkpoint_save", "checkpoint_load",
+           "norm_forward", "norm_backward", "norm_reduce", "ffn_forward", "ffn_recompute", "ffn_dx", "ffn_dw",
+           "ffn_layout", "ffn_reduce"]
+
+# msamp_activation by name
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "_lib", "libmsamp.so")
@@ -81,6 +94,25 @@ class _HParams(ctypes.Structure):
 
 class _StepConstants(ctypes.Structure):
     _fields_ = [(k, ctypes.c_float) for k in ("b1", "ob1", "b2", "ob2", "eps", "ss", "ibs", "dec", "wd")]
+
+
+class _Checkpoint(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("ld_scales", ctypes.c_int64), ("fmt", ctypes.c_int)]
+
+
+class _GatedFfn(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("ffn", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("act", ctypes.c_int),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_ckpt", ctypes.POINTER(_Checkpoint)),
+                ("w_gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64),
+                ("w_up", ctypes.c_void_p), ("ld_up", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+                ("dw_gate", ctypes.c_void_p), ("ld_dw_gate", ctypes.c_int64),
+                ("dw_up", ctypes.c_void_p), ("ld_dw_up", ctypes.c_int64),
+                ("dw_dtype", ctypes.c_int), ("dw_accumulate", ctypes.c_int)]
 
 
 _lib = None
@@ -186,6 +218,25 @@ def lib():
         L.msamp_profile_read.argtypes = [ctypes.c_int, ctypes.POINTER(i64),
                                          ctypes.POINTER(ctypes.c_double)]
         L.msamp_profile_read.restype = st
+        ck, dt, ffn = ctypes.POINTER(_Checkpoint), ctypes.c_int, ctypes.POINTER(_GatedFfn)
+        L.msamp_checkpoint_save.argtypes = [i64, i64, vp, i64, dt, ck, vp]
+        L.msamp_checkpoint_save.restype = st
+        L.msamp_checkpoint_load.argtypes = [i64, i64, ck, vp, i64, dt, vp]
+        L.msamp_checkpoint_load.restype = st
+        L.msamp_layernorm_forward.argtypes = [i64, i64, vp, i64, ck, dt, vp, vp, dt, vp, i64, vp, vp,
+                                              ctypes.c_double, ck, vp]
+        L.msamp_layernorm_forward.restype = st
+        L.msamp_layernorm_backward_workspace.argtypes = [i64, i64]
+        L.msamp_layernorm_backward_workspace.restype = i64
+        L.msamp_layernorm_backward.argtypes = [i64, i64, vp, i64, vp, i64, ck, dt, vp, dt, vp, vp, vp, i64, vp, vp,
+                                               ctypes.c_int, vp, i64, vp]
+        L.msamp_layernorm_backward.restype = st
+        for f in ("msamp_gated_ffn_forward_workspace", "msamp_gated_ffn_backward_workspace"):
+            getattr(L, f).argtypes = [ffn]
+            getattr(L, f).restype = i64
+        for f in ("msamp_gated_ffn_forward", "msamp_gated_ffn_backward"):
+            getattr(L, f).argtypes = [ffn, vp, i64, vp]
+            getattr(L, f).restype = st
         L.msamp_kernel_name.argtypes = [ctypes.c_int]
         L.msamp_kernel_name.restype = ctypes.c_char_p
         _lib = L
@@ -716,6 +767,287 @@ def profile_read(kernel: str):
     ms = ctypes.c_double(0.0)
     _check(lib().msamp_profile_read(kind, ctypes.byref(n), ctypes.byref(ms)))
     return int(n.value), float(ms.value)
+
+
+# ------------------------------------------------------ training operators ---
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+GROUP = 32  # elements of a checkpoint's group (MSAMP_CHECKPOINT_GROUP)
+
+
+def _device_of(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s is not a tensor" % name)
+    if t.device.type != "cuda":
+        raise ValueError("%s is not on a GPU" % name)
+    return t.device
+
+
+def _matrix(t, name: str, device, dtype, shape, written: bool = False):
+    """(pointer, distance between rows) of a matrix argument."""
+    if _device_of(t, name) != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    rows, cols = shape
+    if rows == 0 or cols == 0:
+        return None, 0
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError("%s: the elements of a row must be consecutive" % name)
+    if rows == 1:
+        ld = cols
+    elif written and ld < cols:
+        raise ValueError("%s: its rows overlap" % name)
+    return t.data_ptr(), ld
+
+
+def _vector(t, name: str, device, dtype, n: int):
+    if _device_of(t, name) != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError("%s has shape %s, expected (%d,)" % (name, tuple(t.shape), n))
+    if not t.is_contiguous():
+        raise ValueError("%s is not contiguous" % name)
+    return t.data_ptr() if n else None
+
+
+class Checkpoint:
+    """An activation [rows, cols] in 8 bits: FP8 codes, and for each group of
+    32 elements of a row one power-of-two scale 2^e as the byte e + 127 (see
+    msamp_checkpoint in include/msamp.h).
+
+    codes is a byte tensor (uint8, or a float8 one read as bytes) of at least
+    cols columns, scales uint8 of at least ceil(cols / 32), both with
+    consecutive rows' elements; what lies behind them is neither read nor
+    written."""
+
+    __slots__ = ("codes", "scales", "cols", "fmt", "rows", "device", "_c", "_flat")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: int = E4M3):
+        cols = int(cols)
+        for t, need, name in ((codes, cols, "codes"), (scales, -(-cols // GROUP), "scales")):
+            _device_of(t, name)
+            if t.element_size() != 1:
+                raise TypeError("%s has dtype %s, expected bytes" % (name, t.dtype))
+            if cols < 0 or t.dim() != 2 or t.shape[1] < need:
+                raise ValueError("%s has shape %s, expected at least %d columns" % (name, tuple(t.shape), need))
+            if t.stride(1) != 1 and t.shape[1] > 1:
+                raise ValueError("%s: the elements of a row must be consecutive" % name)
+        if codes.shape[0] != scales.shape[0]:
+            raise ValueError("codes has %d rows, scales %d" % (codes.shape[0], scales.shape[0]))
+        if codes.device != scales.device:
+            raise ValueError("scales is on %s, expected %s" % (scales.device, codes.device))
+        self.codes, self.scales, self.cols, self.fmt = codes, scales, cols, int(fmt)
+        self.rows, self.device = codes.shape[0], codes.device
+        empty = self.rows == 0 or cols == 0
+        self._c = _Checkpoint(None if empty else codes.data_ptr(), codes.stride(0),
+                              None if empty else scales.data_ptr(), scales.stride(0), self.fmt)
+        self._flat = self.rows <= 1 or (codes.stride(0) >= cols and scales.stride(0) >= -(-cols // GROUP))
+
+    def _arg(self, name: str, device, shape, written: bool = False):
+        if self.device != device:
+            raise ValueError("%s is on %s, expected %s" % (name, self.device, device))
+        if (self.rows, self.cols) != tuple(shape):
+            raise ValueError("%s has shape %s, expected %s" % (name, (self.rows, self.cols), tuple(shape)))
+        if written and not self._flat:
+            raise ValueError("%s: its rows overlap" % name)
+        return ctypes.byref(self._c)
+
+
+def new_checkpoint(rows: int, cols: int, fmt: int = E4M3, device="cuda") -> Checkpoint:
+    """A checkpoint of its own memory, its rows padded to whole groups:
+    33 bytes for every 32 elements."""
+    groups = -(-int(cols) // GROUP)
+    return Checkpoint(torch.empty((rows, groups * GROUP), dtype=torch.uint8, device=device),
+                      torch.empty((rows, groups), dtype=torch.uint8, device=device), cols, fmt)
+
+
+def _dtype_of(t, name: str) -> int:
+    _device_of(t, name)
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions" % name)
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError("%s has dtype %s, expected float32, float16 or bfloat16" % (name, t.dtype))
+    return d
+
+
+def _input(x, device, dtype, shape):
+    """(pointer, distance between rows, checkpoint) of x or its checkpoint."""
+    if isinstance(x, Checkpoint):
+        return None, 0, x._arg("x", device, shape)
+    p, ld = _matrix(x, "x", device, dtype, shape)
+    return p, ld, None
+
+
+def checkpoint_save(x: torch.Tensor, ckpt: Checkpoint) -> None:
+    """ckpt <- x in 8 bits, in one pass. x is [rows, cols], float32, float16
+    or bfloat16; its rows may lie apart."""
+    d = _dtype_of(x, "x")
+    p, ld = _matrix(x, "x", x.device, x.dtype, x.shape)
+    c = ckpt._arg("ckpt", x.device, x.shape, True)
+    with torch.cuda.device(x.device):
+        _check(lib().msamp_checkpoint_save(x.shape[0], x.shape[1], p, ld, d, c, _stream(x.device)))
+
+
+def checkpoint_load(ckpt: Checkpoint, out: torch.Tensor) -> None:
+    """out <- the values of ckpt, rounded to out's dtype (exact for bfloat16
+    and float32)."""
+    d = _dtype_of(out, "out")
+    p, ld = _matrix(out, "out", out.device, out.dtype, out.shape, True)
+    c = ckpt._arg("ckpt", out.device, out.shape)
+    with torch.cuda.device(out.device):
+        _check(lib().msamp_checkpoint_load(out.shape[0], out.shape[1], c, p, ld, d, _stream(out.device)))
+
+
+def _norm_weights(weight, bias, device, dtype, cols: int):
+    """(weight pointer, bias pointer, their dtype)."""
+    wdt = dtype
+    for t in (bias, weight):
+        if t is not None:
+            wdt = t.dtype
+    if wdt not in (dtype, torch.float32):
+        raise TypeError("weight and bias must be %s or float32" % dtype)
+    w = None if weight is None else _vector(weight, "weight", device, wdt, cols)
+    b = None if bias is None else _vector(bias, "bias", device, wdt, cols)
+    return w, b, _DTYPES[wdt]
+
+
+def layernorm_forward(x, weight, bias, y: torch.Tensor, mean, rstd: torch.Tensor, *, eps: float = 1e-5,
+                      save: Optional[Checkpoint] = None) -> None:
+    """y <- layer norm of x's rows (RMS norm with mean=None), times weight
+    plus bias (either may be None). mean and rstd (float32, one value a row)
+    receive the statistics that the backward pass takes.
+
+    x is a matrix of y's dtype, or a Checkpoint, which is read in its place
+    (to form y again in a backward pass). save: a Checkpoint that receives x
+    in the same pass."""
+    d = _dtype_of(y, "y")
+    dev, shape = y.device, y.shape
+    rows, cols = shape
+    py, ldy = _matrix(y, "y", dev, y.dtype, shape, True)
+    px, ldx, ck = _input(x, dev, y.dtype, shape)
+    w, b, wd = _norm_weights(weight, bias, dev, y.dtype, cols)
+    m = None if mean is None else _vector(mean, "mean", dev, torch.float32, rows)
+    r = _vector(rstd, "rstd", dev, torch.float32, rows)
+    sv = None if save is None else save._arg("save", dev, shape, True)
+    with torch.cuda.device(dev):
+        _check(lib().msamp_layernorm_forward(rows, cols, px, ldx, ck, d, w, b, wd, py, ldy, m, r, float(eps), sv,
+                                             _stream(dev)))
+
+
+def layernorm_backward(dy: torch.Tensor, x, weight, mean, rstd: torch.Tensor, dx: torch.Tensor, dweight, dbias,
+                       *, accumulate: bool = False) -> None:
+    """Gradients of layernorm_forward from dy and its x (a matrix, or the
+    Checkpoint saved there), mean and rstd: dx of dy's dtype; dweight and
+    dbias in float32, either may be None; accumulate adds them to what is
+    there."""
+    d = _dtype_of(dy, "dy")
+    dev, shape = dy.device, dy.shape
+    rows, cols = shape
+    pdy, lddy = _matrix(dy, "dy", dev, dy.dtype, shape)
+    px, ldx, ck = _input(x, dev, dy.dtype, shape)
+    w, _, wd = _norm_weights(weight, None, dev, dy.dtype, cols)
+    m = None if mean is None else _vector(mean, "mean", dev, torch.float32, rows)
+    r = _vector(rstd, "rstd", dev, torch.float32, rows)
+    pdx, lddx = _matrix(dx, "dx", dev, dy.dtype, shape, True)
+    dw = None if dweight is None else _vector(dweight, "dweight", dev, torch.float32, cols)
+    db = None if dbias is None else _vector(dbias, "dbias", dev, torch.float32, cols)
+    with torch.cuda.device(dev):
+        n, ws = 0, None
+        if dw is not None or db is not None:
+            n = _workspace_bytes(lib().msamp_layernorm_backward_workspace(rows, cols))
+            ws = _workspace(n, dev)
+        _check(lib().msamp_layernorm_backward(rows, cols, pdy, lddy, px, ldx, ck, d, w, wd, m, r, pdx, lddx, dw, db,
+                                              int(bool(accumulate)), None if ws is None else ws.data_ptr(), n,
+                                              _stream(dev)))
+
+
+def _workspace_bytes(n: int) -> int:
+    if n < 0:
+        raise MsampError(1, lib().msamp_last_error().decode())
+    return n
+
+
+def _workspace(n: int, device):
+    """n bytes that belong to the current stream (and to the graph that is
+    being captured on it, if any)."""
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _gated_ffn(x, w_gate, w_up, act: str, dev, dt, tokens: int) -> _GatedFfn:
+    if act not in ACTIVATIONS:
+        raise ValueError("act must be one of %s" % ", ".join(ACTIVATIONS))
+    if dt not in (torch.float16, torch.bfloat16):
+        raise TypeError("the gated feed-forward block takes float16 or bfloat16, not %s" % dt)
+    if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
+        raise ValueError("w_gate must be a tensor of two dimensions")
+    ffn, hidden = w_gate.shape
+    a = _GatedFfn()
+    a.tokens, a.hidden, a.ffn = tokens, hidden, ffn
+    a.dtype, a.act = _DTYPES[dt], ACTIVATIONS[act]
+    if isinstance(x, Checkpoint):
+        x._arg("x", dev, (tokens, hidden))
+        a.x_ckpt = ctypes.pointer(x._c)
+    else:
+        a.x, a.ldx = _matrix(x, "x", dev, dt, (tokens, hidden))
+    a.w_gate, a.ld_gate = _matrix(w_gate, "w_gate", dev, dt, (ffn, hidden))
+    a.w_up, a.ld_up = _matrix(w_up, "w_up", dev, dt, (ffn, hidden))
+    return a
+
+
+def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, h: torch.Tensor, *,
+                      act: str = "silu") -> None:
+    """h <- act(x w_gate^T) * (x w_up^T), both projections, the activation
+    and the product in one kernel. x [tokens, hidden], w_gate and w_up [ffn,
+    hidden], h [tokens, ffn], all float16 or all bfloat16; act is "silu",
+    "gelu" or "gelu_tanh". Nothing else is kept: gated_ffn_backward takes x."""
+    _dtype_of(h, "h")
+    dev, dt = h.device, h.dtype
+    a = _gated_ffn(x, w_gate, w_up, act, dev, dt, h.shape[0])
+    a.h, a.ldh = _matrix(h, "h", dev, dt, (a.tokens, a.ffn), True)
+    if a.x_ckpt:
+        raise TypeError("the forward pass takes x itself, not a checkpoint")
+    with torch.cuda.device(dev):
+        n = _workspace_bytes(lib().msamp_gated_ffn_forward_workspace(ctypes.byref(a)))
+        ws = _workspace(n, dev)
+        _check(lib().msamp_gated_ffn_forward(ctypes.byref(a), None if ws is None else ws.data_ptr(), n, _stream(dev)))
+
+
+def gated_ffn_backward(dh: torch.Tensor, x, w_gate: torch.Tensor, w_up: torch.Tensor, dx: torch.Tensor,
+                       dw_gate: torch.Tensor, dw_up: torch.Tensor, *, act: str = "silu",
+                       h: Optional[torch.Tensor] = None, accumulate: bool = False) -> None:
+    """Gradients of gated_ffn_forward from dh and its x, a matrix or a
+    Checkpoint of it; gate and up are formed again. dw_gate and dw_up are
+    float32 (what amax and the quantizing steps take; accumulate adds to what
+    is there) or of the weights' dtype. h, if given, receives the forward
+    pass's product again (the next projection's gradient needs it)."""
+    _dtype_of(dh, "dh")
+    dev, dt = dh.device, dh.dtype
+    a = _gated_ffn(x, w_gate, w_up, act, dev, dt, dh.shape[0])
+    rows, k, f = a.tokens, a.hidden, a.ffn
+    a.dh, a.lddh = _matrix(dh, "dh", dev, dt, (rows, f))
+    a.dx, a.lddx = _matrix(dx, "dx", dev, dt, (rows, k), True)
+    if h is not None:
+        a.h, a.ldh = _matrix(h, "h", dev, dt, (rows, f), True)
+    wdt = dw_gate.dtype if isinstance(dw_gate, torch.Tensor) else None
+    if wdt not in (dt, torch.float32):
+        raise TypeError("dw_gate must be a %s or float32 tensor" % dt)
+    if accumulate and wdt != torch.float32:
+        raise TypeError("accumulate needs float32 weight gradients")
+    a.dw_gate, a.ld_dw_gate = _matrix(dw_gate, "dw_gate", dev, wdt, (f, k), True)
+    a.dw_up, a.ld_dw_up = _matrix(dw_up, "dw_up", dev, wdt, (f, k), True)
+    a.dw_dtype, a.dw_accumulate = _DTYPES[wdt], int(bool(accumulate))
+    with torch.cuda.device(dev):
+        n = _workspace_bytes(lib().msamp_gated_ffn_backward_workspace(ctypes.byref(a)))
+        ws = _workspace(n, dev)
+        _check(lib().msamp_gated_ffn_backward(ctypes.byref(a), None if ws is None else ws.data_ptr(), n,
+                                              _stream(dev)))
 
 
 # ----------------------------------------------------------- state helpers ---

@@ -10,9 +10,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libmsamp.so")
-SOURCES = [os.path.join(CSRC, "kernels.hip"), os.path.join(CSRC, "abi.hip")]
-HEADERS = [os.path.join(CSRC, "codec.hpp"), os.path.join(CSRC, "device.hpp"), os.path.join(CSRC, "kernels.hpp"),
-           os.path.join(INCLUDE, "msamp.h")]
+SOURCES = [os.path.join(CSRC, n) for n in ("kernels.hip", "abi.hip", "norm.hip", "ffn.hip", "train_abi.hip")]
+HEADERS = [os.path.join(CSRC, n) for n in ("codec.hpp", "device.hpp", "kernels.hpp", "host.hpp", "train.hpp",
+                                           "checkpoint.hpp", "ffn.hpp")] + [os.path.join(INCLUDE, "msamp.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -27,14 +27,17 @@ FLAGS = ["-std=c++17", "-O3", "-fPIC", "--offload-arch=" + ARCH, "-ffp-contract=
 def build(verbose: bool = False) -> str:
     """Compile every HIP source and link libmsamp.so. Always rebuilds."""
     os.makedirs(LIB_DIR, exist_ok=True)
-    objs = []
+    objs, running = [], []
     for src in SOURCES:
         obj = os.path.join(LIB_DIR, os.path.basename(src) + ".o")
         cmd = [HIPCC] + FLAGS + ["-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd))
-        subprocess.run(cmd, check=True)
+        running.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    failed = [cmd for cmd, p in running if p.wait() != 0]
+    if failed:
+        raise RuntimeError("compilation failed: " + " ".join(failed[0]))
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:

@@ -19,13 +19,15 @@
 #include <unordered_map>
 #include <vector>
 
+#include "host.hpp"
 #include "kernels.hpp"
 #include "msamp.h"
 
 namespace msamp {
-namespace {
 
+namespace {
 thread_local std::string g_last_error;
+}
 
 msamp_status fail(msamp_status st, const std::string& msg) {
   g_last_error = msg;
@@ -37,11 +39,9 @@ msamp_status fail_hip(hipError_t e, const char* what) {
   return fail(MSAMP_E_HIP, msg);
 }
 
-#define MSAMP_TRY(expr)                 \
-  do {                                  \
-    msamp_status st__ = (expr);         \
-    if (st__ != MSAMP_OK) return st__;  \
-  } while (0)
+void clear_error() { g_last_error.clear(); }
+
+namespace {
 
 // ------------------------------------------------------------ profiler ---
 
@@ -86,10 +86,9 @@ Profiler& profiler() {
   return *p;
 }
 
-// Runs 'launch' (which enqueues one kernel and returns its launch status),
-// bracketed by events when profiling is on.
-template <typename F>
-hipError_t timed(msamp_kernel_kind kind, hipStream_t s, F&& launch) {
+}  // namespace
+
+hipError_t timed_call(msamp_kernel_kind kind, hipStream_t s, hipError_t (*launch)(void*), void* ctx) {
   Profiler& p = profiler();
   hipEvent_t a = nullptr, b = nullptr;
   bool on;
@@ -102,7 +101,7 @@ hipError_t timed(msamp_kernel_kind kind, hipStream_t s, F&& launch) {
     }
   }
   if (on && a && b) (void)hipEventRecord(a, s);
-  hipError_t e = launch();
+  hipError_t e = launch(ctx);
   if (on && a && b) {
     (void)hipEventRecord(b, s);
     std::lock_guard<std::mutex> lk(p.mu);
@@ -110,6 +109,8 @@ hipError_t timed(msamp_kernel_kind kind, hipStream_t s, F&& launch) {
   }
   return e;
 }
+
+namespace {
 
 // ---------------------------------------------------------- plan cache ---
 
@@ -610,12 +611,6 @@ StepConsts make_consts(const msamp_adamw_hparams* hp, int64_t step, bool coupled
   return k;
 }
 
-#define MSAMP_LAUNCH(kind, stream, call)                                   \
-  do {                                                                     \
-    hipError_t e__ = timed((kind), (stream), [&]() { return (call); });   \
-    if (e__ != hipSuccess) return fail_hip(e__, msamp_kernel_name(kind));  \
-  } while (0)
-
 bool wide_launch(const Plan* p) { return p->wide; }
 bool wide_update(const Plan* p) { return p->wide || p->wide_update; }
 bool wide_copy(const Plan* p) { return p->wide || p->wide_copy; }
@@ -850,19 +845,6 @@ msamp_status step_delayed_impl(int32_t n, const int64_t* numel, const uint8_t* c
                                    exp_avg_meta, p->scratch_a, k, s));
   MSAMP_LAUNCH(MSAMP_KERNEL_FINALIZE, s, launch_delayed_finalize(n, p->scratch_a, exp_avg_meta, s));
   return MSAMP_OK;
-}
-
-template <typename F>
-msamp_status guarded(F&& f) {
-  try {
-    return f();
-  } catch (const std::bad_alloc&) {
-    return fail(MSAMP_E_NO_MEMORY, "host allocation failed");
-  } catch (const std::exception& ex) {
-    return fail(MSAMP_E_INVALID_ARG, std::string("internal error: ") + ex.what());
-  } catch (...) {
-    return fail(MSAMP_E_INVALID_ARG, "internal error");
-  }
 }
 
 // Split-phase step for a flat intra-tensor partition (each rank holds a
@@ -1100,6 +1082,17 @@ const char* msamp_kernel_name(msamp_kernel_kind kind) {
     case MSAMP_KERNEL_READ_PROBE: return "read_probe";
     case MSAMP_KERNEL_COPY_PROBE: return "copy_probe";
     case MSAMP_KERNEL_QP1_PROBE: return "qp1_probe";
+    case MSAMP_KERNEL_CHECKPOINT_SAVE: return "checkpoint_save";
+    case MSAMP_KERNEL_CHECKPOINT_LOAD: return "checkpoint_load";
+    case MSAMP_KERNEL_NORM_FORWARD: return "norm_forward";
+    case MSAMP_KERNEL_NORM_BACKWARD: return "norm_backward";
+    case MSAMP_KERNEL_NORM_REDUCE: return "norm_reduce";
+    case MSAMP_KERNEL_FFN_FORWARD: return "ffn_forward";
+    case MSAMP_KERNEL_FFN_RECOMPUTE: return "ffn_recompute";
+    case MSAMP_KERNEL_FFN_DX: return "ffn_dx";
+    case MSAMP_KERNEL_FFN_DW: return "ffn_dw";
+    case MSAMP_KERNEL_FFN_LAYOUT: return "ffn_layout";
+    case MSAMP_KERNEL_FFN_REDUCE: return "ffn_reduce";
     default: return "";
   }
 }

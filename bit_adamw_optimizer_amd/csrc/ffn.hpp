@@ -1,0 +1,19 @@
+// ffn.hpp -- internal interface of the gated feed-forward block's kernels
+// (ffn.hip): what one call needs, planned once from its arguments.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "host.hpp"
+#include "msamp.h"
+
+namespace msamp {
+
+// Bytes of workspace of a call, and the call itself (arguments checked).
+int64_t ffn_forward_workspace(const msamp_gated_ffn& a);
+int64_t ffn_backward_workspace(const msamp_gated_ffn& a);
+msamp_status ffn_forward(const msamp_gated_ffn& a, void* ws, hipStream_t s);
+msamp_status ffn_backward(const msamp_gated_ffn& a, void* ws, hipStream_t s);
+
+}  // namespace msamp

@@ -1,0 +1,418 @@
+// norm.hip -- 8-bit activation checkpoints (save, load) and layer norm / RMS
+// norm (forward, backward) on gfx950. The definitions are in msamp.h.
+//
+// All of these are bound by memory: one pass over the data, the row of a norm
+// held in registers between its statistics and its output.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "checkpoint.hpp"
+
+namespace msamp {
+namespace {
+
+// ----------------------------------------------------------- checkpoints ---
+
+constexpr int kCkBlock = 256;
+
+// Work units of 8 elements, whole groups per row (units behind the row's last
+// element take part in their group's exchange and store nothing). At most
+// 2^30 a launch, so that their row is a 32-bit division.
+struct Units {
+  uint32_t total;
+  uint32_t per_row;
+};
+
+template <typename T>
+__global__ __launch_bounds__(kCkBlock) void k_checkpoint_save(Units u, int64_t cols, const T* x, int64_t ldx,
+                                                              CkptRef ck) {
+  const uint32_t i = blockIdx.x * kCkBlock + threadIdx.x;
+  // a group's four lanes are inside or outside together (total is a multiple of 4)
+  if (i >= u.total) return;
+  const uint32_t r = i / u.per_row;
+  const int64_t row = r;
+  const int64_t col = (int64_t)(i - r * u.per_row) * 8;
+  const int n = (int)(cols - col < 8 ? cols - col : 8);
+  float f[8];
+  load8(x + row * ldx + col, n, f);
+  save_group8(ck.fmt, ck.codes + row * ck.ld, ck.scales + row * ck.ld_scales, col, n, f);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kCkBlock) void k_checkpoint_load(Units u, int64_t cols, CkptRef ck, T* out,
+                                                              int64_t ldout) {
+  const uint32_t i = blockIdx.x * kCkBlock + threadIdx.x;
+  if (i >= u.total) return;
+  const uint32_t r = i / u.per_row;
+  const int64_t row = r;
+  const int64_t col = (int64_t)(i - r * u.per_row) * 8;
+  const int n = (int)(cols - col < 8 ? cols - col : 8);
+  if (n <= 0) return;
+  float f[8];
+  load_ckpt8(ck.fmt, ck.codes + row * ck.ld, ck.scales + row * ck.ld_scales, col, n, f);
+  if constexpr (sizeof(T) == 2) {
+    if (__is_same(T, f16)) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = clamp_finite(f[k], kF16Max);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = clamp_finite(f[k], 3.3895313892515355e38f);  // bfloat16's largest
+    }
+  }
+  store8(out + row * ldout + col, n, f);
+}
+
+// ----------------------------------------------------------------- norms ---
+
+template <int WAVES>
+__device__ __forceinline__ void row_sum2(float& a, float& b) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    a += __shfl_xor(a, off, 64);
+    b += __shfl_xor(b, off, 64);
+  }
+  if constexpr (WAVES > 1) {
+    __shared__ float part[2][WAVES];
+    __syncthreads();  // the partials of the last sum have been read
+    if ((threadIdx.x & 63) == 0) {
+      part[0][threadIdx.x >> 6] = a;
+      part[1][threadIdx.x >> 6] = b;
+    }
+    __syncthreads();
+    a = part[0][0];
+    b = part[1][0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+      a += part[0][w];
+      b += part[1][w];
+    }
+  }
+}
+
+// Threads of a workgroup: a row per wave (four rows), or a row per workgroup.
+template <int WAVES>
+constexpr int norm_block() {
+  return WAVES == 1 ? 256 : WAVES * 64;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_weight8(const void* w, bool f32, int64_t col, int n, float fill, float* f) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = fill;
+  } else if (sizeof(T) == 2 && !f32) {
+    load8((const T*)w + col, n, f);
+  } else {
+    load8((const float*)w + col, n, f);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void load_x8(const NormArgs& a, int64_t row, int64_t col, int n, float* f) {
+  if (a.x != nullptr)
+    load8((const T*)a.x + row * a.ldx + col, n, f);
+  else
+    load_ckpt8(a.ck.fmt, a.ck.codes + row * a.ck.ld, a.ck.scales + row * a.ck.ld_scales, col, n, f);
+}
+
+// One row per WAVES waves; a lane holds NCH pieces of 8 columns.
+template <typename T, int WAVES, int NCH>
+__global__ __launch_bounds__(norm_block<WAVES>()) void k_norm_forward(NormArgs a) {
+  constexpr int kLanes = WAVES * 64;
+  const int lane = WAVES == 1 ? (threadIdx.x & 63) : threadIdx.x;
+  const int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+  if (row >= a.rows) return;  // whole waves; with WAVES > 1 no row is beyond
+  float v[NCH][8];
+  int n[NCH];
+  float sum = 0.0f, sq = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int64_t col = ((int64_t)c * kLanes + lane) * 8;
+    n[c] = (int)(a.cols - col < 8 ? a.cols - col : 8);
+    if (n[c] < 0) n[c] = 0;
+    load_x8<T>(a, row, col, n[c], v[c]);
+  }
+  if (a.save.codes != nullptr) {
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      save_group8(a.save.fmt, a.save.codes + row * a.save.ld, a.save.scales + row * a.save.ld_scales,
+                  ((int64_t)c * kLanes + lane) * 8, n[c], v[c]);
+  }
+  const float inv = 1.0f / (float)a.cols;
+  float mu = 0.0f;
+  if (a.mean != nullptr) {
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum += v[c][k];
+    row_sum2<WAVES>(sum, sq);
+    mu = sum * inv;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[c][k] = k < n[c] ? v[c][k] - mu : 0.0f;
+    sum = 0.0f;
+  }
+#pragma unroll
+  for (int c = 0; c < NCH; ++c)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sq = __builtin_fmaf(v[c][k], v[c][k], sq);
+  row_sum2<WAVES>(sq, sum);
+  const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(sq, inv, a.eps));
+  if (lane == 0) {
+    if (a.mean != nullptr) a.mean[row] = mu;
+    a.rstd[row] = rstd;
+  }
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int64_t col = ((int64_t)c * kLanes + lane) * 8;
+    if (n[c] > 0) {
+      float w[8], b[8], y[8];
+      load_weight8<T>(a.weight, a.weight_f32, col, n[c], 1.0f, w);
+      load_weight8<T>(a.bias, a.weight_f32, col, n[c], 0.0f, b);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = __builtin_fmaf(v[c][k] * rstd, w[k], b[k]);
+      store8((T*)a.y + row * a.ldy + col, n[c], y);
+    }
+  }
+}
+
+template <typename T, int WAVES, int NCH>
+__global__ __launch_bounds__(norm_block<WAVES>()) void k_norm_backward(NormArgs a) {
+  constexpr int kLanes = WAVES * 64;
+  constexpr int kRows = WAVES == 1 ? 4 : 1;
+  const int lane = WAVES == 1 ? (threadIdx.x & 63) : threadIdx.x;
+  const int64_t first = (int64_t)blockIdx.x * kRows + (WAVES == 1 ? (threadIdx.x >> 6) : 0);
+  const int64_t stride = (int64_t)gridDim.x * kRows;
+  const float inv = 1.0f / (float)a.cols;
+  float w[NCH][8], sw[NCH][8], sb[NCH][8];
+  int n[NCH];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int64_t col = ((int64_t)c * kLanes + lane) * 8;
+    n[c] = (int)(a.cols - col < 8 ? a.cols - col : 8);
+    if (n[c] < 0) n[c] = 0;
+    load_weight8<T>(a.weight, a.weight_f32, col, n[c], 1.0f, w[c]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sw[c][k] = sb[c][k] = 0.0f;
+  }
+  for (int64_t row = first; row < a.rows; row += stride) {
+    float xh[NCH][8], g[NCH][8];
+    const float mu = a.mean != nullptr ? a.mean[row] : 0.0f;
+    const float rstd = a.rstd[row];
+    float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int64_t col = ((int64_t)c * kLanes + lane) * 8;
+      load_x8<T>(a, row, col, n[c], xh[c]);
+      load8((const T*)a.dy + row * a.lddy + col, n[c], g[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        // behind the row's end g is 0, which keeps every sum clean as long
+        // as xh stays finite there
+        xh[c][k] = k < n[c] ? (xh[c][k] - mu) * rstd : 0.0f;
+        sw[c][k] = __builtin_fmaf(g[c][k], xh[c][k], sw[c][k]);
+        sb[c][k] += g[c][k];
+        g[c][k] *= w[c][k];
+        c1 += g[c][k];
+        c2 = __builtin_fmaf(g[c][k], xh[c][k], c2);
+      }
+    row_sum2<WAVES>(c1, c2);
+    c1 = a.mean != nullptr ? c1 * inv : 0.0f;
+    c2 *= inv;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int64_t col = ((int64_t)c * kLanes + lane) * 8;
+      if (n[c] > 0) {
+        float o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = (g[c][k] - c1 - xh[c][k] * c2) * rstd;
+        store8((T*)a.dx + row * a.lddx + col, n[c], o);
+      }
+    }
+  }
+  if (a.partial == nullptr) return;
+  if constexpr (WAVES == 1) {  // the four waves' sums of the same columns, in a fixed order
+    __shared__ float acc[2][NCH * 512];
+    for (int turn = 0; turn < 4; ++turn) {
+      if ((int)(threadIdx.x >> 6) == turn) {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int i = (c * 64 + lane) * 8 + k;
+            if (turn != 0) {
+              sw[c][k] += acc[0][i];
+              sb[c][k] += acc[1][i];
+            }
+            acc[0][i] = sw[c][k];
+            acc[1][i] = sb[c][k];
+          }
+      }
+      __syncthreads();
+    }
+    if ((threadIdx.x >> 6) != 3) return;
+  }
+  float* pw = a.partial + (int64_t)blockIdx.x * a.cols;
+  float* pb = pw + a.nparts * a.cols;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int64_t col = ((int64_t)c * kLanes + lane) * 8;
+    if (n[c] > 0) {
+      if (a.dweight != nullptr) store8(pw + col, n[c], sw[c]);
+      if (a.dbias != nullptr) store8(pb + col, n[c], sb[c]);
+    }
+  }
+}
+
+// 32 columns per workgroup, 32 threads a column, each over every 32nd part.
+__global__ __launch_bounds__(1024) void k_norm_reduce(NormArgs a) {
+  float* out = blockIdx.y == 0 ? a.dweight : a.dbias;
+  if (out == nullptr) return;
+  const float* p = a.partial + (int64_t)blockIdx.y * a.nparts * a.cols;
+  const int64_t col = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+  const int part = threadIdx.x >> 5;
+  __shared__ float acc[32][33];
+  float s = 0.0f;
+  if (col < a.cols)
+    for (int64_t i = part; i < a.nparts; i += 32) s += p[i * a.cols + col];
+  acc[part][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (part == 0 && col < a.cols) {
+    s = 0.0f;
+    for (int k = 0; k < 32; ++k) s += acc[k][threadIdx.x];
+    out[col] = a.accumulate ? out[col] + s : s;
+  }
+}
+
+template <typename T, int WAVES, int NCH>
+void norm_fwd(const NormArgs& a, hipStream_t s) {
+  const int64_t blocks = WAVES == 1 ? (a.rows + 3) / 4 : a.rows;
+  k_norm_forward<T, WAVES, NCH><<<dim3((unsigned)blocks), dim3(norm_block<WAVES>()), 0, s>>>(a);
+}
+template <typename T, int WAVES, int NCH>
+void norm_bwd(const NormArgs& a, hipStream_t s) {
+  k_norm_backward<T, WAVES, NCH><<<dim3((unsigned)a.nparts), dim3(norm_block<WAVES>()), 0, s>>>(a);
+}
+
+template <typename T>
+void norm_fwd_any(const NormArgs& a, hipStream_t s) {
+  if (a.cols <= 512) norm_fwd<T, 1, 1>(a, s);
+  else if (a.cols <= 1024) norm_fwd<T, 1, 2>(a, s);
+  else if (a.cols <= 2048) norm_fwd<T, 1, 4>(a, s);
+  else if (a.cols <= 4096) norm_fwd<T, 4, 2>(a, s);
+  else if (a.cols <= 8192) norm_fwd<T, 4, 4>(a, s);
+  else if (a.cols <= 16384) norm_fwd<T, 16, 2>(a, s);
+  else norm_fwd<T, 16, 4>(a, s);
+}
+template <typename T>
+void norm_bwd_any(const NormArgs& a, hipStream_t s) {
+  if (a.cols <= 512) norm_bwd<T, 1, 1>(a, s);
+  else if (a.cols <= 1024) norm_bwd<T, 1, 2>(a, s);
+  else if (a.cols <= 2048) norm_bwd<T, 4, 1>(a, s);
+  else if (a.cols <= 4096) norm_bwd<T, 4, 2>(a, s);
+  else if (a.cols <= 8192) norm_bwd<T, 8, 2>(a, s);
+  else if (a.cols <= 16384) norm_bwd<T, 16, 2>(a, s);
+  else norm_bwd<T, 16, 4>(a, s);
+}
+
+constexpr int64_t kSlabUnits = (int64_t)1 << 30;
+
+Units units_of(int64_t rows, int64_t cols) {
+  const int64_t per_row = (cols + kGroup - 1) / kGroup * (kGroup / 8);
+  return {(uint32_t)(rows * per_row), (uint32_t)per_row};
+}
+int64_t slab_rows(int64_t cols) {
+  const int64_t per_row = (cols + kGroup - 1) / kGroup * (kGroup / 8);
+  return per_row >= kSlabUnits ? 1 : kSlabUnits / per_row;
+}
+
+template <typename T>
+hipError_t checkpoint_save(int64_t rows, int64_t cols, const T* x, int64_t ldx, CkptRef ck, hipStream_t s) {
+  const int64_t slab = slab_rows(cols);
+  for (; rows > 0; rows -= slab) {
+    const Units u = units_of(rows < slab ? rows : slab, cols);
+    k_checkpoint_save<T><<<dim3((u.total + kCkBlock - 1) / kCkBlock), dim3(kCkBlock), 0, s>>>(u, cols, x, ldx, ck);
+    x += slab * ldx;
+    ck.codes += slab * ck.ld;
+    ck.scales += slab * ck.ld_scales;
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t checkpoint_load(int64_t rows, int64_t cols, CkptRef ck, T* out, int64_t ldout, hipStream_t s) {
+  const int64_t slab = slab_rows(cols);
+  for (; rows > 0; rows -= slab) {
+    const Units u = units_of(rows < slab ? rows : slab, cols);
+    k_checkpoint_load<T><<<dim3((u.total + kCkBlock - 1) / kCkBlock), dim3(kCkBlock), 0, s>>>(u, cols, ck, out,
+                                                                                             ldout);
+    out += slab * ldout;
+    ck.codes += slab * ck.ld;
+    ck.scales += slab * ck.ld_scales;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_checkpoint_save(int dtype, int64_t rows, int64_t cols, const void* x, int64_t ldx,
+                                  const CkptRef& ck, hipStream_t s) {
+  if (dtype == MSAMP_F32) return checkpoint_save(rows, cols, (const float*)x, ldx, ck, s);
+  if (dtype == MSAMP_F16) return checkpoint_save(rows, cols, (const f16*)x, ldx, ck, s);
+  return checkpoint_save(rows, cols, (const bf16*)x, ldx, ck, s);
+}
+
+hipError_t launch_checkpoint_load(int dtype, int64_t rows, int64_t cols, const CkptRef& ck, void* out, int64_t ldout,
+                                  hipStream_t s) {
+  if (dtype == MSAMP_F32) return checkpoint_load(rows, cols, ck, (float*)out, ldout, s);
+  if (dtype == MSAMP_F16) return checkpoint_load(rows, cols, ck, (f16*)out, ldout, s);
+  return checkpoint_load(rows, cols, ck, (bf16*)out, ldout, s);
+}
+
+hipError_t launch_norm_forward(int dtype, const NormArgs& all, hipStream_t s) {
+  // at most 2^22 rows a launch: its threads stay below 2^32
+  constexpr int64_t kSlab = (int64_t)1 << 22;
+  const int64_t es = dtype == MSAMP_F32 ? 4 : 2;
+  NormArgs a = all;
+  for (int64_t done = 0; done < all.rows; done += kSlab) {
+    a.rows = all.rows - done < kSlab ? all.rows - done : kSlab;
+    if (dtype == MSAMP_F32) norm_fwd_any<float>(a, s);
+    else if (dtype == MSAMP_F16) norm_fwd_any<f16>(a, s);
+    else norm_fwd_any<bf16>(a, s);
+    if (a.x != nullptr) a.x = (const char*)a.x + kSlab * a.ldx * es;
+    a.ck.codes += kSlab * a.ck.ld;
+    a.ck.scales += kSlab * a.ck.ld_scales;
+    if (a.save.codes != nullptr) {
+      a.save.codes += kSlab * a.save.ld;
+      a.save.scales += kSlab * a.save.ld_scales;
+    }
+    a.y = (char*)a.y + kSlab * a.ldy * es;
+    if (a.mean != nullptr) a.mean += kSlab;
+    a.rstd += kSlab;
+  }
+  return hipGetLastError();
+}
+
+int64_t norm_backward_parts(int64_t rows, int64_t cols) {
+  const int64_t rpb = cols <= 1024 ? 4 : 1;
+  const int64_t blocks = (rows + rpb - 1) / rpb;
+  return blocks < 512 ? blocks : 512;
+}
+
+hipError_t launch_norm_backward(int dtype, const NormArgs& a, hipStream_t s) {
+  if (dtype == MSAMP_F32) norm_bwd_any<float>(a, s);
+  else if (dtype == MSAMP_F16) norm_bwd_any<f16>(a, s);
+  else norm_bwd_any<bf16>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_reduce(const NormArgs& a, hipStream_t s) {
+  k_norm_reduce<<<dim3((unsigned)((a.cols + 31) / 32), 2), dim3(1024), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace msamp

@@ -485,6 +485,175 @@ msamp_status msamp_adamw_o3_step_phase3(int32_t n, const int64_t* numel, const u
                                         uint8_t* const* weight_fp8, msamp_meta* weight_fp8_meta,
                                         const float* amax_w, void* stream);
 
+/* ----------------------------------------------------------------------
+ * Training operators around the step: 8-bit activation checkpoints, and the
+ * operators whose backward passes read them. They produce the binary32
+ * gradients that msamp_amax and the quantizing steps take.
+ *
+ * Matrices are row-major with the elements of a row consecutive; 'ld' is the
+ * distance between rows in elements. A matrix that is read may have any
+ * ld >= 0 (0 repeats one row); one that is written needs ld >= its columns
+ * when it has more than one row. Bases need the alignment of their elements
+ * only; 16-byte aligned rows are read and written fastest. Sizes of zero are
+ * allowed: NULL is then accepted for the empty matrices. Unlike the list
+ * entry points these build no tables: they allocate nothing, take no lock,
+ * and can be captured into a graph on the first call. Where a workspace is
+ * taken, it is device memory, 16-byte aligned, of at least the size that the
+ * _workspace function gives for the same arguments; its contents are
+ * unspecified before and after. Calls that may run at the same time need
+ * workspaces of their own. Results do not depend on other work on the
+ * device: no sum is formed with atomics, so equal calls give equal bits.
+ * ---------------------------------------------------------------------- */
+
+typedef enum { MSAMP_F32 = 0, MSAMP_F16 = 1, MSAMP_BF16 = 2 } msamp_dtype;
+
+/*
+ * An activation [rows, cols] in 8 bits. Every group of 32 consecutive
+ * elements of a row (the last group of a row may be shorter) has one
+ * power-of-two scale:
+ *   amax   largest |x| of the group
+ *   e      the smallest integer with amax <= fp8_max * 2^e, and at least
+ *          -126; 0 when amax is 0, Inf or NaN
+ *   code   sat_rne_fp8(x * 2^-e), the library's saturating cast (+-Inf give
+ *          +-max, NaN gives 0x7F with the sign of x)
+ *   scale  the byte e + 127
+ * A code stands for decode(code) * 2^e. No finite group saturates. The scale
+ * is a power of two so that the value is exact in binary32 and bfloat16 (a
+ * code has at most 4 significant bits), whichever operator reads it.
+ *   codes      device, codes[row * ld + col]
+ *   scales     device, scales[row * ld_scales + col / 32]
+ * The struct itself is host memory, read during the call only.
+ */
+#define MSAMP_CHECKPOINT_GROUP 32
+typedef struct {
+  uint8_t* codes;
+  int64_t ld;
+  uint8_t* scales;
+  int64_t ld_scales;
+  msamp_fp8_format fmt;
+} msamp_checkpoint;
+
+/*
+ * msamp_checkpoint_save -- x [rows, cols] into its 8-bit checkpoint, in one
+ * pass. Nothing but the rows' cols codes and ceil(cols / 32) scales is
+ * written.
+ */
+msamp_status msamp_checkpoint_save(int64_t rows, int64_t cols, const void* x, int64_t ldx, msamp_dtype dtype,
+                                   const msamp_checkpoint* ckpt, void* stream);
+
+/*
+ * msamp_checkpoint_load -- out [rows, cols] <- the values of a checkpoint,
+ * rounded to dtype (nearest even). A finite value beyond the type's range
+ * (the top binade rounds up to 2^16 for MSAMP_F16, 2^128 otherwise) becomes
+ * the type's largest finite value, as the saturating casts do.
+ */
+msamp_status msamp_checkpoint_load(int64_t rows, int64_t cols, const msamp_checkpoint* ckpt, void* out,
+                                   int64_t ldout, msamp_dtype dtype, void* stream);
+
+/*
+ * msamp_layernorm_forward -- layer norm of every row of x [rows, cols], or
+ * RMS norm when mean is NULL:
+ *   mu = sum(x) / cols                        (0 for RMS norm)
+ *   rstd = 1 / sqrt(sum((x - mu)^2) / cols + eps)
+ *   y = (x - mu) * rstd * weight + bias
+ * in binary32, the row held in registers (the variance is taken around the
+ * mean), y rounded once to dtype.
+ *   x          device, dtype; or NULL, with x_ckpt the checkpoint that is
+ *              read in its place (values in binary32, clamped to its range)
+ *   weight     device [cols] of weight_dtype, or NULL for 1
+ *   bias       device [cols] of weight_dtype, or NULL for 0
+ *   y          device, dtype, out
+ *   mean       device float[rows], out; NULL: RMS norm
+ *   rstd       device float[rows], out
+ *   eps        >= 0, finite
+ *   save       NULL, or a checkpoint that receives x in the same pass
+ *              (x must then not be a checkpoint itself)
+ * weight_dtype is dtype or MSAMP_F32. cols <= MSAMP_NORM_MAX_COLS.
+ */
+#define MSAMP_NORM_MAX_COLS 32768
+msamp_status msamp_layernorm_forward(int64_t rows, int64_t cols, const void* x, int64_t ldx,
+                                     const msamp_checkpoint* x_ckpt, msamp_dtype dtype, const void* weight,
+                                     const void* bias, msamp_dtype weight_dtype, void* y, int64_t ldy, float* mean,
+                                     float* rstd, double eps, const msamp_checkpoint* save, void* stream);
+
+/*
+ * msamp_layernorm_backward -- with xh = (x - mean) * rstd of the forward
+ * pass's statistics (mean NULL: RMS norm, xh = x * rstd):
+ *   dx = rstd * (w*dy - [sum(w*dy)/cols, layer norm only] - xh * sum(w*dy*xh)/cols)
+ *   dweight = sum over rows of dy * xh        dbias = sum over rows of dy
+ * dweight and dbias are binary32 (what msamp_amax takes); with accumulate
+ * they are added to what is there. Either may be NULL.
+ *   dy, dx     device, dtype
+ *   x, x_ckpt  as in the forward pass; the checkpoint saved there serves
+ *   weight     as in the forward pass, or NULL for 1
+ *   workspace  msamp_layernorm_backward_workspace bytes (0: may be NULL)
+ */
+int64_t msamp_layernorm_backward_workspace(int64_t rows, int64_t cols);
+msamp_status msamp_layernorm_backward(int64_t rows, int64_t cols, const void* dy, int64_t lddy, const void* x,
+                                      int64_t ldx, const msamp_checkpoint* x_ckpt, msamp_dtype dtype,
+                                      const void* weight, msamp_dtype weight_dtype, const float* mean,
+                                      const float* rstd, void* dx, int64_t lddx, float* dweight, float* dbias,
+                                      int accumulate, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Activation of the gate: silu(g) = g / (1 + e^-g); gelu(g) = g * Phi(g);
+ * gelu_tanh, its tanh form g/2 * (1 + tanh(sqrt(2/pi) * (g + 0.044715 g^3))). */
+typedef enum { MSAMP_ACT_SILU = 0, MSAMP_ACT_GELU = 1, MSAMP_ACT_GELU_TANH = 2 } msamp_activation;
+
+/*
+ * Arguments of the gated feed-forward block (host struct, read during the
+ * call). x [tokens, hidden]; w_gate, w_up [ffn, hidden], as the gate and up
+ * projections are stored; h, dh [tokens, ffn]; all of dtype, MSAMP_F16 or
+ * MSAMP_BF16. Every size is at most 2^31 - 1.
+ *   forward:   g = x w_gate^T, u = x w_up^T, h = act(g) * u
+ *   backward:  from dh: du = dh * act(g), dg = dh * u * act'(g),
+ *              dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x
+ * The forward pass keeps nothing: the backward pass forms g and u again from
+ * x, or from its checkpoint (exactly one of x and x_ckpt is set; the forward
+ * pass takes x only). The products are summed in binary32; g and u stay in
+ * binary32; dg and du are rounded to dtype, as operands of the matrix
+ * instructions; a checkpoint's values are rounded to dtype. h and dx are
+ * rounded once.
+ *   h          forward: out. Backward: out, the same product again (the down
+ *              projection's gradient needs it), or NULL
+ *   dx         backward: out
+ *   dw_gate, dw_up   backward: out [ffn, hidden] of dw_dtype: dtype, or
+ *              MSAMP_F32, which may be accumulated into (dw_accumulate != 0)
+ * The backward fields are not read by the forward pass.
+ */
+typedef struct {
+  int64_t tokens, hidden, ffn;
+  msamp_dtype dtype;
+  msamp_activation act;
+  const void* x;
+  int64_t ldx;
+  const msamp_checkpoint* x_ckpt;
+  const void* w_gate;
+  int64_t ld_gate;
+  const void* w_up;
+  int64_t ld_up;
+  void* h;
+  int64_t ldh;
+  const void* dh;
+  int64_t lddh;
+  void* dx;
+  int64_t lddx;
+  void* dw_gate;
+  int64_t ld_dw_gate;
+  void* dw_up;
+  int64_t ld_dw_up;
+  msamp_dtype dw_dtype;
+  int dw_accumulate;
+} msamp_gated_ffn;
+
+/* Bytes of workspace of a call with these arguments; -1 with an error set
+ * when the arguments are not valid. */
+int64_t msamp_gated_ffn_forward_workspace(const msamp_gated_ffn* args);
+int64_t msamp_gated_ffn_backward_workspace(const msamp_gated_ffn* args);
+msamp_status msamp_gated_ffn_forward(const msamp_gated_ffn* args, void* workspace, int64_t workspace_bytes,
+                                     void* stream);
+msamp_status msamp_gated_ffn_backward(const msamp_gated_ffn* args, void* workspace, int64_t workspace_bytes,
+                                      void* stream);
+
 /* Frees every cached device table of the library (all devices) that is not
  * pinned by a graph capture, after waiting for the devices to finish. Safe to
  * call at any time from one thread while no other library call runs. */
@@ -587,7 +756,18 @@ typedef enum {
   MSAMP_KERNEL_READ_PROBE = 12, /* msamp_stream_probe, MSAMP_STREAM_READ */
   MSAMP_KERNEL_COPY_PROBE = 13, /* msamp_stream_probe, MSAMP_STREAM_COPY */
   MSAMP_KERNEL_QP1_PROBE = 14,  /* msamp_quantize_pass1_probe (measurement aid) */
-  MSAMP_KERNEL_COUNT = 15
+  MSAMP_KERNEL_CHECKPOINT_SAVE = 15, /* msamp_checkpoint_save */
+  MSAMP_KERNEL_CHECKPOINT_LOAD = 16, /* msamp_checkpoint_load */
+  MSAMP_KERNEL_NORM_FORWARD = 17,  /* msamp_layernorm_forward */
+  MSAMP_KERNEL_NORM_BACKWARD = 18, /* msamp_layernorm_backward, over the rows */
+  MSAMP_KERNEL_NORM_REDUCE = 19,   /* its weight and bias gradients */
+  MSAMP_KERNEL_FFN_FORWARD = 20,   /* gate and up projections, activation, product */
+  MSAMP_KERNEL_FFN_RECOMPUTE = 21, /* the same in the backward pass, giving dg and du */
+  MSAMP_KERNEL_FFN_DX = 22,        /* dx = dg w_gate + du w_up */
+  MSAMP_KERNEL_FFN_DW = 23,        /* dw_gate, dw_up */
+  MSAMP_KERNEL_FFN_LAYOUT = 24,    /* operands laid out for the matrix kernels */
+  MSAMP_KERNEL_FFN_REDUCE = 25,    /* partial sums of a split product */
+  MSAMP_KERNEL_COUNT = 26
 } msamp_kernel_kind;
 
 /* on != 0 starts recording (and discards earlier records; the events for

@@ -1,0 +1,168 @@
+"""8-bit activation checkpoints on the GPU against the binary64 reference
+(tests/train_ref.py): codes, scales and loaded values bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import bit_adamw_optimizer_amd as M
+from tests import train_ref as R
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def matrix(rows, cols, dtype, pad=0, seed=0, wide=True):
+    """Values over many binades, some groups of zeros; rows `pad` elements apart."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g)
+    if wide:
+        x *= torch.exp2(torch.randint(-12, 6, (rows, 1), generator=g).float())
+        x *= torch.exp2(torch.randint(-9, 3, (rows, cols), generator=g).float())
+    if cols >= 64 and rows > 1:
+        x[1, 32:64] = 0.0
+    buf = torch.full((rows, cols + pad), float("nan"), dtype=dtype, device="cuda")
+    buf[:, :cols] = x.to(dtype)
+    return buf[:, :cols]
+
+
+def guarded(rows, cols, pad=5):
+    """A checkpoint inside larger buffers of 0xA5, and those buffers."""
+    groups = -(-cols // 32)
+    codes = torch.full((rows + 1, cols + pad), 0xA5, dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows + 1, groups + 3), 0xA5, dtype=torch.uint8, device="cuda")
+    return codes, scales
+
+
+def same(got: torch.Tensor, ref: np.ndarray) -> bool:
+    """Equal values, NaN where NaN, the same signs of zero."""
+    g = got.cpu().double().numpy()
+    return np.array_equal(g, ref, equal_nan=True) and np.array_equal(np.signbit(g[g == 0]), np.signbit(ref[ref == 0]))
+
+
+def rounded(v: np.ndarray, dtype) -> np.ndarray:
+    """Round to nearest even with the finite range clamped (torch's CPU cast of binary64)."""
+    lim = torch.finfo(dtype).max
+    c = torch.from_numpy(np.where(np.isnan(v), v, np.clip(v, -lim, lim)))
+    return (c.to(dtype) if dtype != torch.bfloat16 else c.float().to(dtype)).double().numpy()
+
+
+@pytest.mark.parametrize("fmt", [M.E4M3, M.E5M2])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (1, 31, 0), (3, 32, 0), (2, 33, 1), (5, 257, 3), (7, 768, 0),
+                                           (4, 1000, 8), (300, 65, 0), (2, 4099, 1)])
+def test_save_and_load(rows, cols, pad, dtype, fmt):
+    x = matrix(rows, cols, DT[dtype], pad, seed=rows * 7919 + cols)
+    codes, scales = guarded(rows, cols)
+    before = codes.clone(), scales.clone()
+    ck = M.Checkpoint(codes[:rows, :cols], scales[:rows, :-(-cols // 32)], cols, fmt)
+    M.checkpoint_save(x, ck)
+    rc, rs = R.checkpoint_save(x.float().cpu().numpy(), fmt)
+    assert np.array_equal(codes[:rows, :cols].cpu().numpy(), rc)
+    assert np.array_equal(scales[:rows, :rs.shape[1]].cpu().numpy(), rs)
+    # nothing else is written
+    assert torch.equal(codes[:, cols:], before[0][:, cols:]) and torch.equal(codes[rows:], before[0][rows:])
+    assert torch.equal(scales[:, rs.shape[1]:], before[1][:, rs.shape[1]:])
+    assert torch.equal(scales[rows:], before[1][rows:])
+    values = R.checkpoint_values(rc, rs, fmt)
+    for to in DT.values():
+        buf = torch.full((rows + 1, cols + 3), 7.0, dtype=to, device="cuda")
+        M.checkpoint_load(ck, buf[:rows, :cols])
+        assert same(buf[:rows, :cols], rounded(values, to)), to
+        assert (buf[:, cols:] == 7).all() and (buf[rows:] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", [M.E4M3, M.E5M2])
+def test_special_values_stay_in_their_group(fmt):
+    x = torch.randn(6, 96, generator=torch.Generator().manual_seed(5))
+    inf, nan = float("inf"), float("nan")
+    x[0, 3], x[1, 40], x[2, 95], x[3, 0], x[4, 64] = inf, -inf, nan, 1e30, -0.0
+    x[3, 64:96] = 1e4  # above the range of E4M3, in a group without specials
+    x[5, 32:64] = torch.tensor([2.0 ** -149, -2.0 ** -140] * 16)
+    x[5, 0:32] = 3.4028234e38
+    x = x.cuda()
+    ck = M.new_checkpoint(6, 96, fmt)
+    M.checkpoint_save(x, ck)
+    rc, rs = R.checkpoint_save(x.cpu().numpy(), fmt)
+    assert np.array_equal(ck.codes.cpu().numpy(), rc) and np.array_equal(ck.scales.cpu().numpy(), rs)
+    out = torch.empty(6, 96, device="cuda")
+    M.checkpoint_load(ck, out)
+    assert same(out, rounded(R.checkpoint_values(rc, rs, fmt), torch.float32))
+    assert torch.isnan(out[2, 95]) and torch.isfinite(out[0]).all() and torch.isfinite(out[5]).all()
+
+
+def test_top_of_each_range_saturates_on_load():
+    for dtype in DT.values():
+        top = torch.full((1, 32), torch.finfo(dtype).max, dtype=dtype, device="cuda")
+        ck = M.new_checkpoint(1, 32, M.E4M3)
+        M.checkpoint_save(top, ck)
+        out = torch.empty_like(top)
+        M.checkpoint_load(ck, out)
+        assert torch.equal(out, top)  # rounds up to the next power of two, then to the largest finite value
+
+
+@pytest.mark.parametrize("fmt", [M.E4M3, M.E5M2])
+def test_every_fp16_value(fmt):
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.float16).view(2048, 32).cuda()
+    ck = M.new_checkpoint(2048, 32, fmt)
+    M.checkpoint_save(x, ck)
+    rc, rs = R.checkpoint_save(x.float().cpu().numpy(), fmt)
+    assert np.array_equal(ck.codes.cpu().numpy(), rc) and np.array_equal(ck.scales.cpu().numpy(), rs)
+
+
+def test_repeated_and_transposed_inputs():
+    row = torch.randn(1, 70, device="cuda")
+    ck = M.new_checkpoint(9, 70)
+    M.checkpoint_save(row.expand(9, 70), ck)  # rows at distance 0
+    one = M.new_checkpoint(1, 70)
+    M.checkpoint_save(row, one)
+    assert torch.equal(ck.codes[:, :70], one.codes[:, :70].expand(9, 70)) and torch.equal(ck.scales, one.scales.expand(9, 3))
+    with pytest.raises(ValueError):
+        M.checkpoint_save(torch.randn(70, 9, device="cuda").t(), ck)
+    with pytest.raises(ValueError):
+        M.checkpoint_load(ck, torch.empty(1, 70, device="cuda").expand(9, 70))
+    with pytest.raises(ValueError):
+        M.checkpoint_save(torch.randn(9, 69, device="cuda"), ck)
+    with pytest.raises(TypeError):
+        M.checkpoint_save(torch.randn(9, 70, device="cuda").double(), ck)
+
+
+def test_long_matrix_past_32_bit_offsets():
+    """More than 2^32 elements: the last rows, whose offsets pass 32 bits."""
+    rows, cols = (1 << 32) // 8192 + 40, 8192
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, cols, device="cuda").bfloat16()
+    ck = M.new_checkpoint(rows, cols)
+    M.checkpoint_save(x, ck)
+    rc, rs = R.checkpoint_save(x[-3:].float().cpu().numpy(), M.E4M3)
+    assert np.array_equal(ck.codes[-3:].cpu().numpy(), rc) and np.array_equal(ck.scales[-3:].cpu().numpy(), rs)
+    assert (ck.scales[:-3] == 127).all() and not ck.codes[:-3].any()
+    out = torch.empty_like(x)
+    M.checkpoint_load(ck, out)
+    assert same(out[-3:], R.checkpoint_values(rc, rs, M.E4M3)) and not out[:-3].any()
+
+
+def test_on_another_stream_and_in_a_graph():
+    x = torch.randn(33, 515, device="cuda").half()
+    ref = M.new_checkpoint(33, 515)
+    M.checkpoint_save(x, ref)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    ck = M.new_checkpoint(33, 515)
+    out = torch.empty_like(x)
+    with torch.cuda.stream(s):
+        M.checkpoint_save(x, ck)
+    s.synchronize()
+    assert torch.equal(ck.codes[:, :515], ref.codes[:, :515]) and torch.equal(ck.scales, ref.scales)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        M.checkpoint_save(x, ck)
+        M.checkpoint_load(ck, out)
+    for k in range(3):
+        x.copy_(torch.randn(33, 515, device="cuda").half() * 2.0 ** k)
+        g.replay()
+        torch.cuda.synchronize()
+        M.checkpoint_save(x, ref)
+        eager = torch.empty_like(x)
+        M.checkpoint_load(ref, eager)
+        assert torch.equal(out, eager) and torch.equal(ck.scales, ref.scales)

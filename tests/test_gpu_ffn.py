@@ -1,0 +1,282 @@
+"""The gated feed-forward block on the GPU, forward and backward, against the
+binary64 reference (tests/train_ref.py), which also bounds the errors of the
+binary32 sums and of the one intermediate rounding (dg and du to the 16-bit
+type)."""
+import pytest
+import torch
+
+import bit_adamw_optimizer_amd as M
+from tests import train_ref as R
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+# one token, a few, ragged, whole tiles and just beyond them; hidden sizes that are no multiple of anything
+SHAPES = [(1, 64, 96, 0), (1, 1000, 129, 0), (3, 40, 7, 1), (16, 128, 256, 0), (17, 136, 264, 8), (65, 257, 130, 0),
+          (128, 256, 512, 0), (129, 300, 513, 3), (256, 64, 256, 0), (300, 1, 33, 0), (31, 33, 1, 0)]
+
+
+def matrix(rows, cols, dtype, pad, seed, size=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g) * size
+    buf = torch.full((rows, cols + pad), float("nan"), dtype=dtype, device="cuda")
+    buf[:, :cols] = x.to(dtype)
+    return buf[:, :cols]
+
+
+def out(rows, cols, dtype, value=7.0):
+    """A matrix inside a larger buffer, whose rest has to stay."""
+    buf = torch.full((rows + 1, cols + 2), value, dtype=dtype, device="cuda")
+    return buf, buf[:rows, :cols]
+
+
+def untouched(buf, rows, cols, value=7.0):
+    return bool((buf[rows:] == value).all() and (buf[:, cols:] == value).all())
+
+
+def problem(t, k, f, dt, pad=0, seed=0):
+    return (matrix(t, k, dt, pad, seed), matrix(f, k, dt, pad, seed + 1, 1.3 * k ** -0.5),
+            matrix(f, k, dt, pad, seed + 2, 1.3 * k ** -0.5), matrix(t, f, dt, pad, seed + 3, 0.1))
+
+
+def check(names, got, val, err, dt):
+    for name in names:
+        R.assert_near(got[name], val[name], err[name], name)
+        # the roundings are as good as independent: in the 2-norm the last one is at most half a step of each
+        # value, and those of dg, du before it weigh no more than it does each
+        ref = val[name]
+        rel = ((got[name].cpu().double() - ref).norm() / ref.norm().clamp_min(1e-300)).item()
+        assert rel <= 3 * R.half(dt) + (err[name].norm() / ref.norm().clamp_min(1e-300)).item() * 0.25, (name, rel)
+
+
+@pytest.mark.parametrize("act", list(M.ACTIVATIONS))
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("t,k,f,pad", SHAPES)
+def test_forward(t, k, f, pad, dtype, act):
+    dt = DT[dtype]
+    x, wg, wu, _ = problem(t, k, f, dt, pad, seed=t + k)
+    buf, h = out(t, f, dt)
+    M.gated_ffn_forward(x, wg, wu, h, act=act)
+    assert untouched(buf, t, f)
+    val, err = R.ffn(x.cpu(), wg.cpu(), wu.cpu(), act, dtype=dt)
+    check(["h"], {"h": h}, val, err, dt)
+
+
+@pytest.mark.parametrize("act", list(M.ACTIVATIONS))
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("t,k,f,pad", SHAPES)
+def test_backward(t, k, f, pad, dtype, act):
+    dt = DT[dtype]
+    x, wg, wu, dh = problem(t, k, f, dt, pad, seed=t + k)
+    wide = (t + k + f) % 2 == 0  # binary32 or 16-bit weight gradients
+    bufs = {"h": out(t, f, dt), "dx": out(t, k, dt), "dw_gate": out(f, k, torch.float32 if wide else dt),
+            "dw_up": out(f, k, torch.float32 if wide else dt)}
+    got = {n: v[1] for n, v in bufs.items()}
+    M.gated_ffn_backward(dh, x, wg, wu, got["dx"], got["dw_gate"], got["dw_up"], act=act, h=got["h"])
+    for n, (buf, v) in bufs.items():
+        assert untouched(buf, *v.shape), n
+    val, err = R.ffn(x.cpu(), wg.cpu(), wu.cpu(), act, dh.cpu(), dt)
+    check(["h", "dx", "dw_gate", "dw_up"], got, val, err, dt)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("t,k,f", [(40, 96, 160), (130, 100, 257), (5, 1000, 64)])
+def test_backward_from_a_checkpoint(t, k, f, dtype):
+    """From the checkpoint: the same bits as from its values, in both formats."""
+    dt = DT[dtype]
+    x, wg, wu, dh = problem(t, k, f, dt, seed=k)
+    for fmt in (M.E4M3, M.E5M2):
+        ck = M.new_checkpoint(t, k, fmt)
+        M.checkpoint_save(x, ck)
+        xv = torch.empty_like(x)
+        M.checkpoint_load(ck, xv)
+        res = []
+        for src in (ck, xv):
+            h, dx = torch.empty(t, f, dtype=dt, device="cuda"), torch.empty(t, k, dtype=dt, device="cuda")
+            a, b = torch.empty(f, k, device="cuda"), torch.empty(f, k, device="cuda")
+            M.gated_ffn_backward(dh, src, wg, wu, dx, a, b, h=h)
+            res.append((h, dx, a, b))
+        assert all(torch.equal(p, q) for p, q in zip(*res))
+        val, err = R.ffn(xv.cpu(), wg.cpu(), wu.cpu(), "silu", dh.cpu(), dt)
+        check(["h", "dx", "dw_gate", "dw_up"], dict(zip(("h", "dx", "dw_gate", "dw_up"), res[0])), val, err, dt)
+
+
+def test_accumulate_and_repeat():
+    t, k, f = 200, 130, 140
+    x, wg, wu, dh = problem(t, k, f, torch.float16)
+    dx = torch.empty(t, k, dtype=torch.float16, device="cuda")
+    a, b = torch.empty(f, k, device="cuda"), torch.empty(f, k, device="cuda")
+    M.gated_ffn_backward(dh, x, wg, wu, dx, a, b)
+    first = dx.clone()
+    a2, b2 = torch.full_like(a, 0.5), torch.full_like(b, -2.0)
+    M.gated_ffn_backward(dh, x, wg, wu, dx, a2, b2, accumulate=True)
+    assert torch.equal(dx, first) and torch.equal(a2, 0.5 + a) and torch.equal(b2, -2.0 + b)
+
+
+def test_empty_calls():
+    f16 = torch.float16
+    e = lambda r, c: torch.empty(r, c, dtype=f16, device="cuda")  # noqa: E731
+    full = lambda r, c: torch.full((r, c), 7.0, dtype=f16, device="cuda")  # noqa: E731
+    M.gated_ffn_forward(e(0, 8), e(16, 8), e(16, 8), e(0, 16))
+    M.gated_ffn_forward(e(4, 8), e(0, 8), e(0, 8), e(4, 0))
+    h = full(4, 16)
+    M.gated_ffn_forward(e(4, 0), e(16, 0), e(16, 0), h)  # sums of nothing
+    assert not h.any()
+    # no token: weight gradients of zero, or unchanged
+    a, b = full(16, 8), full(16, 8)
+    M.gated_ffn_backward(e(0, 16), e(0, 8), e(16, 8), e(16, 8), e(0, 8), a, b)
+    assert not a.any() and not b.any()
+    a, b = torch.full((16, 8), 7.0, device="cuda"), torch.full((16, 8), 7.0, device="cuda")
+    M.gated_ffn_backward(e(0, 16), e(0, 8), e(16, 8), e(16, 8), e(0, 8), a, b, accumulate=True)
+    assert (a == 7).all() and (b == 7).all()
+    # no inner unit: no gradient of x
+    dx = full(4, 8)
+    M.gated_ffn_backward(e(4, 0), e(4, 8), e(0, 8), e(0, 8), dx, e(0, 8), e(0, 8))
+    assert not dx.any()
+    # no hidden unit
+    h = full(4, 16)
+    M.gated_ffn_backward(full(4, 16), e(4, 0), e(16, 0), e(16, 0), e(4, 0), e(16, 0), e(16, 0), h=h)
+    assert not h.any()
+
+
+def test_one_weight_for_gate_and_up_repeated_rows_and_views():
+    dt = torch.bfloat16
+    both = matrix(2 * 72, 80, dt, 0, 1, 0.1)  # gate and up as views of one tensor
+    x = matrix(1, 80, dt, 0, 2).expand(50, 80)
+    h, ref = torch.empty(50, 72, dtype=dt, device="cuda"), torch.empty(1, 72, dtype=dt, device="cuda")
+    M.gated_ffn_forward(x, both[:72], both[72:], h)
+    M.gated_ffn_forward(x[:1], both[:72].clone(), both[72:].clone(), ref)
+    val, err = R.ffn(x.cpu(), both[:72].cpu(), both[72:].cpu(), "silu", dtype=dt)
+    check(["h"], {"h": h}, val, err, dt)
+    check(["h"], {"h": ref}, {"h": val["h"][:1]}, {"h": err["h"][:1]}, dt)
+    M.gated_ffn_forward(x, both[:72], both[:72], h, act="gelu")  # the same weight twice
+    val, err = R.ffn(x.cpu(), both[:72].cpu(), both[:72].cpu(), "gelu", dtype=dt)
+    check(["h"], {"h": h}, val, err, dt)
+
+
+def test_special_values_stay_in_their_token():
+    """A token of NaN or infinity leaves the other tokens' rows as they are."""
+    x, wg, wu, dh = problem(140, 200, 300, torch.bfloat16)
+    outs = []
+    for bad in (False, True):
+        y = x.clone()
+        if bad:
+            y[3], y[77, 5] = float("nan"), float("inf")
+        h, dx = torch.empty_like(dh), torch.empty_like(x)
+        M.gated_ffn_backward(dh, y, wg, wu, dx, torch.empty_like(wg), torch.empty_like(wu), h=h)
+        outs.append((h, dx))
+    keep = [i for i in range(140) if i not in (3, 77)]
+    for p, q in zip(*outs):
+        assert torch.equal(p[keep], q[keep]) and torch.isnan(q[3]).all()
+
+
+def test_large_gates_keep_their_limits():
+    """Gates far out: act(g) is g or 0 there, its slope 1 or 0, and nothing overflows on the way."""
+    dt = torch.bfloat16
+    x = torch.tensor([[200.0], [-200.0], [30000.0], [-30000.0]], device="cuda").to(dt)
+    one = torch.ones(8, 1, dtype=dt, device="cuda")
+    up = torch.full((8, 1), 2.0 ** -7, dtype=dt, device="cuda")
+    for act in M.ACTIVATIONS:
+        h, dx = torch.empty(4, 8, dtype=dt, device="cuda"), torch.empty(4, 1, dtype=dt, device="cuda")
+        a, b = torch.empty(8, 1, device="cuda"), torch.empty(8, 1, device="cuda")
+        dh = torch.ones(4, 8, dtype=dt, device="cuda")
+        M.gated_ffn_backward(dh, x, one, up, dx, a, b, act=act, h=h)
+        xs = x.double().cpu()
+        val, err = R.ffn(xs, one.cpu(), up.cpu(), act, dh.cpu(), dt)
+        for name, g in (("h", h), ("dx", dx), ("dw_gate", a), ("dw_up", b)):
+            R.assert_near(g, val[name], err[name], act + " " + name)
+
+
+def test_refusals():
+    x, wg, wu, dh = problem(4, 8, 16, torch.float16)
+    h = torch.empty_like(dh)
+    for bad in (dict(act="relu"),):
+        with pytest.raises(ValueError):
+            M.gated_ffn_forward(x, wg, wu, h, **bad)
+    with pytest.raises(ValueError):
+        M.gated_ffn_forward(x[:, :7], wg, wu, h)
+    with pytest.raises(ValueError):
+        M.gated_ffn_forward(x, wg, wu[:15], h)
+    with pytest.raises(TypeError):
+        M.gated_ffn_forward(x, wg, wu.bfloat16(), h)
+    with pytest.raises(TypeError):
+        M.gated_ffn_forward(x.float(), wg.float(), wu.float(), h.float())
+    with pytest.raises(ValueError):
+        M.gated_ffn_forward(x, wg, wu, h[:1].expand(4, 16))
+    with pytest.raises(ValueError):
+        M.gated_ffn_forward(x, torch.empty(8, 16, dtype=torch.float16, device="cuda").t(), wu, h)
+    ck = M.new_checkpoint(4, 8)
+    with pytest.raises(TypeError):
+        M.gated_ffn_forward(ck, wg, wu, h)
+    dx = torch.empty_like(x)
+    with pytest.raises(TypeError):
+        M.gated_ffn_backward(dh, x, wg, wu, dx, wg.clone(), wu.clone(), accumulate=True)
+    with pytest.raises(TypeError):
+        M.gated_ffn_backward(dh, x, wg, wu, dx, wg.clone(), wu.float())
+    with pytest.raises(ValueError):
+        M.gated_ffn_backward(dh, M.new_checkpoint(4, 9), wg, wu, dx, wg.clone(), wu.clone())
+
+
+@pytest.mark.parametrize("t,k,f", [(3, 264, 520), (300, 264, 520)])
+def test_gradients_against_differences(t, k, f):
+    """Along one direction, against central differences of the binary64 product (the kernel's own forward pass
+    is rounded to 16 bits, which differences would magnify)."""
+    dt = torch.float16
+    x, wg, wu, dh = problem(t, k, f, dt)
+    dx = torch.empty_like(x)
+    a, b = torch.empty(f, k, device="cuda"), torch.empty(f, k, device="cuda")
+    M.gated_ffn_backward(dh, x, wg, wu, dx, a, b)
+    v = [torch.randn(p.shape, dtype=torch.float64, generator=torch.Generator().manual_seed(i)) * s
+         for i, (p, s) in enumerate(((x, 1.0), (wg, k ** -0.5), (wu, k ** -0.5)))]
+    p = [q.cpu().double() for q in (x, wg, wu)]
+    step = 1e-5
+
+    def f64(sign):
+        y, g, u = (q + sign * step * d for q, d in zip(p, v))
+        return (R.ffn(y, g, u, "silu")[0]["h"] * dh.cpu().double()).sum().item()
+
+    diff = (f64(1) - f64(-1)) / (2 * step)
+    terms = [(q.cpu().double() * d) for q, d in zip((dx, a, b), v)]
+    along = sum(q.sum().item() for q in terms)
+    val, err = R.ffn(*p, "silu", dh.cpu(), dt)
+    bound = sum(((err[n] + R.half(dt) * val[n].abs() + R.floor_of(dt)) * d.abs()).sum().item()
+                for n, d in zip(("dx", "dw_gate", "dw_up"), v))
+    assert abs(diff - along) <= bound + 1e-6 * abs(diff)
+    # and as independent roundings, of which there are three (dg or du, x's gradient, the sum)
+    rms = sum(((R.half(dt) * val[n]) * d).square().sum().item() for n, d in zip(("dx", "dw_gate", "dw_up"), v)) ** 0.5
+    assert abs(diff - along) <= 6 * 3 * rms + 1e-6 * abs(diff)
+
+
+def test_in_a_graph_and_on_another_stream():
+    dt = torch.float16
+    x, wg, wu, dh = problem(70, 144, 200, dt)
+    ck = M.new_checkpoint(70, 144)
+    h, h2, dx = torch.empty_like(dh), torch.empty_like(dh), torch.empty_like(x)
+    a, b = torch.empty(200, 144, device="cuda"), torch.empty(200, 144, device="cuda")
+
+    def step():
+        M.checkpoint_save(x, ck)
+        M.gated_ffn_forward(x, wg, wu, h)
+        M.gated_ffn_backward(dh, ck, wg, wu, dx, a, b, h=h2)
+
+    outs = (h, h2, dx, a, b)
+    step()
+    want = [t.clone() for t in outs]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(outs, want))
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            step()
+    for n in range(4):
+        x.copy_(torch.randn(70, 144, device="cuda"))
+        graphs[n % 2].replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, outs))
