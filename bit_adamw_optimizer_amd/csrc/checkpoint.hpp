@@ -25,6 +25,7 @@ typedef u32x2 u32x2_any __attribute__((aligned(1)));
 
 constexpr int kGroup = MSAMP_CHECKPOINT_GROUP;
 constexpr float kF32Max = 3.402823466e+38f;
+constexpr float kBf16Max = 3.3895313892515355e+38f;
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(f16 v) { return (float)v; }

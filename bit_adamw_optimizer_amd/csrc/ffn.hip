@@ -14,6 +14,13 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+#define LDS __attribute__((address_space(3)))
+
 template <typename T>
 struct Frag;
 template <>
@@ -53,175 +60,628 @@ __device__ __forceinline__ void act_and_grad(int act, float g, float* a, float* 
 }
 
 // -------------------------------------------------------- matrix product ---
+//
+// out[r, c] = sum_k R(r, k) C(c, k), summed in binary32 by 32x32x16 MFMA.
+//
+// A workgroup of 8 waves (2 along r, 4 along c) forms a tile of 64 * FR rows
+// and 256 columns, 64 k a step. Both operand tiles of the next step travel to
+// LDS by buffer loads that write it directly while the current one is
+// multiplied (two LDS stages). C is the instruction's left operand and R its
+// right one, so that a lane ends with four consecutive columns of one row.
+//
+// An operand is stored with k along its rows (kAlong: x, the weights and
+// [dg | du] as they are read by the products over hidden and inner units) or
+// with k across them (kAcross: the same memory in the products over tokens
+// and, for the weights, inner units). Either goes to LDS as it lies in memory,
+// in pieces of 16 bytes whose order within a row is permuted so that the reads
+// of a fragment spread over all banks:
+//   kAlong   LDS row = 64 k of one r or c, 8 pieces; piece p of row i at p ^ (i & 7)
+//   kAcross  LDS row = all r or c of one k; piece p of row k at p ^ ((k & 3) << 2);
+//            read by the transposing LDS load, four k of 16 columns at a time
+// Nothing is copied or transposed beforehand unless rows are not 16-byte
+// aligned.
+//
+// Reads past an operand's last row or k return zero (buffer bounds, and a
+// comparison in the last step along k), so ragged sizes need no other path.
 
-// C[m, n] = sum_k A[m, k] B[n, k] with any strides; 64 x 64 tiles.
 enum Mode { kForward, kRecompute, kDx, kDw };
 
 struct Product {
-  int64_t M, N, K;
-  const void *a0, *a1;  // a1: the second sum's left operand (kDx)
-  int64_t am, ak;
-  const void *b0, *b1;  // b1: up (kForward, kRecompute), the second sum's right operand (kDx)
-  int64_t bn0, bk0, bn1, bk1;
+  int64_t R, C, K;  // output rows and columns (inner units for kForward, kRecompute), sum length of a pass
+  const void *r0, *r1;  // r1: left operand of the second pass (kDx), the up half (kDw)
+  int64_t ldr;
+  const void *c0, *c1;  // c1: up weights
+  int64_t ldc0, ldc1;
+  uint32_t tiles_r, tiles_c;
   int act;
-  void* out;  // h, dx or a weight gradient
-  int64_t ldo;
+  void *out0, *out1;  // h or dx; dw_gate and dw_up
+  int64_t ldo0, ldo1;
   bool out_f32;
   int accumulate;
   const void* dh;
   int64_t lddh;
-  void *dg, *du;
-  int64_t ldd;
+  void* dgu;  // [R, 2 * half] of dg | du (kRecompute)
+  int64_t half;
 };
 
-constexpr int kTileM = 64, kTileN = 64, kTileK = 32, kPad = 8;
+constexpr int kThreads = 512;
+constexpr int kStepK = 64;
+constexpr int kTileC = 256;
 
-template <typename T>
-__device__ __forceinline__ void stage(T (*lds)[kTileK + kPad], const T* src, int64_t rows, int64_t K, int64_t sr,
-                                      int64_t sk, int64_t r0, int64_t k0) {
-  for (int i = threadIdx.x; i < 64 * kTileK; i += 256) {
-    // consecutive threads along the consecutive elements
-    const int r = sk == 1 ? i / kTileK : i % 64, k = sk == 1 ? i % kTileK : i / 64;
-    T v = (T)0.0f;
-    if (r0 + r < rows && k0 + k < K) v = src[(r0 + r) * sr + (k0 + k) * sk];
-    lds[r][k] = v;
-  }
+// Operands hold whole pieces of 8 elements: rows that do not end on one are
+// padded with zeros (lay_out, kRecompute's dg | du).
+__device__ __forceinline__ int64_t round8(int64_t n) { return (n + 7) & ~(int64_t)7; }
+
+// Descriptor of a buffer of 'bytes' bytes (raw, bounds-checked).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
+  const int64_t b = bytes < 0 ? 0 : (bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)b, 0x00020000);
 }
 
-template <typename T, int MODE>
-__global__ __launch_bounds__(256) void k_product(Product p) {
-  typedef typename Frag<T>::type frag;
-  constexpr bool kTwo = MODE == kForward || MODE == kRecompute;
-  __shared__ __attribute__((aligned(16))) T As[kTileM][kTileK + kPad];
-  __shared__ __attribute__((aligned(16))) T Bs[kTwo ? 2 : 1][kTileN][kTileK + kPad];
-  const int64_t m0 = (int64_t)blockIdx.y * kTileM, n0 = (int64_t)blockIdx.x * kTileN;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  f32x16 acc0 = {}, acc1 = {};
-  for (int pass = 0; pass < (MODE == kDx ? 2 : 1); ++pass) {
-    const T* A = (const T*)(pass == 0 ? p.a0 : p.a1);
-    const T* B = (const T*)(pass == 0 ? p.b0 : p.b1);
-    const int64_t bn = pass == 0 ? p.bn0 : p.bn1, bk = pass == 0 ? p.bk0 : p.bk1;
-    for (int64_t k0 = 0; k0 < p.K; k0 += kTileK) {
-      __syncthreads();
-      stage(As, A, p.M, p.K, p.am, p.ak, m0, k0);
-      stage(Bs[0], B, p.N, p.K, bn, bk, n0, k0);
-      if constexpr (kTwo) stage(Bs[1], (const T*)p.b1, p.N, p.K, p.bn1, p.bk1, n0, k0);
-      __syncthreads();
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, LDS char* lds, int voffset, int soffset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LDS void*)lds, 16, voffset, soffset, 0, 0);
+}
+
+constexpr int kOutside = 0x7FFFFFF0;  // beyond every buffer
+
+// One operand tile of ROWS = 64 * FR rows (r or c), k along: its loads to LDS.
+template <int FR>
+struct Along {
+  int voff[FR];
+  int piece;  // first k of this lane's piece
+  __device__ __forceinline__ void init(int wave, int lane, int64_t ld) {
+    piece = ((lane & 7) ^ (lane >> 3)) * 8;
 #pragma unroll
-      for (int kk = 0; kk < kTileK; kk += 16) {
-        const frag a = *(const frag*)&As[wm + (lane & 31)][kk + (lane >> 5) * 8];
-        const frag b = *(const frag*)&Bs[0][wn + (lane & 31)][kk + (lane >> 5) * 8];
-        acc0 = Frag<T>::mma(a, b, acc0);
-        if constexpr (kTwo) {
-          const frag c = *(const frag*)&Bs[1][wn + (lane & 31)][kk + (lane >> 5) * 8];
-          acc1 = Frag<T>::mma(a, c, acc1);
+    for (int j = 0; j < FR; ++j) voff[j] = (int)((64 * j + 8 * wave + (lane >> 3)) * ld * 2) + piece * 2;
+  }
+  // k0: first k of the step; left: k that remain from there
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, LDS char* lds, int wave, int j, int64_t k0,
+                                       int64_t left) const {
+    const int v = piece < left ? voff[j] : kOutside;
+    load_to_lds(r, lds + (64 * j + 8 * wave) * 128, v, (int)(k0 * 2));
+  }
+};
+
+// One operand tile of 64 * FR columns, k across.
+template <int FR>
+struct Across {
+  static constexpr int kPieces = 8 * FR;         // of an LDS row
+  static constexpr int kRows = 64 / kPieces;     // k rows of one load
+  static constexpr int kSpread = FR == 1 ? 1 : 3;
+  int voff[FR];
+  __device__ __forceinline__ void init(int wave, int lane, int64_t ld) {
+#pragma unroll
+    for (int j = 0; j < FR; ++j) {
+      const int k = (wave + 8 * j) * kRows + lane / kPieces;
+      voff[j] = (int)(k * ld * 2) + ((lane % kPieces) ^ ((k & kSpread) << 2)) * 16;
+    }
+  }
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, LDS char* lds, int wave, int j) const {
+    load_to_lds(r, lds + (wave + 8 * j) * 1024, voff[j], 0);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ typename Frag<T>::type along_frag(const LDS char* lds, int block, int kk, int lane) {
+  const int off = (lane & 31) * 128 + (((kk * 2 + (lane >> 5)) ^ (lane & 7)) * 16);
+  return *(const LDS typename Frag<T>::type*)(lds + block * 32 * 128 + off);
+}
+
+template <typename T, int FR>
+__device__ __forceinline__ typename Frag<T>::type across_frag(const LDS char* lds, int block, int kk, int lane) {
+  const int s = lane & 15, q = (s >> 2) & Across<FR>::kSpread;
+  const int off = ((lane >> 5) * 8 + (s >> 2)) * (FR * 128) + ((block ^ q) * 64) + ((lane >> 4) & 1) * 32 + (s & 3) * 8;
+  const LDS char* p = lds + kk * 16 * (FR * 128) + off;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)p);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)(p + 4 * (FR * 128)));
+  return __builtin_bit_cast(typename Frag<T>::type, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Where a workgroup's tile lies. Workgroups go to the 8 XCDs in turn; each XCD
+// gets a contiguous run of tiles, in blocks of 8 tiles along r, so that the 32
+// tiles it works on at a time share 8 row tiles and 4 column tiles in its L2.
+__device__ __forceinline__ void tile_of(const Product& p, uint32_t id, uint32_t* tr, uint32_t* tc) {
+  const uint32_t n = p.tiles_r * p.tiles_c;
+  const uint32_t xcd = id & 7, i = id >> 3, full = n >> 3, rest = n & 7;
+  const uint32_t t = xcd * full + (xcd < rest ? xcd : rest) + i;
+  const uint32_t per = 8 * p.tiles_c;
+  const uint32_t g = t / per, in = t - g * per;
+  const uint32_t rows = p.tiles_r - g * 8 < 8 ? p.tiles_r - g * 8 : 8;
+  *tc = in / rows;
+  *tr = g * 8 + (in - *tc * rows);
+}
+
+// The accumulators of a wave: FR blocks of 32 rows by 2 blocks of 32 columns
+// (kForward, kRecompute: gate and up of the same 32 inner units).
+template <int FR>
+struct Acc {
+  f32x16 v[FR][2];
+};
+
+template <typename T, int MODE, int FR>
+__device__ __forceinline__ void step(const Product& p, const LDS char* __restrict__ rd, LDS char* __restrict__ wr,
+                                     const Along<FR>& ra, const Across<FR>& rx, const Along<4>& ca,
+                                     const Across<4>& cx, int64_t row0, int64_t col0, int z, int wave, int lane,
+                                     int64_t next, int64_t steps1, int64_t steps, bool compute, Acc<FR>& acc) {
+  constexpr bool kPair = MODE == kForward || MODE == kRecompute;
+  constexpr int kTileBytesR = FR * 64 * 128;
+  if (next < steps) {
+    const bool second = MODE == kDx && next >= steps1;
+    const int64_t k0 = (second ? next - steps1 : next) * kStepK;
+    const int64_t left = p.K - k0;
+    if constexpr (MODE == kDw) {
+      const T* r = (const T*)(z == 0 ? p.r0 : p.r1) + k0 * p.ldr + row0;
+      const int64_t rows = left < kStepK ? left : kStepK;
+      const auto b = buffer_of(r, ((rows - 1) * p.ldr + round8(p.R) - row0) * 2);
+#pragma unroll
+      for (int j = 0; j < FR; ++j) rx.load(b, wr, wave, j);
+    } else {
+      const T* r = (const T*)(second ? p.r1 : p.r0) + row0 * p.ldr;
+      const int64_t rows = p.R - row0 < 64 * FR ? p.R - row0 : 64 * FR;
+      const auto b = buffer_of(r, ((rows - 1) * p.ldr + round8(p.K)) * 2);
+#pragma unroll
+      for (int j = 0; j < FR; ++j) ra.load(b, wr, wave, j, k0, left);
+    }
+    LDS char* wc = wr + kTileBytesR;
+    if constexpr (kPair) {
+      const int64_t rows = p.C - col0 < 128 ? p.C - col0 : 128;
+      const auto bg = buffer_of((const T*)p.c0 + col0 * p.ldc0, ((rows - 1) * p.ldc0 + round8(p.K)) * 2);
+      const auto bu = buffer_of((const T*)p.c1 + col0 * p.ldc1, ((rows - 1) * p.ldc1 + round8(p.K)) * 2);
+      // LDS rows 0..127 gate, 128..255 up; ca holds the gate's offsets, cx (its first two) the up's
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        ca.load(bg, wc, wave, j, k0, left);
+        const int v = ca.piece < left ? cx.voff[j] : kOutside;
+        load_to_lds(bu, wc + (128 + 64 * j + 8 * wave) * 128, v, (int)(k0 * 2));
+      }
+    } else {
+      const int64_t ld = second ? p.ldc1 : p.ldc0;
+      const T* c = (const T*)(second ? p.c1 : p.c0) + k0 * ld + col0;
+      const int64_t rows = left < kStepK ? left : kStepK;
+      const auto b = buffer_of(c, ((rows - 1) * ld + round8(p.C) - col0) * 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // the second pass's weights may have rows of another length
+        if (second) {
+          const int k = (wave + 8 * j) * Across<4>::kRows + lane / Across<4>::kPieces;
+          const int v = (int)(k * ld * 2) + ((lane % Across<4>::kPieces) ^ ((k & 3) << 2)) * 16;
+          load_to_lds(b, wc + (wave + 8 * j) * 1024, v, 0);
+        } else {
+          cx.load(b, wc, wave, j);
         }
       }
     }
   }
-  const int64_t n = n0 + wn + (lane & 31);
+  if (!compute) return;
+  const LDS char* rc = rd + kTileBytesR;
+  const int wr_block = (wave >> 2) * FR, wc_block = wave & 3;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t m = m0 + wm + (i / 4) * 8 + (lane >> 5) * 4 + (i & 3);
-    if (m >= p.M || n >= p.N) continue;
-    if constexpr (kTwo) {
-      float a, d;
-      act_and_grad(p.act, acc0[i], &a, &d);
-      if (p.out != nullptr) ((T*)p.out)[m * p.ldo + n] = from_f32<T>(a * acc1[i]);
-      if constexpr (MODE == kRecompute) {
-        const float dh = to_f32(((const T*)p.dh)[m * p.lddh + n]);
-        ((T*)p.dg)[m * p.ldd + n] = from_f32<T>(dh * acc1[i] * d);
-        ((T*)p.du)[m * p.ldd + n] = from_f32<T>(dh * a);
+  for (int kk = 0; kk < 4; ++kk) {
+    typename Frag<T>::type fc[2], fr[FR];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if constexpr (kPair) fc[c] = along_frag<T>(rc, wc_block + 4 * c, kk, lane);
+      else fc[c] = across_frag<T, 4>(rc, wc_block * 2 + c, kk, lane);
+    }
+#pragma unroll
+    for (int r = 0; r < FR; ++r) {
+      if constexpr (MODE == kDw) fr[r] = across_frag<T, FR>(rd, wr_block + r, kk, lane);
+      else fr[r] = along_frag<T>(rd, wr_block + r, kk, lane);
+    }
+#pragma unroll
+    for (int r = 0; r < FR; ++r)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) acc.v[r][c] = Frag<T>::mma(fc[c], fr[r], acc.v[r][c]);
+  }
+}
+
+// 16-bit tile in LDS on its way out (or dh on its way in): rows of COLS
+// columns, pieces of 16 bytes, piece p of row i at p ^ (i & (pieces - 1)).
+template <int COLS>
+__device__ __forceinline__ int tile_piece(int row, int piece) {
+  return row * (COLS * 2) + ((piece ^ (row & (COLS / 8 - 1))) * 16);
+}
+
+template <typename T, int COLS, int ROWS>
+__device__ __forceinline__ void store_tile(const LDS char* lds, T* out, int64_t ld, int64_t rows, int64_t cols) {
+  for (int i = threadIdx.x; i < ROWS * (COLS / 8); i += kThreads) {
+    const int row = i / (COLS / 8), piece = i % (COLS / 8);
+    if (row < rows && piece * 8 < cols) {
+      const u32x4 v = *(const LDS u32x4*)(lds + tile_piece<COLS>(row, piece));
+      T* o = out + row * ld + piece * 8;
+      if (cols - piece * 8 >= 8) {
+        *(GLOBAL u32x4_any*)o = v;
+      } else {
+        typedef T t8 __attribute__((ext_vector_type(8)));
+        const t8 e = __builtin_bit_cast(t8, v);
+        for (int k = 0; k < cols - piece * 8; ++k) ((GLOBAL T*)o)[k] = e[k];
       }
-    } else if (p.out_f32) {
-      float* o = (float*)p.out + m * p.ldo + n;
-      *o = p.accumulate ? *o + acc0[i] : acc0[i];
-    } else {
-      ((T*)p.out)[m * p.ldo + n] = from_f32<T>(acc0[i]);
     }
   }
 }
 
-template <int MODE>
-hipError_t launch_product(int dtype, const Product& p, hipStream_t s) {
-  const dim3 g((unsigned)((p.N + kTileN - 1) / kTileN), (unsigned)((p.M + kTileM - 1) / kTileM));
-  if (dtype == MSAMP_F16) k_product<f16, MODE><<<g, dim3(256), 0, s>>>(p);
-  else k_product<bf16, MODE><<<g, dim3(256), 0, s>>>(p);
+template <typename T>
+__device__ __forceinline__ uint64_t pack4(const float* f) {
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  t4 v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = from_f32<T>(f[k]);
+  return __builtin_bit_cast(uint64_t, v);
+}
+
+// The tile's sums to where they go.
+template <typename T, int MODE, int FR>
+__device__ __forceinline__ void finish(const Product& p, LDS char* lds, int64_t row0, int64_t col0, int z, int wave,
+                                       int lane, const Acc<FR>& acc) {
+  constexpr int kRows = 64 * FR;
+  const int64_t rows = p.R - row0;
+  const int lrow = (wave >> 2) * (32 * FR) + (lane & 31);  // + 32 r
+  __syncthreads();  // the stages have been read
+  if constexpr (MODE == kForward || MODE == kRecompute) {
+    const int lcol = (wave & 3) * 32 + (lane >> 5) * 4;  // + 8 q + e
+    LDS char* second = lds + kRows * 256;
+    const int64_t cols = p.C - col0;
+    if constexpr (MODE == kRecompute) {
+      for (int i = threadIdx.x; i < kRows * 16; i += kThreads) {
+        const int row = i / 16, piece = i % 16;
+        float f[8] = {};
+        const int64_t n = cols - piece * 8;
+        if (row < rows && n > 0)
+          load8((const T*)p.dh + (row0 + row) * p.lddh + col0 + piece * 8, (int)(n < 8 ? n : 8), f);
+        typedef T t8 __attribute__((ext_vector_type(8)));
+        t8 v;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = (T)f[k];
+        *(LDS u32x4*)(lds + tile_piece<128>(row, piece)) = __builtin_bit_cast(u32x4, v);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < FR; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float a[4], d[4], g[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) act_and_grad(p.act, acc.v[r][0][q * 4 + e], &a[e], &d[e]);
+        const int at = tile_piece<128>(lrow + 32 * r, (lcol >> 3) + q) + (lane >> 5) * 8;
+        if constexpr (MODE == kForward) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] *= acc.v[r][1][q * 4 + e];
+          *(LDS uint64_t*)(lds + at) = pack4<T>(a);
+        } else {
+          typedef T t4 __attribute__((ext_vector_type(4)));
+          const t4 dh = *(const LDS t4*)(lds + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            g[e] = to_f32(dh[e]) * acc.v[r][1][q * 4 + e] * d[e];
+            d[e] = to_f32(dh[e]) * a[e];
+          }
+          *(LDS uint64_t*)(lds + at) = pack4<T>(g);
+          *(LDS uint64_t*)(second + at) = pack4<T>(d);
+        }
+      }
+    __syncthreads();
+    if constexpr (MODE == kForward) {
+      store_tile<T, 128, kRows>(lds, (T*)p.out0 + row0 * p.ldo0 + col0, p.ldo0, rows, cols);
+    } else {
+      // columns behind the last inner unit are zero: they are operands of the next products
+      T* o = (T*)p.dgu + row0 * (2 * p.half) + col0;
+      store_tile<T, 128, kRows>(lds, o, 2 * p.half, rows, p.half - col0);
+      store_tile<T, 128, kRows>(second, o + p.half, 2 * p.half, rows, p.half - col0);
+      if (p.out0 != nullptr) {
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < FR; ++r)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float a[4], d[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              act_and_grad(p.act, acc.v[r][0][q * 4 + e], &a[e], &d[e]);
+              a[e] *= acc.v[r][1][q * 4 + e];
+            }
+            *(LDS uint64_t*)(lds + tile_piece<128>(lrow + 32 * r, (lcol >> 3) + q) + (lane >> 5) * 8) = pack4<T>(a);
+          }
+        __syncthreads();
+        store_tile<T, 128, kRows>(lds, (T*)p.out0 + row0 * p.ldo0 + col0, p.ldo0, rows, cols);
+      }
+    }
+  } else {
+    void* base = MODE == kDw && z == 1 ? p.out1 : p.out0;
+    const int64_t ld = MODE == kDw && z == 1 ? p.ldo1 : p.ldo0;
+    const int64_t cols = p.C - col0;
+    const int lcol = (wave & 3) * 64 + (lane >> 5) * 4;  // + 32 c + 8 q + e
+    if (MODE == kDw && p.out_f32) {
+#pragma unroll
+      for (int r = 0; r < FR; ++r) {
+        const int row = lrow + 32 * r;
+        float* o = (float*)base + (row0 + row) * ld + col0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int col = lcol + 32 * c + 8 * q;
+            typedef float f32x4 __attribute__((ext_vector_type(4)));
+            typedef f32x4 f32x4_any __attribute__((aligned(4)));
+            if (row < rows && col + 4 <= cols) {
+              f32x4 v;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = acc.v[r][c][q * 4 + e];
+              if (p.accumulate) v += *(const GLOBAL f32x4_any*)(o + col);
+              *(GLOBAL f32x4_any*)(o + col) = v;
+            } else if (row < rows) {
+              for (int e = 0; e < 4; ++e)
+                if (col + e < cols) {
+                  const float v = acc.v[r][c][q * 4 + e];
+                  o[col + e] = p.accumulate ? o[col + e] + v : v;
+                }
+            }
+          }
+      }
+      return;
+    }
+#pragma unroll
+    for (int r = 0; r < FR; ++r)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc.v[r][c][q * 4 + e];
+          const int at = tile_piece<256>(lrow + 32 * r, ((lcol + 32 * c) >> 3) + q) + (lane >> 5) * 8;
+          *(LDS uint64_t*)(lds + at) = pack4<T>(v);
+        }
+    __syncthreads();
+    store_tile<T, 256, kRows>(lds, (T*)base + row0 * ld + col0, ld, rows, cols);
+  }
+}
+
+template <typename T, int MODE, int FR>
+__global__ __launch_bounds__(kThreads) void k_product(Product p) {
+  constexpr bool kPair = MODE == kForward || MODE == kRecompute;
+  constexpr int kStage = FR * 64 * 128 + kTileC * 128;
+  __shared__ __attribute__((aligned(16))) char smem[2 * kStage];  // also holds the outgoing tiles
+  LDS char* lds = (LDS char*)smem;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  uint32_t tr, tc;
+  const int z = MODE == kDw ? (int)blockIdx.y : 0;
+  tile_of(p, blockIdx.x, &tr, &tc);
+  const int64_t row0 = (int64_t)tr * (64 * FR), col0 = (int64_t)tc * (kPair ? 128 : 256);
+  Along<FR> ra;
+  Across<FR> rx;
+  Along<4> ca;
+  Across<4> cx;
+  if constexpr (MODE == kDw) rx.init(wave, lane, p.ldr);
+  else ra.init(wave, lane, p.ldr);
+  if constexpr (kPair) {
+    ca.init(wave, lane, p.ldc0);
+    Along<4> up;
+    up.init(wave, lane, p.ldc1);
+    cx.voff[0] = up.voff[0];
+    cx.voff[1] = up.voff[1];
+  } else {
+    cx.init(wave, lane, p.ldc0);
+  }
+  Acc<FR> acc;
+#pragma unroll
+  for (int r = 0; r < FR; ++r) acc.v[r][0] = acc.v[r][1] = f32x16{};
+  const int64_t steps1 = (p.K + kStepK - 1) / kStepK;
+  const int64_t steps = MODE == kDx ? 2 * steps1 : steps1;
+  step<T, MODE, FR>(p, lds + kStage, lds, ra, rx, ca, cx, row0, col0, z, wave, lane, 0, steps1, steps, false, acc);
+  __syncthreads();
+  for (int64_t i = 0; i < steps; ++i) {
+    const int at = (int)(i & 1) * kStage;
+    step<T, MODE, FR>(p, lds + at, lds + (kStage - at), ra, rx, ca, cx, row0, col0, z, wave, lane, i + 1, steps1,
+                      steps, true, acc);
+    __syncthreads();
+  }
+  finish<T, MODE, FR>(p, lds, row0, col0, z, wave, lane, acc);
+}
+
+template <typename T, int MODE, int FR>
+hipError_t launch_tiles(Product p, hipStream_t s) {
+  p.tiles_r = (uint32_t)((p.R + 64 * FR - 1) / (64 * FR));
+  const int tc = MODE == kForward || MODE == kRecompute ? 128 : 256;
+  p.tiles_c = (uint32_t)((p.C + tc - 1) / tc);
+  const dim3 g(p.tiles_r * p.tiles_c, MODE == kDw ? 2 : 1);
+  k_product<T, MODE, FR><<<g, dim3(kThreads), 0, s>>>(p);
   return hipGetLastError();
 }
 
-int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
-
-}  // namespace
-
-int64_t ffn_forward_workspace(const msamp_gated_ffn&) { return 0; }
-
-int64_t ffn_backward_workspace(const msamp_gated_ffn& a) {
-  return 2 * round256(a.tokens * a.ffn * 2) + (a.x_ckpt != nullptr ? round256(a.tokens * a.hidden * 2) : 0);
+template <int MODE>
+hipError_t launch_product(int dtype, const Product& p, hipStream_t s) {
+  return dtype == MSAMP_F16 ? launch_tiles<f16, MODE, 4>(p, s) : launch_tiles<bf16, MODE, 4>(p, s);
 }
 
-msamp_status ffn_forward(const msamp_gated_ffn& a, void*, hipStream_t s) {
+// ---------------------------------------------------------------- layout ---
+
+// out [rows, ld] <- src [rows, cols] or a checkpoint's values, zeros behind the
+// last column.
+template <typename T>
+__global__ __launch_bounds__(256) void k_layout(int64_t rows, int64_t cols, const T* src, int64_t lds, CkptRef ck,
+                                                T* out, int64_t ld) {
+  const int64_t per = ld / 8, total = rows * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per, col = (i - row * per) * 8;
+    const int64_t left = cols - col;
+    const int n = left < 0 ? 0 : (left < 8 ? (int)left : 8);
+    float f[8];
+    if (src != nullptr) {
+      load8(src + row * lds + col, n, f);
+    } else {
+      load_ckpt8(ck.fmt, ck.codes + row * ck.ld, ck.scales + row * ck.ld_scales, col, n, f);
+      const float lim = __is_same(T, f16) ? kF16Max : kBf16Max;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = clamp_finite(f[k], lim);
+    }
+    store8(out + row * ld + col, 8, f);
+  }
+}
+
+hipError_t launch_layout(int dtype, int64_t rows, int64_t cols, const void* src, int64_t lds, const CkptRef& ck,
+                         void* out, int64_t ld, hipStream_t s) {
+  const int64_t blocks = (rows * (ld / 8) + 255) / 256;
+  const dim3 g((unsigned)(blocks < 65536 ? blocks : 65536));
+  if (dtype == MSAMP_F16) k_layout<f16><<<g, dim3(256), 0, s>>>(rows, cols, (const f16*)src, lds, ck, (f16*)out, ld);
+  else k_layout<bf16><<<g, dim3(256), 0, s>>>(rows, cols, (const bf16*)src, lds, ck, (bf16*)out, ld);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ plan ---
+
+int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
+int64_t round64(int64_t n) { return (n + 63) / 64 * 64; }
+
+// Whether the matrix kernels can read an operand where it lies: 16-byte
+// aligned rows of whole 16-byte pieces, and a tile of 256 rows within the 2^31
+// bytes of a buffer.
+bool direct(const void* p, int64_t ld, int64_t cols) {
+  return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0 && cols % 8 == 0 && ld >= cols && ld < (1 << 22);
+}
+
+// Hands out pieces of the workspace (or only counts them).
+struct Arena {
+  char* base;
+  int64_t used = 0;
+  void* take(int64_t bytes) {
+    void* p = base == nullptr ? nullptr : base + used;
+    used += round256(bytes);
+    return p;
+  }
+};
+
+struct Operand {
+  const void* p;
+  int64_t ld;
+};
+
+// An operand [rows, cols], laid out in the workspace when it has to be.
+msamp_status lay_out(int dtype, int64_t rows, int64_t cols, const void* p, int64_t ld, const msamp_checkpoint* ck,
+                     Arena& ws, bool run, hipStream_t s, Operand* out) {
+  *out = {p, ld};
+  if (rows == 0 || cols == 0 || (ck == nullptr && direct(p, ld, cols))) return MSAMP_OK;
+  const int64_t lp = round64(cols);
+  if (lp >= (1 << 22)) return fail(MSAMP_E_INVALID_ARG, "rows longer than 2^22 elements have to be 16-byte aligned");
+  void* q = ws.take(rows * lp * 2);
+  *out = {q, lp};
+  CkptRef c;
+  if (ck != nullptr) c = {ck->codes, ck->ld, ck->scales, ck->ld_scales, (int)ck->fmt};
+  if (run)
+    MSAMP_LAUNCH(MSAMP_KERNEL_FFN_LAYOUT, s,
+                 launch_layout(dtype, rows, cols, ck == nullptr ? p : nullptr, ld, c, q, lp, s));
+  return MSAMP_OK;
+}
+
+// Output of zeros: the sums of nothing.
+template <typename T>
+__global__ void k_fill_zero(int64_t rows, int64_t cols, T* out, int64_t ld) {
+  const int64_t total = rows * cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256)
+    out[i / cols * ld + i % cols] = (T)0.0f;
+}
+
+msamp_status fill_zero(int dtype, int64_t rows, int64_t cols, void* out, int64_t ld, hipStream_t s) {
+  if (rows == 0 || cols == 0) return MSAMP_OK;
+  const int64_t blocks = (rows * cols + 255) / 256;
+  const dim3 g((unsigned)(blocks < 65536 ? blocks : 65536));
+  auto launch = [&]() {
+    if (dtype == MSAMP_F32) k_fill_zero<float><<<g, dim3(256), 0, s>>>(rows, cols, (float*)out, ld);
+    else k_fill_zero<uint16_t><<<g, dim3(256), 0, s>>>(rows, cols, (uint16_t*)out, ld);
+    return hipGetLastError();
+  };
+  MSAMP_LAUNCH(MSAMP_KERNEL_FFN_LAYOUT, s, launch());
+  return MSAMP_OK;
+}
+
+// Counts the workspace (run = false) or makes the call.
+msamp_status forward(const msamp_gated_ffn& a, Arena& ws, bool run, hipStream_t s) {
   if (a.tokens == 0 || a.ffn == 0) return MSAMP_OK;
+  if (a.hidden == 0) return run ? fill_zero(a.dtype, a.tokens, a.ffn, a.h, a.ldh, s) : MSAMP_OK;
+  Operand x, g, u;
+  MSAMP_TRY(lay_out(a.dtype, a.tokens, a.hidden, a.x, a.ldx, nullptr, ws, run, s, &x));
+  MSAMP_TRY(lay_out(a.dtype, a.ffn, a.hidden, a.w_gate, a.ld_gate, nullptr, ws, run, s, &g));
+  MSAMP_TRY(lay_out(a.dtype, a.ffn, a.hidden, a.w_up, a.ld_up, nullptr, ws, run, s, &u));
+  if (!run) return MSAMP_OK;
   Product p = {};
-  p.M = a.tokens, p.N = a.ffn, p.K = a.hidden;
-  p.a0 = a.x, p.am = a.ldx, p.ak = 1;
-  p.b0 = a.w_gate, p.bn0 = a.ld_gate, p.bk0 = 1;
-  p.b1 = a.w_up, p.bn1 = a.ld_up, p.bk1 = 1;
+  p.R = a.tokens, p.C = a.ffn, p.K = a.hidden;
+  p.r0 = x.p, p.ldr = x.ld;
+  p.c0 = g.p, p.ldc0 = g.ld, p.c1 = u.p, p.ldc1 = u.ld;
   p.act = a.act;
-  p.out = a.h, p.ldo = a.ldh;
+  p.out0 = a.h, p.ldo0 = a.ldh;
   MSAMP_LAUNCH(MSAMP_KERNEL_FFN_FORWARD, s, launch_product<kForward>(a.dtype, p, s));
   return MSAMP_OK;
 }
 
-msamp_status ffn_backward(const msamp_gated_ffn& a, void* ws, hipStream_t s) {
-  char* w = (char*)ws;
-  void* dg = w;
-  w += round256(a.tokens * a.ffn * 2);
-  void* du = w;
-  w += round256(a.tokens * a.ffn * 2);
-  const void* x = a.x;
-  int64_t ldx = a.ldx;
-  if (a.x_ckpt != nullptr && a.tokens > 0 && a.hidden > 0) {
-    const CkptRef ck = {a.x_ckpt->codes, a.x_ckpt->ld, a.x_ckpt->scales, a.x_ckpt->ld_scales, (int)a.x_ckpt->fmt};
-    MSAMP_LAUNCH(MSAMP_KERNEL_FFN_LAYOUT, s,
-                 launch_checkpoint_load(a.dtype, a.tokens, a.hidden, ck, w, a.hidden, s));
-    x = w;
-    ldx = a.hidden;
+msamp_status backward(const msamp_gated_ffn& a, Arena& ws, bool run, hipStream_t s) {
+  const int64_t T = a.tokens, K = a.hidden, F = a.ffn;
+  if (T == 0 || F == 0 || K == 0) {  // sums of nothing
+    if (!run) return MSAMP_OK;
+    if (a.h != nullptr) MSAMP_TRY(fill_zero(a.dtype, T, F, a.h, a.ldh, s));
+    MSAMP_TRY(fill_zero(a.dtype, T, K, a.dx, a.lddx, s));
+    if (a.dw_accumulate) return MSAMP_OK;
+    MSAMP_TRY(fill_zero(a.dw_dtype, F, K, a.dw_gate, a.ld_dw_gate, s));
+    return fill_zero(a.dw_dtype, F, K, a.dw_up, a.ld_dw_up, s);
   }
+  Operand x, g, u;
+  MSAMP_TRY(lay_out(a.dtype, T, K, a.x, a.ldx, a.x_ckpt, ws, run, s, &x));
+  MSAMP_TRY(lay_out(a.dtype, F, K, a.w_gate, a.ld_gate, nullptr, ws, run, s, &g));
+  MSAMP_TRY(lay_out(a.dtype, F, K, a.w_up, a.ld_up, nullptr, ws, run, s, &u));
+  const int64_t half = round64(F);
+  if (2 * half >= (1 << 22)) return fail(MSAMP_E_INVALID_ARG, "ffn exceeds 2^21 - 64");
+  char* dgu = (char*)ws.take(T * 2 * half * 2);
+  if (!run) return MSAMP_OK;
   Product p = {};
-  if (a.tokens > 0 && a.ffn > 0) {
-    p.M = a.tokens, p.N = a.ffn, p.K = a.hidden;
-    p.a0 = x, p.am = ldx, p.ak = 1;
-    p.b0 = a.w_gate, p.bn0 = a.ld_gate, p.bk0 = 1;
-    p.b1 = a.w_up, p.bn1 = a.ld_up, p.bk1 = 1;
-    p.act = a.act;
-    p.out = a.h, p.ldo = a.ldh;
-    p.dh = a.dh, p.lddh = a.lddh;
-    p.dg = dg, p.du = du, p.ldd = a.ffn;
-    MSAMP_LAUNCH(MSAMP_KERNEL_FFN_RECOMPUTE, s, launch_product<kRecompute>(a.dtype, p, s));
-  }
-  if (a.hidden == 0) return MSAMP_OK;
-  if (a.tokens > 0) {
-    p = {};
-    p.M = a.tokens, p.N = a.hidden, p.K = a.ffn;
-    p.a0 = dg, p.a1 = du, p.am = a.ffn, p.ak = 1;
-    p.b0 = a.w_gate, p.bn0 = 1, p.bk0 = a.ld_gate;
-    p.b1 = a.w_up, p.bn1 = 1, p.bk1 = a.ld_up;
-    p.out = a.dx, p.ldo = a.lddx;
-    MSAMP_LAUNCH(MSAMP_KERNEL_FFN_DX, s, launch_product<kDx>(a.dtype, p, s));
-  }
-  for (int i = 0; i < 2 && a.ffn > 0; ++i) {
-    p = {};
-    p.M = a.ffn, p.N = a.hidden, p.K = a.tokens;
-    p.a0 = i == 0 ? dg : du, p.am = 1, p.ak = a.ffn;
-    p.b0 = x, p.bn0 = 1, p.bk0 = ldx;
-    p.out = i == 0 ? a.dw_gate : a.dw_up, p.ldo = i == 0 ? a.ld_dw_gate : a.ld_dw_up;
-    p.out_f32 = a.dw_dtype == MSAMP_F32;
-    p.accumulate = a.dw_accumulate;
-    MSAMP_LAUNCH(MSAMP_KERNEL_FFN_DW, s, launch_product<kDw>(a.dtype, p, s));
-  }
+  p.R = T, p.C = F, p.K = K;
+  p.r0 = x.p, p.ldr = x.ld;
+  p.c0 = g.p, p.ldc0 = g.ld, p.c1 = u.p, p.ldc1 = u.ld;
+  p.act = a.act;
+  p.out0 = a.h, p.ldo0 = a.ldh;
+  p.dh = a.dh, p.lddh = a.lddh;
+  p.dgu = dgu, p.half = half;
+  MSAMP_LAUNCH(MSAMP_KERNEL_FFN_RECOMPUTE, s, launch_product<kRecompute>(a.dtype, p, s));
+
+  p = {};
+  p.R = T, p.C = K, p.K = F;
+  p.r0 = dgu, p.r1 = dgu + half * 2, p.ldr = 2 * half;
+  p.c0 = g.p, p.ldc0 = g.ld, p.c1 = u.p, p.ldc1 = u.ld;
+  p.out0 = a.dx, p.ldo0 = a.lddx;
+  MSAMP_LAUNCH(MSAMP_KERNEL_FFN_DX, s, launch_product<kDx>(a.dtype, p, s));
+
+  p = {};
+  p.R = F, p.C = K, p.K = T;
+  p.r0 = dgu, p.r1 = dgu + half * 2, p.ldr = 2 * half;
+  p.c0 = x.p, p.ldc0 = x.ld;
+  p.out0 = a.dw_gate, p.ldo0 = a.ld_dw_gate, p.out1 = a.dw_up, p.ldo1 = a.ld_dw_up;
+  p.out_f32 = a.dw_dtype == MSAMP_F32, p.accumulate = a.dw_accumulate;
+  MSAMP_LAUNCH(MSAMP_KERNEL_FFN_DW, s, launch_product<kDw>(a.dtype, p, s));
   return MSAMP_OK;
+}
+
+}  // namespace
+
+msamp_status ffn_forward_workspace(const msamp_gated_ffn& a, int64_t* bytes) {
+  Arena ws = {nullptr};
+  MSAMP_TRY(forward(a, ws, false, nullptr));
+  *bytes = ws.used;
+  return MSAMP_OK;
+}
+
+msamp_status ffn_backward_workspace(const msamp_gated_ffn& a, int64_t* bytes) {
+  Arena ws = {nullptr};
+  MSAMP_TRY(backward(a, ws, false, nullptr));
+  *bytes = ws.used;
+  return MSAMP_OK;
+}
+
+msamp_status ffn_forward(const msamp_gated_ffn& a, void* ws, hipStream_t s) {
+  Arena arena = {(char*)ws};
+  return forward(a, arena, true, s);
+}
+
+msamp_status ffn_backward(const msamp_gated_ffn& a, void* ws, hipStream_t s) {
+  Arena arena = {(char*)ws};
+  return backward(a, arena, true, s);
 }
 
 }  // namespace msamp

@@ -11,8 +11,8 @@
 namespace msamp {
 
 // Bytes of workspace of a call, and the call itself (arguments checked).
-int64_t ffn_forward_workspace(const msamp_gated_ffn& a);
-int64_t ffn_backward_workspace(const msamp_gated_ffn& a);
+msamp_status ffn_forward_workspace(const msamp_gated_ffn& a, int64_t* bytes);
+msamp_status ffn_backward_workspace(const msamp_gated_ffn& a, int64_t* bytes);
 msamp_status ffn_forward(const msamp_gated_ffn& a, void* ws, hipStream_t s);
 msamp_status ffn_backward(const msamp_gated_ffn& a, void* ws, hipStream_t s);
 

@@ -51,13 +51,9 @@ __global__ __launch_bounds__(kCkBlock) void k_checkpoint_load(Units u, int64_t c
   float f[8];
   load_ckpt8(ck.fmt, ck.codes + row * ck.ld, ck.scales + row * ck.ld_scales, col, n, f);
   if constexpr (sizeof(T) == 2) {
-    if (__is_same(T, f16)) {
+    const float lim = __is_same(T, f16) ? kF16Max : kBf16Max;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = clamp_finite(f[k], kF16Max);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = clamp_finite(f[k], 3.3895313892515355e38f);  // bfloat16's largest
-    }
+    for (int k = 0; k < 8; ++k) f[k] = clamp_finite(f[k], lim);
   }
   store8(out + row * ldout + col, n, f);
 }

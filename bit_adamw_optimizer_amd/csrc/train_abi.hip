@@ -247,16 +247,14 @@ msamp_status msamp_layernorm_backward(int64_t rows, int64_t cols, const void* dy
 int64_t msamp_gated_ffn_forward_workspace(const msamp_gated_ffn* args) {
   return workspace_of([&](int64_t* bytes) -> msamp_status {
     MSAMP_TRY(check_ffn(args, false));
-    *bytes = ffn_forward_workspace(*args);
-    return MSAMP_OK;
+    return ffn_forward_workspace(*args, bytes);
   });
 }
 
 int64_t msamp_gated_ffn_backward_workspace(const msamp_gated_ffn* args) {
   return workspace_of([&](int64_t* bytes) -> msamp_status {
     MSAMP_TRY(check_ffn(args, true));
-    *bytes = ffn_backward_workspace(*args);
-    return MSAMP_OK;
+    return ffn_backward_workspace(*args, bytes);
   });
 }
 
@@ -265,7 +263,9 @@ msamp_status msamp_gated_ffn_forward(const msamp_gated_ffn* args, void* workspac
   return guarded([&]() -> msamp_status {
     clear_error();
     MSAMP_TRY(check_ffn(args, false));
-    MSAMP_TRY(check_workspace(workspace, workspace_bytes, ffn_forward_workspace(*args)));
+    int64_t need = 0;
+    MSAMP_TRY(ffn_forward_workspace(*args, &need));
+    MSAMP_TRY(check_workspace(workspace, workspace_bytes, need));
     return ffn_forward(*args, workspace, (hipStream_t)stream);
   });
 }
@@ -275,7 +275,9 @@ msamp_status msamp_gated_ffn_backward(const msamp_gated_ffn* args, void* workspa
   return guarded([&]() -> msamp_status {
     clear_error();
     MSAMP_TRY(check_ffn(args, true));
-    MSAMP_TRY(check_workspace(workspace, workspace_bytes, ffn_backward_workspace(*args)));
+    int64_t need = 0;
+    MSAMP_TRY(ffn_backward_workspace(*args, &need));
+    MSAMP_TRY(check_workspace(workspace, workspace_bytes, need));
     return ffn_backward(*args, workspace, (hipStream_t)stream);
   });
 }
