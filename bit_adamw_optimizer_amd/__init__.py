@@ -775,18 +775,20 @@ _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 GROUP = 32  # elements of a checkpoint's group (MSAMP_CHECKPOINT_GROUP)
 
 
-def _device_of(t, name: str):
+def _device_of(t, name: str) -> int:
+    """Index of the GPU a tensor argument is on."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s is not a tensor" % name)
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("%s is not on a GPU" % name)
-    return t.device
+    return t.get_device()
 
 
-def _matrix(t, name: str, device, dtype, shape, written: bool = False):
+def _matrix(t, name: str, device: int, dtype, shape, written: bool = False):
     """(pointer, distance between rows) of a matrix argument."""
-    if _device_of(t, name) != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        if _device_of(t, name) != device:
+            raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, device))
     if t.dtype != dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != shape:
@@ -804,16 +806,28 @@ def _matrix(t, name: str, device, dtype, shape, written: bool = False):
     return t.data_ptr(), ld
 
 
-def _vector(t, name: str, device, dtype, n: int):
-    if _device_of(t, name) != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+def _vector(t, name: str, device: int, dtype, n: int):
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        if _device_of(t, name) != device:
+            raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, device))
     if t.dtype != dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,):
         raise ValueError("%s has shape %s, expected (%d,)" % (name, tuple(t.shape), n))
     if not t.is_contiguous():
         raise ValueError("%s is not contiguous" % name)
     return t.data_ptr() if n else None
+
+
+def _run(device: int, entry, *args) -> None:
+    """entry(*args, current stream) with the tensors' GPU as the current one."""
+    if torch.cuda.current_device() == device:
+        status = entry(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            status = entry(*args, torch._C._cuda_getCurrentRawStream(device))
+    if status != 0:
+        _check(status)
 
 
 class Checkpoint:
@@ -843,16 +857,16 @@ class Checkpoint:
         if codes.device != scales.device:
             raise ValueError("scales is on %s, expected %s" % (scales.device, codes.device))
         self.codes, self.scales, self.cols, self.fmt = codes, scales, cols, int(fmt)
-        self.rows, self.device = codes.shape[0], codes.device
+        self.rows, self.device = codes.shape[0], codes.get_device()
         empty = self.rows == 0 or cols == 0
         self._c = _Checkpoint(None if empty else codes.data_ptr(), codes.stride(0),
                               None if empty else scales.data_ptr(), scales.stride(0), self.fmt)
         self._flat = self.rows <= 1 or (codes.stride(0) >= cols and scales.stride(0) >= -(-cols // GROUP))
 
-    def _arg(self, name: str, device, shape, written: bool = False):
+    def _arg(self, name: str, device: int, shape, written: bool = False):
         if self.device != device:
-            raise ValueError("%s is on %s, expected %s" % (name, self.device, device))
-        if (self.rows, self.cols) != tuple(shape):
+            raise ValueError("%s is on cuda:%d, expected cuda:%d" % (name, self.device, device))
+        if (self.rows, self.cols) != shape:
             raise ValueError("%s has shape %s, expected %s" % (name, (self.rows, self.cols), tuple(shape)))
         if written and not self._flat:
             raise ValueError("%s: its rows overlap" % name)
@@ -867,17 +881,24 @@ def new_checkpoint(rows: int, cols: int, fmt: int = E4M3, device="cuda") -> Chec
                       torch.empty((rows, groups), dtype=torch.uint8, device=device), cols, fmt)
 
 
-def _dtype_of(t, name: str) -> int:
-    _device_of(t, name)
+def _checkpoint(t, name: str) -> Checkpoint:
+    if not isinstance(t, Checkpoint):
+        raise TypeError("%s is not a Checkpoint" % name)
+    return t
+
+
+def _leading(t, name: str):
+    """(device, dtype code, shape) of the matrix the other arguments go by."""
+    dev = _device_of(t, name)
     if t.dim() != 2:
         raise ValueError("%s must have two dimensions" % name)
     d = _DTYPES.get(t.dtype)
     if d is None:
         raise TypeError("%s has dtype %s, expected float32, float16 or bfloat16" % (name, t.dtype))
-    return d
+    return dev, d, t.shape
 
 
-def _input(x, device, dtype, shape):
+def _input(x, device: int, dtype, shape):
     """(pointer, distance between rows, checkpoint) of x or its checkpoint."""
     if isinstance(x, Checkpoint):
         return None, 0, x._arg("x", device, shape)
@@ -888,30 +909,29 @@ def _input(x, device, dtype, shape):
 def checkpoint_save(x: torch.Tensor, ckpt: Checkpoint) -> None:
     """ckpt <- x in 8 bits, in one pass. x is [rows, cols], float32, float16
     or bfloat16; its rows may lie apart."""
-    d = _dtype_of(x, "x")
-    p, ld = _matrix(x, "x", x.device, x.dtype, x.shape)
-    c = ckpt._arg("ckpt", x.device, x.shape, True)
-    with torch.cuda.device(x.device):
-        _check(lib().msamp_checkpoint_save(x.shape[0], x.shape[1], p, ld, d, c, _stream(x.device)))
+    dev, d, shape = _leading(x, "x")
+    p, ld = _matrix(x, "x", dev, x.dtype, shape)
+    c = _checkpoint(ckpt, "ckpt")._arg("ckpt", dev, shape, True)
+    _run(dev, lib().msamp_checkpoint_save, shape[0], shape[1], p, ld, d, c)
 
 
 def checkpoint_load(ckpt: Checkpoint, out: torch.Tensor) -> None:
     """out <- the values of ckpt, rounded to out's dtype (exact for bfloat16
     and float32)."""
-    d = _dtype_of(out, "out")
-    p, ld = _matrix(out, "out", out.device, out.dtype, out.shape, True)
-    c = ckpt._arg("ckpt", out.device, out.shape)
-    with torch.cuda.device(out.device):
-        _check(lib().msamp_checkpoint_load(out.shape[0], out.shape[1], c, p, ld, d, _stream(out.device)))
+    dev, d, shape = _leading(out, "out")
+    p, ld = _matrix(out, "out", dev, out.dtype, shape, True)
+    c = _checkpoint(ckpt, "ckpt")._arg("ckpt", dev, shape)
+    _run(dev, lib().msamp_checkpoint_load, shape[0], shape[1], c, p, ld, d)
 
 
-def _norm_weights(weight, bias, device, dtype, cols: int):
+def _norm_weights(weight, bias, device: int, dtype, cols: int):
     """(weight pointer, bias pointer, their dtype)."""
     wdt = dtype
     for t in (bias, weight):
         if t is not None:
+            _device_of(t, "weight and bias")
             wdt = t.dtype
-    if wdt not in (dtype, torch.float32):
+    if wdt != dtype and wdt != torch.float32:
         raise TypeError("weight and bias must be %s or float32" % dtype)
     w = None if weight is None else _vector(weight, "weight", device, wdt, cols)
     b = None if bias is None else _vector(bias, "bias", device, wdt, cols)
@@ -927,18 +947,15 @@ def layernorm_forward(x, weight, bias, y: torch.Tensor, mean, rstd: torch.Tensor
     x is a matrix of y's dtype, or a Checkpoint, which is read in its place
     (to form y again in a backward pass). save: a Checkpoint that receives x
     in the same pass."""
-    d = _dtype_of(y, "y")
-    dev, shape = y.device, y.shape
+    dev, d, shape = _leading(y, "y")
     rows, cols = shape
     py, ldy = _matrix(y, "y", dev, y.dtype, shape, True)
     px, ldx, ck = _input(x, dev, y.dtype, shape)
     w, b, wd = _norm_weights(weight, bias, dev, y.dtype, cols)
     m = None if mean is None else _vector(mean, "mean", dev, torch.float32, rows)
     r = _vector(rstd, "rstd", dev, torch.float32, rows)
-    sv = None if save is None else save._arg("save", dev, shape, True)
-    with torch.cuda.device(dev):
-        _check(lib().msamp_layernorm_forward(rows, cols, px, ldx, ck, d, w, b, wd, py, ldy, m, r, float(eps), sv,
-                                             _stream(dev)))
+    sv = None if save is None else _checkpoint(save, "save")._arg("save", dev, shape, True)
+    _run(dev, lib().msamp_layernorm_forward, rows, cols, px, ldx, ck, d, w, b, wd, py, ldy, m, r, eps, sv)
 
 
 def layernorm_backward(dy: torch.Tensor, x, weight, mean, rstd: torch.Tensor, dx: torch.Tensor, dweight, dbias,
@@ -947,8 +964,7 @@ def layernorm_backward(dy: torch.Tensor, x, weight, mean, rstd: torch.Tensor, dx
     Checkpoint saved there), mean and rstd: dx of dy's dtype; dweight and
     dbias in float32, either may be None; accumulate adds them to what is
     there."""
-    d = _dtype_of(dy, "dy")
-    dev, shape = dy.device, dy.shape
+    dev, d, shape = _leading(dy, "dy")
     rows, cols = shape
     pdy, lddy = _matrix(dy, "dy", dev, dy.dtype, shape)
     px, ldx, ck = _input(x, dev, dy.dtype, shape)
@@ -958,14 +974,12 @@ def layernorm_backward(dy: torch.Tensor, x, weight, mean, rstd: torch.Tensor, dx
     pdx, lddx = _matrix(dx, "dx", dev, dy.dtype, shape, True)
     dw = None if dweight is None else _vector(dweight, "dweight", dev, torch.float32, cols)
     db = None if dbias is None else _vector(dbias, "dbias", dev, torch.float32, cols)
-    with torch.cuda.device(dev):
-        n, ws = 0, None
-        if dw is not None or db is not None:
-            n = _workspace_bytes(lib().msamp_layernorm_backward_workspace(rows, cols))
-            ws = _workspace(n, dev)
-        _check(lib().msamp_layernorm_backward(rows, cols, pdy, lddy, px, ldx, ck, d, w, wd, m, r, pdx, lddx, dw, db,
-                                              int(bool(accumulate)), None if ws is None else ws.data_ptr(), n,
-                                              _stream(dev)))
+    n, ws = 0, None
+    if dw is not None or db is not None:
+        n = _workspace_bytes(lib().msamp_layernorm_backward_workspace(rows, cols))
+        ws = _workspace(n, dev)
+    _run(dev, lib().msamp_layernorm_backward, rows, cols, pdy, lddy, px, ldx, ck, d, w, wd, m, r, pdx, lddx, dw, db,
+         1 if accumulate else 0, None if ws is None else ws.data_ptr(), n)
 
 
 def _workspace_bytes(n: int) -> int:
@@ -974,13 +988,13 @@ def _workspace_bytes(n: int) -> int:
     return n
 
 
-def _workspace(n: int, device):
-    """n bytes that belong to the current stream (and to the graph that is
-    being captured on it, if any)."""
+def _workspace(n: int, device: int):
+    """n bytes that belong to the device's current stream (and to the graph
+    that is being captured on it, if any)."""
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
-def _gated_ffn(x, w_gate, w_up, act: str, dev, dt, tokens: int) -> _GatedFfn:
+def _gated_ffn(x, w_gate, w_up, act: str, dev: int, dt, tokens: int) -> _GatedFfn:
     if act not in ACTIVATIONS:
         raise ValueError("act must be one of %s" % ", ".join(ACTIVATIONS))
     if dt not in (torch.float16, torch.bfloat16):
@@ -1007,16 +1021,15 @@ def gated_ffn_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     and the product in one kernel. x [tokens, hidden], w_gate and w_up [ffn,
     hidden], h [tokens, ffn], all float16 or all bfloat16; act is "silu",
     "gelu" or "gelu_tanh". Nothing else is kept: gated_ffn_backward takes x."""
-    _dtype_of(h, "h")
-    dev, dt = h.device, h.dtype
+    dev, _, _ = _leading(h, "h")
+    dt = h.dtype
     a = _gated_ffn(x, w_gate, w_up, act, dev, dt, h.shape[0])
     a.h, a.ldh = _matrix(h, "h", dev, dt, (a.tokens, a.ffn), True)
     if a.x_ckpt:
         raise TypeError("the forward pass takes x itself, not a checkpoint")
-    with torch.cuda.device(dev):
-        n = _workspace_bytes(lib().msamp_gated_ffn_forward_workspace(ctypes.byref(a)))
-        ws = _workspace(n, dev)
-        _check(lib().msamp_gated_ffn_forward(ctypes.byref(a), None if ws is None else ws.data_ptr(), n, _stream(dev)))
+    n = _workspace_bytes(lib().msamp_gated_ffn_forward_workspace(a))
+    ws = _workspace(n, dev)
+    _run(dev, lib().msamp_gated_ffn_forward, a, None if ws is None else ws.data_ptr(), n)
 
 
 def gated_ffn_backward(dh: torch.Tensor, x, w_gate: torch.Tensor, w_up: torch.Tensor, dx: torch.Tensor,
@@ -1027,8 +1040,8 @@ def gated_ffn_backward(dh: torch.Tensor, x, w_gate: torch.Tensor, w_up: torch.Te
     float32 (what amax and the quantizing steps take; accumulate adds to what
     is there) or of the weights' dtype. h, if given, receives the forward
     pass's product again (the next projection's gradient needs it)."""
-    _dtype_of(dh, "dh")
-    dev, dt = dh.device, dh.dtype
+    dev, _, _ = _leading(dh, "dh")
+    dt = dh.dtype
     a = _gated_ffn(x, w_gate, w_up, act, dev, dt, dh.shape[0])
     rows, k, f = a.tokens, a.hidden, a.ffn
     a.dh, a.lddh = _matrix(dh, "dh", dev, dt, (rows, f))
@@ -1043,11 +1056,9 @@ def gated_ffn_backward(dh: torch.Tensor, x, w_gate: torch.Tensor, w_up: torch.Te
     a.dw_gate, a.ld_dw_gate = _matrix(dw_gate, "dw_gate", dev, wdt, (f, k), True)
     a.dw_up, a.ld_dw_up = _matrix(dw_up, "dw_up", dev, wdt, (f, k), True)
     a.dw_dtype, a.dw_accumulate = _DTYPES[wdt], int(bool(accumulate))
-    with torch.cuda.device(dev):
-        n = _workspace_bytes(lib().msamp_gated_ffn_backward_workspace(ctypes.byref(a)))
-        ws = _workspace(n, dev)
-        _check(lib().msamp_gated_ffn_backward(ctypes.byref(a), None if ws is None else ws.data_ptr(), n,
-                                              _stream(dev)))
+    n = _workspace_bytes(lib().msamp_gated_ffn_backward_workspace(a))
+    ws = _workspace(n, dev)
+    _run(dev, lib().msamp_gated_ffn_backward, a, None if ws is None else ws.data_ptr(), n)
 
 
 # ----------------------------------------------------------- state helpers ---

@@ -153,6 +153,18 @@ __device__ __forceinline__ float clamp_finite(float v, float lim) {
   return __builtin_isnan(v) ? v : c;
 }
 
+// The values of eight codes with their group's scale byte.
+__device__ __forceinline__ void decode_group8(int fmt, u32x2 q, uint32_t b, float* f) {
+  if (fmt == kE4M3) dec8<kE4M3>(q, f); else dec8<kE5M2>(q, f);
+  const float s = __uint_as_float(b << 23);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] *= s;
+  if (b >= 127u + 112u) {  // 57344 * 2^112 and above may leave binary32
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = clamp_finite(f[k], kF32Max);
+  }
+}
+
 // n (<= 8) values of a checkpoint's row from column col; zeros behind them.
 __device__ __forceinline__ void load_ckpt8(int fmt, const uint8_t* codes, const uint8_t* scales, int64_t col, int n,
                                            float* f) {
@@ -167,14 +179,7 @@ __device__ __forceinline__ void load_ckpt8(int fmt, const uint8_t* codes, const 
     }
   }
   if (n > 0) b = ((const GLOBAL uint8_t*)scales)[col / kGroup];
-  if (fmt == kE4M3) dec8<kE4M3>(q, f); else dec8<kE5M2>(q, f);
-  const float s = __uint_as_float(b << 23);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] *= s;
-  if (b >= 127u + 112u) {  // 57344 * 2^112 and above may leave binary32
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = clamp_finite(f[k], kF32Max);
-  }
+  decode_group8(fmt, q, b, f);
 }
 
 }  // namespace msamp
