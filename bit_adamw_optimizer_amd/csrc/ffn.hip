@@ -10,6 +10,7 @@
 namespace msamp {
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -85,6 +86,8 @@ __device__ __forceinline__ void act_and_grad(int act, float g, float* a, float* 
 // comparison in the last step along k), so ragged sizes need no other path.
 
 enum Mode { kForward, kRecompute, kDx, kDw };
+// Modes whose tile is a pair, gate and up of the same 128 inner units.
+constexpr bool is_pair(int mode) { return mode == kForward || mode == kRecompute; }
 
 struct Product {
   int64_t R, C, K;  // output rows and columns (inner units for kForward, kRecompute), sum length of a pass
@@ -93,6 +96,11 @@ struct Product {
   const void *c0, *c1;  // c1: up weights
   int64_t ldc0, ldc1;
   uint32_t tiles_r, tiles_c;
+  // The sum over k in 'splits' parts of 'part' steps each: their sums go to
+  // 'partial', one tile after another, and are joined by k_product_sum.
+  uint32_t splits;
+  int64_t part;
+  float* partial;
   int act;
   void *out0, *out1;  // h or dx; dw_gate and dw_up
   int64_t ldo0, ldo1;
@@ -177,18 +185,27 @@ __device__ __forceinline__ typename Frag<T>::type across_frag(const LDS char* ld
   return __builtin_bit_cast(typename Frag<T>::type, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Where a workgroup's tile lies. Workgroups go to the 8 XCDs in turn; each XCD
-// gets a contiguous run of tiles, in blocks of 8 tiles along r, so that the 32
-// tiles it works on at a time share 8 row tiles and 4 column tiles in its L2.
-__device__ __forceinline__ void tile_of(const Product& p, uint32_t id, uint32_t* tr, uint32_t* tc) {
-  const uint32_t n = p.tiles_r * p.tiles_c;
+// Where a workgroup's tile lies: unit 'id' of 'n'. Workgroups go to the 8 XCDs
+// in turn; each XCD gets a contiguous run of units, in blocks of 8 tiles along
+// r, so that the 32 tiles it works on at a time share 8 row tiles and 4 column
+// tiles in its L2.
+struct Place {
+  uint32_t tr, tc, part, z, unit;
+};
+__device__ __forceinline__ Place place_of(const Product& p, uint32_t id, uint32_t n) {
+  Place q;
+  const uint32_t tiles = p.tiles_r * p.tiles_c;
   const uint32_t xcd = id & 7, i = id >> 3, full = n >> 3, rest = n & 7;
-  const uint32_t t = xcd * full + (xcd < rest ? xcd : rest) + i;
+  q.unit = xcd * full + (xcd < rest ? xcd : rest) + i;
+  const uint32_t zs = q.unit / tiles, t = q.unit - zs * tiles;
+  q.z = zs / p.splits;
+  q.part = zs - q.z * p.splits;
   const uint32_t per = 8 * p.tiles_c;
   const uint32_t g = t / per, in = t - g * per;
   const uint32_t rows = p.tiles_r - g * 8 < 8 ? p.tiles_r - g * 8 : 8;
-  *tc = in / rows;
-  *tr = g * 8 + (in - *tc * rows);
+  q.tc = in / rows;
+  q.tr = g * 8 + (in - q.tc * rows);
+  return q;
 }
 
 // The accumulators of a wave: FR blocks of 32 rows by 2 blocks of 32 columns
@@ -202,10 +219,10 @@ template <typename T, int MODE, int FR>
 __device__ __forceinline__ void step(const Product& p, const LDS char* __restrict__ rd, LDS char* __restrict__ wr,
                                      const Along<FR>& ra, const Across<FR>& rx, const Along<4>& ca,
                                      const Across<4>& cx, int64_t row0, int64_t col0, int z, int wave, int lane,
-                                     int64_t next, int64_t steps1, int64_t steps, bool compute, Acc<FR>& acc) {
-  constexpr bool kPair = MODE == kForward || MODE == kRecompute;
+                                     int64_t next, int64_t steps1, int64_t end, bool compute, Acc<FR>& acc) {
+  constexpr bool kPair = is_pair(MODE);
   constexpr int kTileBytesR = FR * 64 * 128;
-  if (next < steps) {
+  if (next < end) {
     const bool second = MODE == kDx && next >= steps1;
     const int64_t k0 = (second ? next - steps1 : next) * kStepK;
     const int64_t left = p.K - k0;
@@ -401,7 +418,6 @@ __device__ __forceinline__ void finish(const Product& p, LDS char* lds, int64_t 
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int col = lcol + 32 * c + 8 * q;
-            typedef float f32x4 __attribute__((ext_vector_type(4)));
             typedef f32x4 f32x4_any __attribute__((aligned(4)));
             if (row < rows && col + 4 <= cols) {
               f32x4 v;
@@ -439,15 +455,14 @@ __device__ __forceinline__ void finish(const Product& p, LDS char* lds, int64_t 
 
 template <typename T, int MODE, int FR>
 __global__ __launch_bounds__(kThreads) void k_product(Product p) {
-  constexpr bool kPair = MODE == kForward || MODE == kRecompute;
+  constexpr bool kPair = is_pair(MODE);
   constexpr int kStage = FR * 64 * 128 + kTileC * 128;
   __shared__ __attribute__((aligned(16))) char smem[2 * kStage];  // also holds the outgoing tiles
   LDS char* lds = (LDS char*)smem;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  uint32_t tr, tc;
-  const int z = MODE == kDw ? (int)blockIdx.y : 0;
-  tile_of(p, blockIdx.x, &tr, &tc);
-  const int64_t row0 = (int64_t)tr * (64 * FR), col0 = (int64_t)tc * (kPair ? 128 : 256);
+  const Place at = place_of(p, blockIdx.x, gridDim.x);
+  const int z = MODE == kDw ? (int)at.z : 0;
+  const int64_t row0 = (int64_t)at.tr * (64 * FR), col0 = (int64_t)at.tc * (kPair ? 128 : 256);
   Along<FR> ra;
   Across<FR> rx;
   Along<4> ca;
@@ -468,30 +483,280 @@ __global__ __launch_bounds__(kThreads) void k_product(Product p) {
   for (int r = 0; r < FR; ++r) acc.v[r][0] = acc.v[r][1] = f32x16{};
   const int64_t steps1 = (p.K + kStepK - 1) / kStepK;
   const int64_t steps = MODE == kDx ? 2 * steps1 : steps1;
-  step<T, MODE, FR>(p, lds + kStage, lds, ra, rx, ca, cx, row0, col0, z, wave, lane, 0, steps1, steps, false, acc);
+  const int64_t begin = (int64_t)at.part * p.part;
+  const int64_t end = steps < begin + p.part ? steps : begin + p.part;
+  step<T, MODE, FR>(p, lds + kStage, lds, ra, rx, ca, cx, row0, col0, z, wave, lane, begin, steps1, end, false, acc);
   __syncthreads();
-  for (int64_t i = 0; i < steps; ++i) {
-    const int at = (int)(i & 1) * kStage;
-    step<T, MODE, FR>(p, lds + at, lds + (kStage - at), ra, rx, ca, cx, row0, col0, z, wave, lane, i + 1, steps1,
-                      steps, true, acc);
+  for (int64_t i = begin; i < end; ++i) {
+    const int cur = (int)((i - begin) & 1) * kStage;
+    step<T, MODE, FR>(p, lds + cur, lds + (kStage - cur), ra, rx, ca, cx, row0, col0, z, wave, lane, i + 1, steps1,
+                      end, true, acc);
     __syncthreads();
+  }
+  if (p.splits > 1) {
+    f32x4* o = (f32x4*)p.partial + (int64_t)at.unit * (64 * FR * kTileC / 4) + wave * (FR * 2 * 4 * 64) + lane;
+    const int lrow = (wave >> 2) * (32 * FR) + (lane & 31);
+#pragma unroll
+    for (int r = 0; r < FR; ++r)
+      if (row0 + lrow + 32 * r < p.R) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc.v[r][c][q * 4 + e];
+            o[((r * 2 + c) * 4 + q) * 64] = v;
+          }
+      }
+    return;
   }
   finish<T, MODE, FR>(p, lds, row0, col0, z, wave, lane, acc);
 }
 
+// Joins the parts of a split sum, in their order, and finishes the tile.
 template <typename T, int MODE, int FR>
-hipError_t launch_tiles(Product p, hipStream_t s) {
-  p.tiles_r = (uint32_t)((p.R + 64 * FR - 1) / (64 * FR));
-  const int tc = MODE == kForward || MODE == kRecompute ? 128 : 256;
-  p.tiles_c = (uint32_t)((p.C + tc - 1) / tc);
-  const dim3 g(p.tiles_r * p.tiles_c, MODE == kDw ? 2 : 1);
-  k_product<T, MODE, FR><<<g, dim3(kThreads), 0, s>>>(p);
+__global__ __launch_bounds__(kThreads) void k_product_sum(Product p) {
+  constexpr bool kPair = is_pair(MODE);
+  __shared__ __attribute__((aligned(16))) char smem[64 * FR * 512];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  Product one = p;
+  one.splits = 1;
+  const Place at = place_of(one, blockIdx.x, gridDim.x);
+  const int z = MODE == kDw ? (int)at.z : 0;
+  const int64_t row0 = (int64_t)at.tr * (64 * FR), col0 = (int64_t)at.tc * (kPair ? 128 : 256);
+  const uint32_t tiles = p.tiles_r * p.tiles_c;
+  const int64_t tile = at.unit - at.z * tiles;
+  Acc<FR> acc;
+#pragma unroll
+  for (int r = 0; r < FR; ++r) acc.v[r][0] = acc.v[r][1] = f32x16{};
+  const int lrow = (wave >> 2) * (32 * FR) + (lane & 31);
+  for (uint32_t part = 0; part < p.splits; ++part) {
+    const int64_t unit = ((int64_t)at.z * p.splits + part) * tiles + tile;
+    const f32x4* o = (const f32x4*)p.partial + unit * (64 * FR * kTileC / 4) + wave * (FR * 2 * 4 * 64) + lane;
+#pragma unroll
+    for (int r = 0; r < FR; ++r)
+      if (row0 + lrow + 32 * r < p.R) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 v = o[((r * 2 + c) * 4 + q) * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc.v[r][c][q * 4 + e] += v[e];
+          }
+      }
+  }
+  finish<T, MODE, FR>(p, (LDS char*)smem, row0, col0, z, wave, lane, acc);
+}
+
+// How a product is cut: rows of a tile (64 * fr) and parts of the sum over k.
+struct Cut {
+  int fr;
+  uint32_t tiles_r, tiles_c, splits;
+  int64_t part;
+  int64_t partial_bytes;
+};
+
+// The cut with the least estimated time. A compute unit takes about 0.35 us
+// for what a step does whatever its tile (the column operand's 32 KB, the
+// barrier) and 0.35 us for each 64 rows; a tile costs 4 us to start and to
+// finish; joining parts costs a launch and one pass over them.
+Cut choose_cut(int mode, int64_t R, int64_t C, int64_t K) {
+  Cut best = {};
+  double least = 1e30;
+  const int64_t steps = (K + kStepK - 1) / kStepK * (mode == kDx ? 2 : 1);
+  const int tc = is_pair(mode) ? 128 : 256;
+  const int64_t nc = (C + tc - 1) / tc, zs = mode == kDw ? 2 : 1;
+  for (int fr = 4; fr >= 1; fr /= 2) {
+    const int64_t nr = (R + 64 * fr - 1) / (64 * fr), tiles = nr * nc * zs;
+    const double step_us = 0.35 + 0.35 * fr;
+    const int64_t slots = 256;
+    for (int64_t splits = 1; splits <= 64 && (splits == 1 || steps / splits >= 2); ++splits) {
+      const int64_t part = (steps + splits - 1) / splits;
+      const int64_t used = (steps + part - 1) / part;
+      if (used != splits) continue;
+      const int64_t rounds = (tiles * splits + slots - 1) / slots;
+      const int64_t bytes = splits == 1 ? 0 : tiles * splits * (64 * fr * kTileC * 4);
+      if (bytes > (int64_t)1 << 30) break;
+      const double t = rounds * (part * step_us + 4.0) + (splits == 1 ? 0.0 : 6.0 + bytes * 2 / 4e6);
+      if (t < least) {
+        least = t;
+        best = {fr, (uint32_t)nr, (uint32_t)nc, (uint32_t)splits, part, bytes};
+      }
+      if (splits > 1 && rounds > 4) break;
+    }
+  }
+  return best;
+}
+
+template <typename T, int MODE, int FR>
+hipError_t launch_tiles(const Product& p, bool sum, hipStream_t s) {
+  const uint32_t tiles = p.tiles_r * p.tiles_c * (MODE == kDw ? 2 : 1);
+  if (sum) k_product_sum<T, MODE, FR><<<dim3(tiles), dim3(kThreads), 0, s>>>(p);
+  else k_product<T, MODE, FR><<<dim3(tiles * p.splits), dim3(kThreads), 0, s>>>(p);
   return hipGetLastError();
 }
 
 template <int MODE>
-hipError_t launch_product(int dtype, const Product& p, hipStream_t s) {
-  return dtype == MSAMP_F16 ? launch_tiles<f16, MODE, 4>(p, s) : launch_tiles<bf16, MODE, 4>(p, s);
+hipError_t launch_product(int dtype, int fr, const Product& p, bool sum, hipStream_t s) {
+  if (dtype == MSAMP_F16)
+    return fr == 4 ? launch_tiles<f16, MODE, 4>(p, sum, s)
+                   : (fr == 2 ? launch_tiles<f16, MODE, 2>(p, sum, s) : launch_tiles<f16, MODE, 1>(p, sum, s));
+  return fr == 4 ? launch_tiles<bf16, MODE, 4>(p, sum, s)
+                 : (fr == 2 ? launch_tiles<bf16, MODE, 2>(p, sum, s) : launch_tiles<bf16, MODE, 1>(p, sum, s));
+}
+
+// Hands out pieces of the workspace (or only counts them).
+struct Arena {
+  char* base;
+  int64_t used = 0;
+  void* take(int64_t bytes) {
+    if (bytes == 0) return nullptr;
+    void* p = base == nullptr ? nullptr : base + used;
+    used += (bytes + 255) / 256 * 256;
+    return p;
+  }
+};
+
+// Plans a product (taking its partial sums' workspace) and runs it.
+template <int MODE>
+msamp_status product(msamp_kernel_kind kind, int dtype, Product p, Arena& ws, bool run, hipStream_t s) {
+  const Cut c = choose_cut(MODE, p.R, p.C, p.K);
+  if ((int64_t)c.tiles_r * c.tiles_c * c.splits * 2 > (int64_t)UINT32_MAX / kThreads)
+    return fail(MSAMP_E_INVALID_ARG, "the product has too many tiles");
+  p.tiles_r = c.tiles_r, p.tiles_c = c.tiles_c, p.splits = c.splits, p.part = c.part;
+  p.partial = (float*)ws.take(c.partial_bytes);
+  if (!run) return MSAMP_OK;
+  MSAMP_LAUNCH(kind, s, launch_product<MODE>(dtype, c.fr, p, false, s));
+  if (c.splits > 1) MSAMP_LAUNCH(MSAMP_KERNEL_FFN_REDUCE, s, launch_product<MODE>(dtype, c.fr, p, true, s));
+  return MSAMP_OK;
+}
+
+// -------------------------------------------------------------- few rows ---
+//
+// Up to 64 tokens the gate and up projections are bound by reading the
+// weights, each once. A workgroup forms 16 inner units for all tokens; its 8
+// waves share the sum over k and read their parts of the 32 weight rows
+// straight into the operands of 16x16x32 MFMA, 128 bytes of every row at a
+// time (k is taken in the order of the bytes a lane holds, the same for x), so
+// no LDS and no barrier stand between the loads. The waves' sums are joined
+// through LDS.
+
+template <typename T>
+struct Frag16;
+template <>
+struct Frag16<f16> {
+  static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+  }
+};
+template <>
+struct Frag16<bf16> {
+  static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+};
+
+constexpr int kFewRows = 64;
+
+template <typename T, int MODE, int NT>
+__global__ __launch_bounds__(kThreads) void k_few_rows(Product p) {
+  constexpr int kUnroll = NT == 1 ? 4 : 2;
+  __shared__ f32x4 sums[8][NT][2][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t col0 = (int64_t)blockIdx.x * 16;
+  // rows of this block's weights that exist (none: columns that pad dg | du)
+  const int64_t left = p.C - col0, cols = left < 0 ? 0 : (left < 16 ? left : 16);
+  const auto bg = buffer_of((const T*)p.c0 + col0 * p.ldc0, cols == 0 ? 0 : ((cols - 1) * p.ldc0 + round8(p.K)) * 2);
+  const auto bu = buffer_of((const T*)p.c1 + col0 * p.ldc1, cols == 0 ? 0 : ((cols - 1) * p.ldc1 + round8(p.K)) * 2);
+  const auto bx = buffer_of(p.r0, ((p.R - 1) * p.ldr + round8(p.K)) * 2);
+  const int piece = (lane >> 4) * 16;  // this lane's 16 k of a chunk of 64
+  const int og = (int)((lane & 15) * p.ldc0 * 2) + piece * 2, ou = (int)((lane & 15) * p.ldc1 * 2) + piece * 2;
+  int ox[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) ox[t] = (int)(((lane & 15) + 16 * t) * p.ldr * 2) + piece * 2;
+  f32x4 acc[NT][2] = {};
+  const int chunks = (int)((p.K + 63) / 64);
+  for (int i = wave; i < chunks; i += 8 * kUnroll) {
+    u32x4 g[kUnroll][2], u[kUnroll][2], x[kUnroll][NT][2];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int k0 = (i + 8 * j) * 64;
+      const int64_t rest = p.K - k0 - piece;  // k of this lane that exist
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool in = rest > 8 * h;
+        g[j][h] = __builtin_amdgcn_raw_buffer_load_b128(bg, in ? og + k0 * 2 + 16 * h : kOutside, 0, 0);
+        u[j][h] = __builtin_amdgcn_raw_buffer_load_b128(bu, in ? ou + k0 * 2 + 16 * h : kOutside, 0, 0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          x[j][t][h] = __builtin_amdgcn_raw_buffer_load_b128(bx, in ? ox[t] + k0 * 2 + 16 * h : kOutside, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          acc[t][0] = Frag16<T>::mma(g[j][h], x[j][t][h], acc[t][0]);
+          acc[t][1] = Frag16<T>::mma(u[j][h], x[j][t][h], acc[t][1]);
+        }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    sums[wave][t][0][lane] = acc[t][0];
+    sums[wave][t][1][lane] = acc[t][1];
+  }
+  __syncthreads();
+  // element e of sums[..][lane]: inner unit 4 * (lane / 16) + e, token lane % 16
+  for (int i = threadIdx.x; i < NT * 256; i += kThreads) {
+    const int t = i / 256, token = (i / 16) & 15, unit = i & 15;
+    const int64_t row = 16 * t + token, col = col0 + unit;
+    if (row >= p.R) continue;
+    const int from = (unit >> 2) * 16 + token;
+    float g = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      g += sums[w][t][0][from][unit & 3];
+      u += sums[w][t][1][from][unit & 3];
+    }
+    float a, d;
+    act_and_grad(p.act, g, &a, &d);
+    if (col < p.C && p.out0 != nullptr) ((GLOBAL T*)p.out0)[row * p.ldo0 + col] = from_f32<T>(a * u);
+    if constexpr (MODE == kRecompute) {
+      const float dh = col < p.C ? to_f32(((const GLOBAL T*)p.dh)[row * p.lddh + col]) : 0.0f;
+      GLOBAL T* o = (GLOBAL T*)p.dgu + row * (2 * p.half) + col;
+      o[0] = from_f32<T>(dh * u * d);
+      o[p.half] = from_f32<T>(dh * a);
+    }
+  }
+}
+
+template <typename T, int MODE>
+hipError_t launch_few_rows(const Product& p, hipStream_t s) {
+  const int64_t cols = MODE == kRecompute ? p.half : p.C;
+  const dim3 g((unsigned)((cols + 15) / 16));
+  if (p.R <= 16) k_few_rows<T, MODE, 1><<<g, dim3(kThreads), 0, s>>>(p);
+  else if (p.R <= 32) k_few_rows<T, MODE, 2><<<g, dim3(kThreads), 0, s>>>(p);
+  else k_few_rows<T, MODE, 4><<<g, dim3(kThreads), 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <int MODE>
+hipError_t launch_few(int dtype, const Product& p, hipStream_t s) {
+  return dtype == MSAMP_F16 ? launch_few_rows<f16, MODE>(p, s) : launch_few_rows<bf16, MODE>(p, s);
+}
+
+// The gate and up projections by the kernel that suits the number of tokens.
+template <int MODE>
+msamp_status projections(msamp_kernel_kind kind, int dtype, const Product& p, Arena& ws, bool run, hipStream_t s) {
+  if (p.R > kFewRows) return product<MODE>(kind, dtype, p, ws, run, s);
+  if (run) MSAMP_LAUNCH(kind, s, launch_few<MODE>(dtype, p, s));
+  return MSAMP_OK;
 }
 
 // ---------------------------------------------------------------- layout ---
@@ -530,7 +795,6 @@ hipError_t launch_layout(int dtype, int64_t rows, int64_t cols, const void* src,
 
 // ------------------------------------------------------------------ plan ---
 
-int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 int64_t round64(int64_t n) { return (n + 63) / 64 * 64; }
 
 // Whether the matrix kernels can read an operand where it lies: 16-byte
@@ -539,17 +803,6 @@ int64_t round64(int64_t n) { return (n + 63) / 64 * 64; }
 bool direct(const void* p, int64_t ld, int64_t cols) {
   return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0 && cols % 8 == 0 && ld >= cols && ld < (1 << 22);
 }
-
-// Hands out pieces of the workspace (or only counts them).
-struct Arena {
-  char* base;
-  int64_t used = 0;
-  void* take(int64_t bytes) {
-    void* p = base == nullptr ? nullptr : base + used;
-    used += round256(bytes);
-    return p;
-  }
-};
 
 struct Operand {
   const void* p;
@@ -602,15 +855,13 @@ msamp_status forward(const msamp_gated_ffn& a, Arena& ws, bool run, hipStream_t 
   MSAMP_TRY(lay_out(a.dtype, a.tokens, a.hidden, a.x, a.ldx, nullptr, ws, run, s, &x));
   MSAMP_TRY(lay_out(a.dtype, a.ffn, a.hidden, a.w_gate, a.ld_gate, nullptr, ws, run, s, &g));
   MSAMP_TRY(lay_out(a.dtype, a.ffn, a.hidden, a.w_up, a.ld_up, nullptr, ws, run, s, &u));
-  if (!run) return MSAMP_OK;
   Product p = {};
   p.R = a.tokens, p.C = a.ffn, p.K = a.hidden;
   p.r0 = x.p, p.ldr = x.ld;
   p.c0 = g.p, p.ldc0 = g.ld, p.c1 = u.p, p.ldc1 = u.ld;
   p.act = a.act;
   p.out0 = a.h, p.ldo0 = a.ldh;
-  MSAMP_LAUNCH(MSAMP_KERNEL_FFN_FORWARD, s, launch_product<kForward>(a.dtype, p, s));
-  return MSAMP_OK;
+  return projections<kForward>(MSAMP_KERNEL_FFN_FORWARD, a.dtype, p, ws, run, s);
 }
 
 msamp_status backward(const msamp_gated_ffn& a, Arena& ws, bool run, hipStream_t s) {
@@ -629,8 +880,7 @@ msamp_status backward(const msamp_gated_ffn& a, Arena& ws, bool run, hipStream_t
   MSAMP_TRY(lay_out(a.dtype, F, K, a.w_up, a.ld_up, nullptr, ws, run, s, &u));
   const int64_t half = round64(F);
   if (2 * half >= (1 << 22)) return fail(MSAMP_E_INVALID_ARG, "ffn exceeds 2^21 - 64");
-  char* dgu = (char*)ws.take(T * 2 * half * 2);
-  if (!run) return MSAMP_OK;
+  char* dgu = (char*)ws.take(T * 2 * half * 2);  // null while only counting
   Product p = {};
   p.R = T, p.C = F, p.K = K;
   p.r0 = x.p, p.ldr = x.ld;
@@ -639,22 +889,30 @@ msamp_status backward(const msamp_gated_ffn& a, Arena& ws, bool run, hipStream_t
   p.out0 = a.h, p.ldo0 = a.ldh;
   p.dh = a.dh, p.lddh = a.lddh;
   p.dgu = dgu, p.half = half;
-  MSAMP_LAUNCH(MSAMP_KERNEL_FFN_RECOMPUTE, s, launch_product<kRecompute>(a.dtype, p, s));
+  // the three products' partial sums take turns in the same memory
+  const int64_t mark = ws.used;
+  int64_t most = mark;
+  MSAMP_TRY(projections<kRecompute>(MSAMP_KERNEL_FFN_RECOMPUTE, a.dtype, p, ws, run, s));
+  most = ws.used > most ? ws.used : most;
+  ws.used = mark;
 
   p = {};
   p.R = T, p.C = K, p.K = F;
-  p.r0 = dgu, p.r1 = dgu + half * 2, p.ldr = 2 * half;
+  p.r0 = dgu, p.r1 = run ? dgu + half * 2 : nullptr, p.ldr = 2 * half;
   p.c0 = g.p, p.ldc0 = g.ld, p.c1 = u.p, p.ldc1 = u.ld;
   p.out0 = a.dx, p.ldo0 = a.lddx;
-  MSAMP_LAUNCH(MSAMP_KERNEL_FFN_DX, s, launch_product<kDx>(a.dtype, p, s));
+  MSAMP_TRY(product<kDx>(MSAMP_KERNEL_FFN_DX, a.dtype, p, ws, run, s));
+  most = ws.used > most ? ws.used : most;
+  ws.used = mark;
 
   p = {};
   p.R = F, p.C = K, p.K = T;
-  p.r0 = dgu, p.r1 = dgu + half * 2, p.ldr = 2 * half;
+  p.r0 = dgu, p.r1 = run ? dgu + half * 2 : nullptr, p.ldr = 2 * half;
   p.c0 = x.p, p.ldc0 = x.ld;
   p.out0 = a.dw_gate, p.ldo0 = a.ld_dw_gate, p.out1 = a.dw_up, p.ldo1 = a.ld_dw_up;
   p.out_f32 = a.dw_dtype == MSAMP_F32, p.accumulate = a.dw_accumulate;
-  MSAMP_LAUNCH(MSAMP_KERNEL_FFN_DW, s, launch_product<kDw>(a.dtype, p, s));
+  MSAMP_TRY(product<kDw>(MSAMP_KERNEL_FFN_DW, a.dtype, p, ws, run, s));
+  ws.used = ws.used > most ? ws.used : most;
   return MSAMP_OK;
 }
 

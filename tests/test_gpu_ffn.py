@@ -280,3 +280,30 @@ def test_in_a_graph_and_on_another_stream():
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, outs))
+
+
+# sizes that are cut in each way: tiles of 64, 128 and 256 rows, sums over k in one part and in several
+@pytest.mark.parametrize("t,k,f,dtype,act", [(70, 2600, 200, "f16", "silu"), (1500, 200, 130, "bf16", "silu"),
+                                             (200, 130, 2100, "f16", "gelu"), (300, 264, 9000, "bf16", "gelu_tanh"),
+                                             (2050, 264, 4100, "bf16", "silu"), (64, 1500, 1030, "f16", "silu"),
+                                             (33, 520, 270, "bf16", "gelu"), (2500, 1100, 1300, "f16", "silu")])
+def test_every_cut(t, k, f, dtype, act):
+    dt = DT[dtype]
+    x, wg, wu, dh = problem(t, k, f, dt, seed=t + k)
+    val, err = R.ffn(x.cpu(), wg.cpu(), wu.cpu(), act, dh.cpu(), dt)
+    buf, h = out(t, f, dt)
+    M.gated_ffn_forward(x, wg, wu, h, act=act)
+    assert untouched(buf, t, f)
+    check(["h"], {"h": h}, val, err, dt)
+    for wide in (False, True):
+        bufs = {"h": out(t, f, dt), "dx": out(t, k, dt), "dw_gate": out(f, k, torch.float32 if wide else dt),
+                "dw_up": out(f, k, torch.float32 if wide else dt)}
+        got = {n: v[1] for n, v in bufs.items()}
+        M.gated_ffn_backward(dh, x, wg, wu, got["dx"], got["dw_gate"], got["dw_up"], act=act, h=got["h"])
+        for n, (buf, v) in bufs.items():
+            assert untouched(buf, *v.shape), n
+        check(["h", "dx", "dw_gate", "dw_up"], got, val, err, dt)
+        if wide:  # the parts are joined in one order
+            first = {n: v.clone() for n, v in got.items()}
+            M.gated_ffn_backward(dh, x, wg, wu, got["dx"], got["dw_gate"], got["dw_up"], act=act, h=got["h"])
+            assert all(torch.equal(first[n], got[n]) for n in got)
