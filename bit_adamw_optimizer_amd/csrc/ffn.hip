@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "checkpoint.hpp"
 #include "ffn.hpp"
 
@@ -41,23 +43,36 @@ struct Frag<bf16> {
 
 // ------------------------------------------------------------ activation ---
 
-// act(g) and act'(g).
-__device__ __forceinline__ void act_and_grad(int act, float g, float* a, float* d) {
-  if (act == MSAMP_ACT_SILU) {
-    const float s = 1.0f / (1.0f + __expf(-g));
+// act(g) and act'(g). The exponential and the reciprocal are the hardware's
+// (one unit in the last place of binary32 each).
+template <int ACT>
+__device__ __forceinline__ void act_and_grad(float g, float* a, float* d) {
+  if constexpr (ACT == MSAMP_ACT_SILU) {
+    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
     *a = g * s;
-    *d = s * (1.0f + g * (1.0f - s));
-  } else if (act == MSAMP_ACT_GELU) {
+    *d = s * __builtin_fmaf(g, 1.0f - s, 1.0f);
+  } else if constexpr (ACT == MSAMP_ACT_GELU) {
     const float phi = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
     *a = g * phi;
     *d = phi + g * 0.39894228040143268f * __expf(-0.5f * g * g);
   } else {
     // (1 + tanh(z)) / 2 = 1 / (1 + e^(-2z))
-    const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
-    const float s = 1.0f / (1.0f + __expf(-z2));
+    const float g2 = g * g;
+    const float z2 = 1.5957691216057308f * __builtin_fmaf(0.044715f * g2, g, g);
+    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-z2));
     *a = g * s;
-    *d = s + g * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * g * g);
+    // far out, s (1 - s) is 0 and outweighs the slope of z, which may overflow
+    const float t = s * (1.0f - s);
+    *d = s + (t == 0.0f ? 0.0f : g * t * 1.5957691216057308f * __builtin_fmaf(0.134145f, g2, 1.0f));
   }
+}
+
+// f(std::integral_constant of the activation).
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  if (act == MSAMP_ACT_SILU) f(std::integral_constant<int, MSAMP_ACT_SILU>());
+  else if (act == MSAMP_ACT_GELU) f(std::integral_constant<int, MSAMP_ACT_GELU>());
+  else f(std::integral_constant<int, MSAMP_ACT_GELU_TANH>());
 }
 
 // -------------------------------------------------------- matrix product ---
@@ -326,82 +341,101 @@ __device__ __forceinline__ uint64_t pack4(const float* f) {
   return __builtin_bit_cast(uint64_t, v);
 }
 
+// dh of a tile as it lies in memory, 16 bytes a thread and piece: loaded
+// before the sums, so that it is there when they are.
+template <typename T, int FR>
+struct Incoming {
+  u32x4 v[64 * FR * 16 / kThreads];
+  __device__ __forceinline__ void load(const Product& p, int64_t row0, int64_t col0) {
+#pragma unroll
+    for (int k = 0; k < 64 * FR * 16 / kThreads; ++k) {
+      const int i = threadIdx.x + k * kThreads, row = i / 16, piece = i % 16;
+      const int64_t n = p.C - col0 - piece * 8;
+      v[k] = u32x4{0u, 0u, 0u, 0u};
+      if (row0 + row < p.R && n > 0) {
+        const GLOBAL T* q = (const GLOBAL T*)p.dh + (row0 + row) * p.lddh + col0 + piece * 8;
+        if (n >= 8) {
+          v[k] = *(const GLOBAL u32x4_any*)q;
+        } else {
+          typedef T t8 __attribute__((ext_vector_type(8)));
+          t8 e = __builtin_bit_cast(t8, v[k]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < n) e[j] = q[j];
+          v[k] = __builtin_bit_cast(u32x4, e);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void to_lds(LDS char* lds) const {
+#pragma unroll
+    for (int k = 0; k < 64 * FR * 16 / kThreads; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      *(LDS u32x4*)(lds + tile_piece<128>(i / 16, i % 16)) = v[k];
+    }
+  }
+};
+
 // The tile's sums to where they go.
 template <typename T, int MODE, int FR>
 __device__ __forceinline__ void finish(const Product& p, LDS char* lds, int64_t row0, int64_t col0, int z, int wave,
-                                       int lane, const Acc<FR>& acc) {
+                                       int lane, const Acc<FR>& acc, const Incoming<T, FR>& dh) {
   constexpr int kRows = 64 * FR;
   const int64_t rows = p.R - row0;
   const int lrow = (wave >> 2) * (32 * FR) + (lane & 31);  // + 32 r
   __syncthreads();  // the stages have been read
-  if constexpr (MODE == kForward || MODE == kRecompute) {
-    const int lcol = (wave & 3) * 32 + (lane >> 5) * 4;  // + 8 q + e
+  if constexpr (is_pair(MODE)) {
+    const int lcol = (wave & 3) * 32;  // + 8 q + 4 (lane / 32) + e
     LDS char* second = lds + kRows * 256;
     const int64_t cols = p.C - col0;
+    auto place = [&](int r, int q) { return tile_piece<128>(lrow + 32 * r, (lcol >> 3) + q) + (lane >> 5) * 8; };
+    uint64_t du[MODE == kRecompute ? FR : 1][4];
     if constexpr (MODE == kRecompute) {
-      for (int i = threadIdx.x; i < kRows * 16; i += kThreads) {
-        const int row = i / 16, piece = i % 16;
-        float f[8] = {};
-        const int64_t n = cols - piece * 8;
-        if (row < rows && n > 0)
-          load8((const T*)p.dh + (row0 + row) * p.lddh + col0 + piece * 8, (int)(n < 8 ? n : 8), f);
-        typedef T t8 __attribute__((ext_vector_type(8)));
-        t8 v;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = (T)f[k];
-        *(LDS u32x4*)(lds + tile_piece<128>(row, piece)) = __builtin_bit_cast(u32x4, v);
-      }
+      dh.to_lds(lds);
       __syncthreads();
     }
+    with_act(p.act, [&](auto act) {
 #pragma unroll
-    for (int r = 0; r < FR; ++r)
+      for (int r = 0; r < FR; ++r)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float a[4], d[4], g[4];
+        for (int q = 0; q < 4; ++q) {
+          float a[4], d[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) act_and_grad(p.act, acc.v[r][0][q * 4 + e], &a[e], &d[e]);
-        const int at = tile_piece<128>(lrow + 32 * r, (lcol >> 3) + q) + (lane >> 5) * 8;
-        if constexpr (MODE == kForward) {
+          for (int e = 0; e < 4; ++e) act_and_grad<decltype(act)::value>(acc.v[r][0][q * 4 + e], &a[e], &d[e]);
+          const int at = place(r, q);
+          if constexpr (MODE == kRecompute) {  // dg takes dh's place
+            typedef T t4 __attribute__((ext_vector_type(4)));
+            const t4 in = *(const LDS t4*)(lds + at);
+            float g[4], u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              g[e] = to_f32(in[e]) * acc.v[r][1][q * 4 + e] * d[e];
+              u[e] = to_f32(in[e]) * a[e];
+            }
+            *(LDS uint64_t*)(lds + at) = pack4<T>(g);
+            du[r][q] = pack4<T>(u);
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) a[e] *= acc.v[r][1][q * 4 + e];
-          *(LDS uint64_t*)(lds + at) = pack4<T>(a);
-        } else {
-          typedef T t4 __attribute__((ext_vector_type(4)));
-          const t4 dh = *(const LDS t4*)(lds + at);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            g[e] = to_f32(dh[e]) * acc.v[r][1][q * 4 + e] * d[e];
-            d[e] = to_f32(dh[e]) * a[e];
-          }
-          *(LDS uint64_t*)(lds + at) = pack4<T>(g);
-          *(LDS uint64_t*)(second + at) = pack4<T>(d);
+          *(LDS uint64_t*)((MODE == kForward ? lds : second) + at) = pack4<T>(a);
         }
-      }
+    });
     __syncthreads();
+    T* out = (T*)p.out0 + row0 * p.ldo0 + col0;
     if constexpr (MODE == kForward) {
-      store_tile<T, 128, kRows>(lds, (T*)p.out0 + row0 * p.ldo0 + col0, p.ldo0, rows, cols);
+      store_tile<T, 128, kRows>(lds, out, p.ldo0, rows, cols);
     } else {
       // columns behind the last inner unit are zero: they are operands of the next products
       T* o = (T*)p.dgu + row0 * (2 * p.half) + col0;
       store_tile<T, 128, kRows>(lds, o, 2 * p.half, rows, p.half - col0);
-      store_tile<T, 128, kRows>(second, o + p.half, 2 * p.half, rows, p.half - col0);
-      if (p.out0 != nullptr) {
-        __syncthreads();
+      if (p.out0 != nullptr) store_tile<T, 128, kRows>(second, out, p.ldo0, rows, cols);
+      __syncthreads();
 #pragma unroll
-        for (int r = 0; r < FR; ++r)
+      for (int r = 0; r < FR; ++r)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float a[4], d[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              act_and_grad(p.act, acc.v[r][0][q * 4 + e], &a[e], &d[e]);
-              a[e] *= acc.v[r][1][q * 4 + e];
-            }
-            *(LDS uint64_t*)(lds + tile_piece<128>(lrow + 32 * r, (lcol >> 3) + q) + (lane >> 5) * 8) = pack4<T>(a);
-          }
-        __syncthreads();
-        store_tile<T, 128, kRows>(lds, (T*)p.out0 + row0 * p.ldo0 + col0, p.ldo0, rows, cols);
-      }
+        for (int q = 0; q < 4; ++q) *(LDS uint64_t*)(lds + place(r, q)) = du[r][q];
+      __syncthreads();
+      store_tile<T, 128, kRows>(lds, o + p.half, 2 * p.half, rows, p.half - col0);
     }
   } else {
     void* base = MODE == kDw && z == 1 ? p.out1 : p.out0;
@@ -478,6 +512,10 @@ __global__ __launch_bounds__(kThreads) void k_product(Product p) {
   } else {
     cx.init(wave, lane, p.ldc0);
   }
+  Incoming<T, FR> dh;
+  if constexpr (MODE == kRecompute) {
+    if (p.splits == 1) dh.load(p, row0, col0);
+  }
   Acc<FR> acc;
 #pragma unroll
   for (int r = 0; r < FR; ++r) acc.v[r][0] = acc.v[r][1] = f32x16{};
@@ -511,7 +549,7 @@ __global__ __launch_bounds__(kThreads) void k_product(Product p) {
       }
     return;
   }
-  finish<T, MODE, FR>(p, lds, row0, col0, z, wave, lane, acc);
+  finish<T, MODE, FR>(p, lds, row0, col0, z, wave, lane, acc, dh);
 }
 
 // Joins the parts of a split sum, in their order, and finishes the tile.
@@ -527,6 +565,8 @@ __global__ __launch_bounds__(kThreads) void k_product_sum(Product p) {
   const int64_t row0 = (int64_t)at.tr * (64 * FR), col0 = (int64_t)at.tc * (kPair ? 128 : 256);
   const uint32_t tiles = p.tiles_r * p.tiles_c;
   const int64_t tile = at.unit - at.z * tiles;
+  Incoming<T, FR> dh;
+  if constexpr (MODE == kRecompute) dh.load(p, row0, col0);
   Acc<FR> acc;
 #pragma unroll
   for (int r = 0; r < FR; ++r) acc.v[r][0] = acc.v[r][1] = f32x16{};
@@ -547,7 +587,7 @@ __global__ __launch_bounds__(kThreads) void k_product_sum(Product p) {
           }
       }
   }
-  finish<T, MODE, FR>(p, (LDS char*)smem, row0, col0, z, wave, lane, acc);
+  finish<T, MODE, FR>(p, (LDS char*)smem, row0, col0, z, wave, lane, acc, dh);
 }
 
 // How a product is cut: rows of a tile (64 * fr) and parts of the sum over k.
@@ -660,12 +700,12 @@ struct Frag16<bf16> {
   }
 };
 
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 64, kFewWaves = 8, kFewThreads = 64 * kFewWaves;
 
 template <typename T, int MODE, int NT>
-__global__ __launch_bounds__(kThreads) void k_few_rows(Product p) {
-  constexpr int kUnroll = NT == 1 ? 4 : 2;
-  __shared__ f32x4 sums[8][NT][2][64];
+__global__ __launch_bounds__(kFewThreads) void k_few_rows(Product p) {
+  constexpr int kUnroll = NT == 1 ? 4 : 2;  // chunks of 64 k whose loads are under way at a time
+  __shared__ f32x4 sums[kFewWaves][NT][2][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t col0 = (int64_t)blockIdx.x * 16;
   // rows of this block's weights that exist (none: columns that pad dg | du)
@@ -680,11 +720,11 @@ __global__ __launch_bounds__(kThreads) void k_few_rows(Product p) {
   for (int t = 0; t < NT; ++t) ox[t] = (int)(((lane & 15) + 16 * t) * p.ldr * 2) + piece * 2;
   f32x4 acc[NT][2] = {};
   const int chunks = (int)((p.K + 63) / 64);
-  for (int i = wave; i < chunks; i += 8 * kUnroll) {
+  for (int i = wave * kUnroll; i < chunks; i += kFewWaves * kUnroll) {
     u32x4 g[kUnroll][2], u[kUnroll][2], x[kUnroll][NT][2];
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      const int k0 = (i + 8 * j) * 64;
+      const int k0 = (i + j) * 64;
       const int64_t rest = p.K - k0 - piece;  // k of this lane that exist
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -696,6 +736,7 @@ __global__ __launch_bounds__(kThreads) void k_few_rows(Product p) {
           x[j][t][h] = __builtin_amdgcn_raw_buffer_load_b128(bx, in ? ox[t] + k0 * 2 + 16 * h : kOutside, 0, 0);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);  // all of these loads are under way before the first is waited for
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j)
 #pragma unroll
@@ -713,19 +754,19 @@ __global__ __launch_bounds__(kThreads) void k_few_rows(Product p) {
   }
   __syncthreads();
   // element e of sums[..][lane]: inner unit 4 * (lane / 16) + e, token lane % 16
-  for (int i = threadIdx.x; i < NT * 256; i += kThreads) {
+  for (int i = threadIdx.x; i < NT * 256; i += kFewThreads) {
     const int t = i / 256, token = (i / 16) & 15, unit = i & 15;
     const int64_t row = 16 * t + token, col = col0 + unit;
     if (row >= p.R) continue;
     const int from = (unit >> 2) * 16 + token;
     float g = 0.0f, u = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < kFewWaves; ++w) {
       g += sums[w][t][0][from][unit & 3];
       u += sums[w][t][1][from][unit & 3];
     }
     float a, d;
-    act_and_grad(p.act, g, &a, &d);
+    with_act(p.act, [&](auto act) { act_and_grad<decltype(act)::value>(g, &a, &d); });
     if (col < p.C && p.out0 != nullptr) ((GLOBAL T*)p.out0)[row * p.ldo0 + col] = from_f32<T>(a * u);
     if constexpr (MODE == kRecompute) {
       const float dh = col < p.C ? to_f32(((const GLOBAL T*)p.dh)[row * p.lddh + col]) : 0.0f;
@@ -740,9 +781,9 @@ template <typename T, int MODE>
 hipError_t launch_few_rows(const Product& p, hipStream_t s) {
   const int64_t cols = MODE == kRecompute ? p.half : p.C;
   const dim3 g((unsigned)((cols + 15) / 16));
-  if (p.R <= 16) k_few_rows<T, MODE, 1><<<g, dim3(kThreads), 0, s>>>(p);
-  else if (p.R <= 32) k_few_rows<T, MODE, 2><<<g, dim3(kThreads), 0, s>>>(p);
-  else k_few_rows<T, MODE, 4><<<g, dim3(kThreads), 0, s>>>(p);
+  if (p.R <= 16) k_few_rows<T, MODE, 1><<<g, dim3(kFewThreads), 0, s>>>(p);
+  else if (p.R <= 32) k_few_rows<T, MODE, 2><<<g, dim3(kFewThreads), 0, s>>>(p);
+  else k_few_rows<T, MODE, 4><<<g, dim3(kFewThreads), 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -752,9 +793,14 @@ hipError_t launch_few(int dtype, const Product& p, hipStream_t s) {
 }
 
 // The gate and up projections by the kernel that suits the number of tokens.
+// Every workgroup of k_few_rows reads all of x, from L2: with more than about
+// 8e8 products (100 MB of it) that costs more than the partial sums of the
+// tiled kernel save. Measured at hidden 4096, 11008 inner units: 16 tokens
+// 39.9 us against 50.3 us by tiles, 24 tokens 49.5 against 50.5, 64 tokens 79.5
+// against 57.8; at 768 and 2048, 64 tokens 8.3 against 11.2.
 template <int MODE>
 msamp_status projections(msamp_kernel_kind kind, int dtype, const Product& p, Arena& ws, bool run, hipStream_t s) {
-  if (p.R > kFewRows) return product<MODE>(kind, dtype, p, ws, run, s);
+  if (p.R > kFewRows || (double)p.R * (double)p.C * (double)p.K > 8e8) return product<MODE>(kind, dtype, p, ws, run, s);
   if (run) MSAMP_LAUNCH(kind, s, launch_few<MODE>(dtype, p, s));
   return MSAMP_OK;
 }

@@ -154,6 +154,18 @@ def test_one_weight_for_gate_and_up_repeated_rows_and_views():
     check(["h"], {"h": h}, val, err, dt)
 
 
+@pytest.mark.parametrize("pads", [(0, 8), (8, 0), (0, 3), (16, 24)])
+def test_weights_with_rows_of_different_length(pads):
+    t, k, f = 70, 136, 200
+    x, _, _, dh = problem(t, k, f, torch.float16)
+    wg, wu = (matrix(f, k, torch.float16, pad, 5 + pad, 0.1) for pad in pads)
+    got = {"h": torch.empty_like(dh), "dx": torch.empty_like(x),
+           "dw_gate": torch.empty(f, k, device="cuda"), "dw_up": torch.empty(f, k, device="cuda")}
+    M.gated_ffn_backward(dh, x, wg, wu, got["dx"], got["dw_gate"], got["dw_up"], h=got["h"])
+    val, err = R.ffn(x.cpu(), wg.cpu(), wu.cpu(), "silu", dh.cpu(), torch.float16)
+    check(["h", "dx", "dw_gate", "dw_up"], got, val, err, torch.float16)
+
+
 def test_special_values_stay_in_their_token():
     """A token of NaN or infinity leaves the other tokens' rows as they are."""
     x, wg, wu, dh = problem(140, 200, 300, torch.bfloat16)
@@ -185,6 +197,23 @@ def test_large_gates_keep_their_limits():
         val, err = R.ffn(xs, one.cpu(), up.cpu(), act, dh.cpu(), dt)
         for name, g in (("h", h), ("dx", dx), ("dw_gate", a), ("dw_up", b)):
             R.assert_near(g, val[name], err[name], act + " " + name)
+
+
+def test_gates_whose_powers_overflow():
+    """g = 1e25: g^2 and g^3 leave binary32, the results do not."""
+    dt = torch.bfloat16
+    x = torch.tensor([[2.0 ** 83], [-2.0 ** 83]], device="cuda").to(dt)
+    one = torch.ones(8, 1, dtype=dt, device="cuda")
+    up = torch.full((8, 1), 2.0 ** -100, dtype=dt, device="cuda")
+    dh = torch.full((2, 8), 2.0 ** -60, dtype=dt, device="cuda")
+    for act in M.ACTIVATIONS:
+        h, dx = torch.empty(2, 8, dtype=dt, device="cuda"), torch.empty(2, 1, dtype=dt, device="cuda")
+        a, b = torch.empty(8, 1, device="cuda"), torch.empty(8, 1, device="cuda")
+        M.gated_ffn_backward(dh, x, one, up, dx, a, b, act=act, h=h)
+        # above: act(g) = g with slope 1; below: 0 with slope 0. All of it in powers of two.
+        assert (h[0] == 2.0 ** 66).all() and (h[1] == 0).all(), act
+        assert (a == 2.0 ** -77 * 2.0 ** 83).all() and (b == 2.0 ** 23 * 2.0 ** 83).all(), act
+        assert dx[0, 0].item() == 8 * (2.0 ** -77 + 2.0 ** -77) and dx[1, 0].item() == 0, act
 
 
 def test_refusals():
