@@ -91,7 +91,8 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 // and, for the weights, inner units). Either goes to LDS as it lies in memory,
 // in pieces of 16 bytes whose order within a row is permuted so that the reads
 // of a fragment spread over all banks:
-//   kAlong   LDS row = 64 k of one r or c, 8 pieces; piece p of row i at p ^ (i & 7)
+//   kAlong   LDS row = 64 k of one r or c, 8 pieces; piece p of row i at p ^ (i / 2 & 7),
+//            so that 16 rows at one k cover the 256 bytes of all banks
 //   kAcross  LDS row = all r or c of one k; piece p of row k at p ^ ((k & 3) << 2);
 //            read by the transposing LDS load, four k of 16 columns at a time
 // Nothing is copied or transposed beforehand unless rows are not 16-byte
@@ -153,7 +154,7 @@ struct Along {
   int voff[FR];
   int piece;  // first k of this lane's piece
   __device__ __forceinline__ void init(int wave, int lane, int64_t ld) {
-    piece = ((lane & 7) ^ (lane >> 3)) * 8;
+    piece = ((lane & 7) ^ (((wave & 1) << 2) | (lane >> 4))) * 8;
 #pragma unroll
     for (int j = 0; j < FR; ++j) voff[j] = (int)((64 * j + 8 * wave + (lane >> 3)) * ld * 2) + piece * 2;
   }
@@ -186,7 +187,7 @@ struct Across {
 
 template <typename T>
 __device__ __forceinline__ typename Frag<T>::type along_frag(const LDS char* lds, int block, int kk, int lane) {
-  const int off = (lane & 31) * 128 + (((kk * 2 + (lane >> 5)) ^ (lane & 7)) * 16);
+  const int off = (lane & 31) * 128 + (((kk * 2 + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16);
   return *(const LDS typename Frag<T>::type*)(lds + block * 32 * 128 + off);
 }
 
