@@ -158,11 +158,13 @@ struct Along {
 #pragma unroll
     for (int j = 0; j < FR; ++j) voff[j] = (int)((64 * j + 8 * wave + (lane >> 3)) * ld * 2) + piece * 2;
   }
-  // k0: first k of the step; left: k that remain from there
+  // k0: first k of the step; left: k that remain from there (0: none, all
+  // zeros). The scalar offset stays within the buffer, whose bounds are
+  // compared with it subtracted.
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, LDS char* lds, int wave, int j, int64_t k0,
                                        int64_t left) const {
     const int v = piece < left ? voff[j] : kOutside;
-    load_to_lds(r, lds + (64 * j + 8 * wave) * 128, v, (int)(k0 * 2));
+    load_to_lds(r, lds + (64 * j + 8 * wave) * 128, v, left > 0 ? (int)(k0 * 2) : 0);
   }
 };
 
@@ -231,81 +233,123 @@ struct Acc {
   f32x16 v[FR][2];
 };
 
+// The loads of step 'next' into the stage wr; zeros from step 'end' on (no
+// branch, so that they can be spread between matrix instructions).
 template <typename T, int MODE, int FR>
-__device__ __forceinline__ void step(const Product& p, const LDS char* __restrict__ rd, LDS char* __restrict__ wr,
+__device__ __forceinline__ void load_step(const Product& p, LDS char* wr, const Along<FR>& ra, const Across<FR>& rx,
+                                          const Along<4>& ca, const Across<4>& cx, const Across<4>& cy, int64_t row0,
+                                          int64_t col0, int z, int wave, int64_t next, int64_t steps1, int64_t end) {
+  const bool second = MODE == kDx && next >= steps1;
+  const int64_t k0 = (second ? next - steps1 : next) * kStepK;
+  const int64_t left = next < end ? p.K - k0 : 0;
+  const int64_t ks = left < kStepK ? left : kStepK;
+  if constexpr (MODE == kDw) {
+    const T* r = (const T*)(z == 0 ? p.r0 : p.r1) + k0 * p.ldr + row0;
+    const auto b = buffer_of(r, ks <= 0 ? 0 : ((ks - 1) * p.ldr + round8(p.R) - row0) * 2);
+#pragma unroll
+    for (int j = 0; j < FR; ++j) rx.load(b, wr, wave, j);
+  } else {
+    const T* r = (const T*)(second ? p.r1 : p.r0) + row0 * p.ldr;
+    const int64_t rows = p.R - row0 < 64 * FR ? p.R - row0 : 64 * FR;
+    const auto b = buffer_of(r, ((rows - 1) * p.ldr + round8(p.K)) * 2);
+#pragma unroll
+    for (int j = 0; j < FR; ++j) ra.load(b, wr, wave, j, k0, left);
+  }
+  LDS char* wc = wr + FR * 64 * 128;
+  if constexpr (is_pair(MODE)) {
+    const int64_t rows = p.C - col0 < 128 ? p.C - col0 : 128;
+    const auto bg = buffer_of((const T*)p.c0 + col0 * p.ldc0, ((rows - 1) * p.ldc0 + round8(p.K)) * 2);
+    const auto bu = buffer_of((const T*)p.c1 + col0 * p.ldc1, ((rows - 1) * p.ldc1 + round8(p.K)) * 2);
+    // LDS rows 0..127 gate, 128..255 up; ca holds the gate's offsets, then the up's
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ca.load(j < 2 ? bg : bu, wc, wave, j, k0, left);
+  } else {
+    const int64_t ld = second ? p.ldc1 : p.ldc0;
+    const T* c = (const T*)(second ? p.c1 : p.c0) + k0 * ld + col0;
+    const auto b = buffer_of(c, ks <= 0 ? 0 : ((ks - 1) * ld + round8(p.C) - col0) * 2);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      load_to_lds(b, wc + (wave + 8 * j) * 1024, MODE == kDx && second ? cy.voff[j] : cx.voff[j], 0);
+  }
+}
+
+// The operands of 16 k from a stage: blocks of 32 rows and of 32 columns.
+template <typename T, int FR>
+struct Frags {
+  typename Frag<T>::type r[FR], c[2];
+};
+
+template <typename T, int MODE, int FR>
+__device__ __forceinline__ void read_frags(const LDS char* rd, int wave, int lane, int kk, Frags<T, FR>& f) {
+  const LDS char* rc = rd + FR * 64 * 128;
+  const int rb = (wave >> 2) * FR, cb = wave & 3;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    if constexpr (is_pair(MODE)) f.c[c] = along_frag<T>(rc, cb + 4 * c, kk, lane);
+    else f.c[c] = across_frag<T, 4>(rc, cb * 2 + c, kk, lane);
+  }
+#pragma unroll
+  for (int r = 0; r < FR; ++r) {
+    if constexpr (MODE == kDw) f.r[r] = across_frag<T, FR>(rd, rb + r, kk, lane);
+    else f.r[r] = along_frag<T>(rd, rb + r, kk, lane);
+  }
+}
+
+template <typename T, int FR>
+__device__ __forceinline__ void multiply(const Frags<T, FR>& f, Acc<FR>& acc) {
+#pragma unroll
+  for (int r = 0; r < FR; ++r)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) acc.v[r][c] = Frag<T>::mma(f.c[c], f.r[r], acc.v[r][c]);
+}
+
+// Spreads a section's LDS reads and loads evenly between its 2 FR matrix
+// instructions.
+template <int READS, int LOADS, int FR>
+__device__ __forceinline__ void interleave() {
+  constexpr int kMfma = 0x8, kVmem = 0x10, kDsRead = 0x100, n = 2 * FR;
+#pragma unroll
+  for (int g = 0; g < n; ++g) {
+    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    if constexpr (READS >= n) __builtin_amdgcn_sched_group_barrier(kDsRead, (READS + n - 1) / n, 0);
+    else if (g < READS) __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
+    if constexpr (LOADS >= n) __builtin_amdgcn_sched_group_barrier(kVmem, (LOADS + n - 1) / n, 0);
+    else if (g < LOADS) __builtin_amdgcn_sched_group_barrier(kVmem, 1, 0);
+  }
+}
+
+// One step of 64 k: four sections of 16 k, each reading the operands of the
+// next section while it multiplies its own. Before the last section all reads
+// of this stage have arrived; the barrier there lets the waves write over it
+// (the loads of step i + 2, into 'again', the same stage) and, as every wave
+// has waited for its own loads of step i + 1, read the other stage 'nx'. So the
+// loads have a whole step to arrive, and no wave meets the barrier without
+// matrix instructions to go on with.
+template <typename T, int MODE, int FR>
+__device__ __forceinline__ void step(const Product& p, const LDS char* __restrict__ rd,
+                                     const LDS char* __restrict__ nx, LDS char* __restrict__ again,
                                      const Along<FR>& ra, const Across<FR>& rx, const Along<4>& ca,
-                                     const Across<4>& cx, int64_t row0, int64_t col0, int z, int wave, int lane,
-                                     int64_t next, int64_t steps1, int64_t end, bool compute, Acc<FR>& acc) {
-  constexpr bool kPair = is_pair(MODE);
-  constexpr int kTileBytesR = FR * 64 * 128;
-  if (next < end) {
-    const bool second = MODE == kDx && next >= steps1;
-    const int64_t k0 = (second ? next - steps1 : next) * kStepK;
-    const int64_t left = p.K - k0;
-    if constexpr (MODE == kDw) {
-      const T* r = (const T*)(z == 0 ? p.r0 : p.r1) + k0 * p.ldr + row0;
-      const int64_t rows = left < kStepK ? left : kStepK;
-      const auto b = buffer_of(r, ((rows - 1) * p.ldr + round8(p.R) - row0) * 2);
+                                     const Across<4>& cx, const Across<4>& cy, int64_t row0, int64_t col0, int z,
+                                     int wave, int lane, int64_t i, int64_t steps1, int64_t end, Frags<T, FR>& f,
+                                     Acc<FR>& acc) {
+  constexpr int kReads = (is_pair(MODE) ? 2 : 4) + (MODE == kDw ? 2 * FR : FR);
 #pragma unroll
-      for (int j = 0; j < FR; ++j) rx.load(b, wr, wave, j);
-    } else {
-      const T* r = (const T*)(second ? p.r1 : p.r0) + row0 * p.ldr;
-      const int64_t rows = p.R - row0 < 64 * FR ? p.R - row0 : 64 * FR;
-      const auto b = buffer_of(r, ((rows - 1) * p.ldr + round8(p.K)) * 2);
-#pragma unroll
-      for (int j = 0; j < FR; ++j) ra.load(b, wr, wave, j, k0, left);
-    }
-    LDS char* wc = wr + kTileBytesR;
-    if constexpr (kPair) {
-      const int64_t rows = p.C - col0 < 128 ? p.C - col0 : 128;
-      const auto bg = buffer_of((const T*)p.c0 + col0 * p.ldc0, ((rows - 1) * p.ldc0 + round8(p.K)) * 2);
-      const auto bu = buffer_of((const T*)p.c1 + col0 * p.ldc1, ((rows - 1) * p.ldc1 + round8(p.K)) * 2);
-      // LDS rows 0..127 gate, 128..255 up; ca holds the gate's offsets, cx (its first two) the up's
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        ca.load(bg, wc, wave, j, k0, left);
-        const int v = ca.piece < left ? cx.voff[j] : kOutside;
-        load_to_lds(bu, wc + (128 + 64 * j + 8 * wave) * 128, v, (int)(k0 * 2));
-      }
-    } else {
-      const int64_t ld = second ? p.ldc1 : p.ldc0;
-      const T* c = (const T*)(second ? p.c1 : p.c0) + k0 * ld + col0;
-      const int64_t rows = left < kStepK ? left : kStepK;
-      const auto b = buffer_of(c, ((rows - 1) * ld + round8(p.C) - col0) * 2);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // the second pass's weights may have rows of another length
-        if (second) {
-          const int k = (wave + 8 * j) * Across<4>::kRows + lane / Across<4>::kPieces;
-          const int v = (int)(k * ld * 2) + ((lane % Across<4>::kPieces) ^ ((k & 3) << 2)) * 16;
-          load_to_lds(b, wc + (wave + 8 * j) * 1024, v, 0);
-        } else {
-          cx.load(b, wc, wave, j);
-        }
-      }
-    }
+  for (int kk = 0; kk < 3; ++kk) {
+    Frags<T, FR> next;
+    read_frags<T, MODE, FR>(rd, wave, lane, kk + 1, next);
+    multiply<T, FR>(f, acc);
+    interleave<kReads, 0, FR>();
+    f = next;
   }
-  if (!compute) return;
-  const LDS char* rc = rd + kTileBytesR;
-  const int wr_block = (wave >> 2) * FR, wc_block = wave & 3;
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) {
-    typename Frag<T>::type fc[2], fr[FR];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if constexpr (kPair) fc[c] = along_frag<T>(rc, wc_block + 4 * c, kk, lane);
-      else fc[c] = across_frag<T, 4>(rc, wc_block * 2 + c, kk, lane);
-    }
-#pragma unroll
-    for (int r = 0; r < FR; ++r) {
-      if constexpr (MODE == kDw) fr[r] = across_frag<T, FR>(rd, wr_block + r, kk, lane);
-      else fr[r] = along_frag<T>(rd, wr_block + r, kk, lane);
-    }
-#pragma unroll
-    for (int r = 0; r < FR; ++r)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) acc.v[r][c] = Frag<T>::mma(fc[c], fr[r], acc.v[r][c]);
-  }
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  Frags<T, FR> next;
+  read_frags<T, MODE, FR>(nx, wave, lane, 0, next);
+  load_step<T, MODE, FR>(p, again, ra, rx, ca, cx, cy, row0, col0, z, wave, i + 2, steps1, end);
+  multiply<T, FR>(f, acc);
+  interleave<kReads, FR + 4, FR>();
+  f = next;
 }
 
 // 16-bit tile in LDS on its way out (or dh on its way in): rows of COLS
@@ -501,17 +545,18 @@ __global__ __launch_bounds__(kThreads) void k_product(Product p) {
   Along<FR> ra;
   Across<FR> rx;
   Along<4> ca;
-  Across<4> cx;
+  Across<4> cx, cy;  // cy: the second pass's
   if constexpr (MODE == kDw) rx.init(wave, lane, p.ldr);
   else ra.init(wave, lane, p.ldr);
   if constexpr (kPair) {
     ca.init(wave, lane, p.ldc0);
     Along<4> up;
     up.init(wave, lane, p.ldc1);
-    cx.voff[0] = up.voff[0];
-    cx.voff[1] = up.voff[1];
+    ca.voff[2] = up.voff[0];
+    ca.voff[3] = up.voff[1];
   } else {
     cx.init(wave, lane, p.ldc0);
+    if constexpr (MODE == kDx) cy.init(wave, lane, p.ldc1);
   }
   Incoming<T, FR> dh;
   if constexpr (MODE == kRecompute) {
@@ -524,14 +569,17 @@ __global__ __launch_bounds__(kThreads) void k_product(Product p) {
   const int64_t steps = MODE == kDx ? 2 * steps1 : steps1;
   const int64_t begin = (int64_t)at.part * p.part;
   const int64_t end = steps < begin + p.part ? steps : begin + p.part;
-  step<T, MODE, FR>(p, lds + kStage, lds, ra, rx, ca, cx, row0, col0, z, wave, lane, begin, steps1, end, false, acc);
+  load_step<T, MODE, FR>(p, lds, ra, rx, ca, cx, cy, row0, col0, z, wave, begin, steps1, end);
   __syncthreads();
+  load_step<T, MODE, FR>(p, lds + kStage, ra, rx, ca, cx, cy, row0, col0, z, wave, begin + 1, steps1, end);
+  Frags<T, FR> f;
+  read_frags<T, MODE, FR>(lds, wave, lane, 0, f);
   for (int64_t i = begin; i < end; ++i) {
     const int cur = (int)((i - begin) & 1) * kStage;
-    step<T, MODE, FR>(p, lds + cur, lds + (kStage - cur), ra, rx, ca, cx, row0, col0, z, wave, lane, i + 1, steps1,
-                      end, true, acc);
-    __syncthreads();
+    step<T, MODE, FR>(p, lds + cur, lds + (kStage - cur), lds + cur, ra, rx, ca, cx, cy, row0, col0, z, wave, lane, i,
+                      steps1, end, f, acc);
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the last loads to LDS, of zeros, are still under way
   if (p.splits > 1) {
     f32x4* o = (f32x4*)p.partial + (int64_t)at.unit * (64 * FR * kTileC / 4) + wave * (FR * 2 * 4 * 64) + lane;
     const int lrow = (wave >> 2) * (32 * FR) + (lane & 31);
@@ -599,10 +647,12 @@ struct Cut {
   int64_t partial_bytes;
 };
 
-// The cut with the least estimated time. A compute unit takes about 0.35 us
-// for what a step does whatever its tile (the column operand's 32 KB, the
-// barrier) and 0.35 us for each 64 rows; a tile costs 4 us to start and to
-// finish; joining parts costs a launch and one pass over them.
+// The cut with the least estimated time, by constants fitted to measurements
+// of every cut of 14 problems (tokens 64 to 8192, hidden 128 to 8192, 128 to
+// 13824 inner units; on these the chosen cut is within 2% of the best one on
+// average, 18% at most): a step of a tile of 64, 128 or 256 rows takes 0.8, 1.05
+// or 1.8 us, its start and finish 2, 7.5 or 13 us, and joining parts 3 us and
+// two passes over them at 8 TB/s. One workgroup a compute unit runs at a time.
 Cut choose_cut(int mode, int64_t R, int64_t C, int64_t K) {
   Cut best = {};
   double least = 1e30;
@@ -611,7 +661,7 @@ Cut choose_cut(int mode, int64_t R, int64_t C, int64_t K) {
   const int64_t nc = (C + tc - 1) / tc, zs = mode == kDw ? 2 : 1;
   for (int fr = 4; fr >= 1; fr /= 2) {
     const int64_t nr = (R + 64 * fr - 1) / (64 * fr), tiles = nr * nc * zs;
-    const double step_us = 0.35 + 0.35 * fr;
+    const double step_us = fr == 4 ? 1.8 : (fr == 2 ? 1.05 : 0.8), ends_us = fr == 4 ? 13.0 : (fr == 2 ? 7.5 : 2.0);
     const int64_t slots = 256;
     for (int64_t splits = 1; splits <= 64 && (splits == 1 || steps / splits >= 2); ++splits) {
       const int64_t part = (steps + splits - 1) / splits;
@@ -620,7 +670,7 @@ Cut choose_cut(int mode, int64_t R, int64_t C, int64_t K) {
       const int64_t rounds = (tiles * splits + slots - 1) / slots;
       const int64_t bytes = splits == 1 ? 0 : tiles * splits * (64 * fr * kTileC * 4);
       if (bytes > (int64_t)1 << 30) break;
-      const double t = rounds * (part * step_us + 4.0) + (splits == 1 ? 0.0 : 6.0 + bytes * 2 / 4e6);
+      const double t = rounds * (part * step_us + ends_us) + (splits == 1 ? 0.0 : 3.0 + bytes * 2 / 8e6);
       if (t < least) {
         least = t;
         best = {fr, (uint32_t)nr, (uint32_t)nc, (uint32_t)splits, part, bytes};
