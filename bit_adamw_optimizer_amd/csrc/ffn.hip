@@ -620,22 +620,29 @@ __global__ __launch_bounds__(kThreads) void k_product_sum(Product p) {
 #pragma unroll
   for (int r = 0; r < FR; ++r) acc.v[r][0] = acc.v[r][1] = f32x16{};
   const int lrow = (wave >> 2) * (32 * FR) + (lane & 31);
-  for (uint32_t part = 0; part < p.splits; ++part) {
-    const int64_t unit = ((int64_t)at.z * p.splits + part) * tiles + tile;
-    const f32x4* o = (const f32x4*)p.partial + unit * (64 * FR * kTileC / 4) + wave * (FR * 2 * 4 * 64) + lane;
+  constexpr int kAhead = FR == 4 ? 2 : 4;  // parts whose loads are under way at a time
+  const int64_t size = 64 * FR * kTileC / 4;  // of a unit, in f32x4
+  const f32x4* from = (const f32x4*)p.partial + ((int64_t)at.z * p.splits * tiles + tile) * size +
+                      wave * (FR * 2 * 4 * 64) + lane;
 #pragma unroll
-    for (int r = 0; r < FR; ++r)
-      if (row0 + lrow + 32 * r < p.R) {
+  for (int r = 0; r < FR; ++r)
+    if (row0 + lrow + 32 * r < p.R)
+      for (uint32_t part = 0; part < p.splits; part += kAhead) {
+        f32x4 v[kAhead][8];
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x4 v = o[((r * 2 + c) * 4 + q) * 64];
+          for (int q = 0; q < 8; ++q)
+            if (part + k < p.splits) v[k][q] = from[(int64_t)(part + k) * tiles * size + (r * 8 + q) * 64];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc.v[r][c][q * 4 + e] += v[e];
+        for (int k = 0; k < kAhead; ++k)
+          if (part + k < p.splits) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc.v[r][q >> 2][(q & 3) * 4 + e] += v[k][q][e];
           }
       }
-  }
   finish<T, MODE, FR>(p, (LDS char*)smem, row0, col0, z, wave, lane, acc, dh);
 }
 
@@ -646,6 +653,12 @@ struct Cut {
   int64_t part;
   int64_t partial_bytes;
 };
+
+// A part takes a workgroup of the joining kernel this long at least.
+double join_us(int fr, int64_t splits, int64_t bytes) {
+  const double each = splits * (fr == 4 ? 2.0 : (fr == 2 ? 0.6 : 0.25)), all = bytes * 2 / 8e6;
+  return 3.5 + (each > all ? each : all);
+}
 
 // The cut with the least estimated time, by constants fitted to measurements
 // of every cut of 14 problems (tokens 64 to 8192, hidden 128 to 8192, 128 to
@@ -670,7 +683,7 @@ Cut choose_cut(int mode, int64_t R, int64_t C, int64_t K) {
       const int64_t rounds = (tiles * splits + slots - 1) / slots;
       const int64_t bytes = splits == 1 ? 0 : tiles * splits * (64 * fr * kTileC * 4);
       if (bytes > (int64_t)1 << 30) break;
-      const double t = rounds * (part * step_us + ends_us) + (splits == 1 ? 0.0 : 3.0 + bytes * 2 / 8e6);
+      const double t = rounds * (part * step_us + ends_us) + (splits == 1 ? 0.0 : join_us(fr, splits, bytes));
       if (t < least) {
         least = t;
         best = {fr, (uint32_t)nr, (uint32_t)nc, (uint32_t)splits, part, bytes};
@@ -753,7 +766,23 @@ struct Frag16<bf16> {
 
 constexpr int kFewRows = 64, kFewWaves = 8, kFewThreads = 64 * kFewWaves;
 
-template <typename T, int MODE, int NT>
+// n (<= 8) consecutive elements at any address; zeros behind them.
+template <typename T>
+__device__ __forceinline__ u32x4 load_piece(const T* p, int64_t n) {
+  if (n >= 8) return *(const GLOBAL u32x4_any*)p;
+  typedef T t8 __attribute__((ext_vector_type(8)));
+  t8 v = {};
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < n) v[k] = ((const GLOBAL T*)p)[k];
+  return __builtin_bit_cast(u32x4, v);
+}
+
+// ALIGNED: 16-byte aligned rows of whole pieces, read through buffers whose
+// bounds give the zeros behind the last row and k. Otherwise the rows behind
+// the last one repeat it (their sums go nowhere), and the chunk that k ends in
+// is read on its own.
+template <typename T, int MODE, int NT, bool ALIGNED>
 __global__ __launch_bounds__(kFewThreads) void k_few_rows(Product p) {
   constexpr int kUnroll = NT == 1 ? 4 : 2;  // chunks of 64 k whose loads are under way at a time
   __shared__ f32x4 sums[kFewWaves][NT][2][64];
@@ -761,42 +790,89 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(Product p) {
   const int64_t col0 = (int64_t)blockIdx.x * 16;
   // rows of this block's weights that exist (none: columns that pad dg | du)
   const int64_t left = p.C - col0, cols = left < 0 ? 0 : (left < 16 ? left : 16);
-  const auto bg = buffer_of((const T*)p.c0 + col0 * p.ldc0, cols == 0 ? 0 : ((cols - 1) * p.ldc0 + round8(p.K)) * 2);
-  const auto bu = buffer_of((const T*)p.c1 + col0 * p.ldc1, cols == 0 ? 0 : ((cols - 1) * p.ldc1 + round8(p.K)) * 2);
-  const auto bx = buffer_of(p.r0, ((p.R - 1) * p.ldr + round8(p.K)) * 2);
   const int piece = (lane >> 4) * 16;  // this lane's 16 k of a chunk of 64
-  const int og = (int)((lane & 15) * p.ldc0 * 2) + piece * 2, ou = (int)((lane & 15) * p.ldc1 * 2) + piece * 2;
-  int ox[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) ox[t] = (int)(((lane & 15) + 16 * t) * p.ldr * 2) + piece * 2;
   f32x4 acc[NT][2] = {};
-  const int chunks = (int)((p.K + 63) / 64);
-  for (int i = wave * kUnroll; i < chunks; i += kFewWaves * kUnroll) {
-    u32x4 g[kUnroll][2], u[kUnroll][2], x[kUnroll][NT][2];
+  const int chunks = (int)(ALIGNED ? (p.K + 63) / 64 : p.K / 64);
+  auto multiply = [&](const u32x4(&g)[2], const u32x4(&u)[2], const u32x4(&x)[NT][2]) {
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const int k0 = (i + j) * 64;
-      const int64_t rest = p.K - k0 - piece;  // k of this lane that exist
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        acc[t][0] = Frag16<T>::mma(g[h], x[t][h], acc[t][0]);
+        acc[t][1] = Frag16<T>::mma(u[h], x[t][h], acc[t][1]);
+      }
+  };
+  if constexpr (ALIGNED) {
+    const auto bg = buffer_of((const T*)p.c0 + col0 * p.ldc0, cols == 0 ? 0 : ((cols - 1) * p.ldc0 + round8(p.K)) * 2);
+    const auto bu = buffer_of((const T*)p.c1 + col0 * p.ldc1, cols == 0 ? 0 : ((cols - 1) * p.ldc1 + round8(p.K)) * 2);
+    const auto bx = buffer_of(p.r0, ((p.R - 1) * p.ldr + round8(p.K)) * 2);
+    const int og = (int)((lane & 15) * p.ldc0 * 2) + piece * 2, ou = (int)((lane & 15) * p.ldc1 * 2) + piece * 2;
+    int ox[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) ox[t] = (int)(((lane & 15) + 16 * t) * p.ldr * 2) + piece * 2;
+    for (int i = wave * kUnroll; i < chunks; i += kFewWaves * kUnroll) {
+      u32x4 g[kUnroll][2], u[kUnroll][2], x[kUnroll][NT][2];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        const int k0 = (i + j) * 64;
+        const int64_t rest = p.K - k0 - piece;  // k of this lane that exist
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool in = rest > 8 * h;
+          g[j][h] = __builtin_amdgcn_raw_buffer_load_b128(bg, in ? og + k0 * 2 + 16 * h : kOutside, 0, 0);
+          u[j][h] = __builtin_amdgcn_raw_buffer_load_b128(bu, in ? ou + k0 * 2 + 16 * h : kOutside, 0, 0);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            x[j][t][h] = __builtin_amdgcn_raw_buffer_load_b128(bx, in ? ox[t] + k0 * 2 + 16 * h : kOutside, 0, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);  // all of these loads are under way before the first is waited for
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) multiply(g[j], u[j], x[j]);
+    }
+  } else {
+    const int64_t row = col0 + (lane & 15) < p.C ? col0 + (lane & 15) : p.C - 1;
+    const T* pg = (const T*)p.c0 + row * p.ldc0 + piece;
+    const T* pu = (const T*)p.c1 + row * p.ldc1 + piece;
+    const T* px[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int64_t token = (lane & 15) + 16 * t;
+      px[t] = (const T*)p.r0 + (token < p.R ? token : p.R - 1) * p.ldr + piece;
+    }
+    for (int i = wave * kUnroll; i < chunks; i += kFewWaves * kUnroll) {
+      u32x4 g[kUnroll][2], u[kUnroll][2], x[kUnroll][NT][2];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        // in the place of a chunk behind the last whole one the first is read, and not used
+        const bool in = i + j < chunks;
+        const int64_t k0 = in ? (int64_t)(i + j) * 64 : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          g[j][h] = *(const GLOBAL u32x4_any*)(pg + k0 + 8 * h);
+          u[j][h] = *(const GLOBAL u32x4_any*)(pu + k0 + 8 * h);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) x[j][t][h] = *(const GLOBAL u32x4_any*)(px[t] + k0 + 8 * h);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+        if (i + j < chunks) multiply(g[j], u[j], x[j]);
+    }
+    if (p.K % 64 != 0 && wave == chunks % kFewWaves) {
+      u32x4 g[2], u[2], x[NT][2];
+      const int64_t k0 = (int64_t)chunks * 64;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const bool in = rest > 8 * h;
-        g[j][h] = __builtin_amdgcn_raw_buffer_load_b128(bg, in ? og + k0 * 2 + 16 * h : kOutside, 0, 0);
-        u[j][h] = __builtin_amdgcn_raw_buffer_load_b128(bu, in ? ou + k0 * 2 + 16 * h : kOutside, 0, 0);
+        const int64_t n = p.K - k0 - piece - 8 * h;
+        g[h] = load_piece(pg + k0 + 8 * h, n);
+        u[h] = load_piece(pu + k0 + 8 * h, n);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          x[j][t][h] = __builtin_amdgcn_raw_buffer_load_b128(bx, in ? ox[t] + k0 * 2 + 16 * h : kOutside, 0, 0);
+        for (int t = 0; t < NT; ++t) x[t][h] = load_piece(px[t] + k0 + 8 * h, n);
       }
+      multiply(g, u, x);
     }
-    __builtin_amdgcn_sched_barrier(0);  // all of these loads are under way before the first is waited for
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          acc[t][0] = Frag16<T>::mma(g[j][h], x[j][t][h], acc[t][0]);
-          acc[t][1] = Frag16<T>::mma(u[j][h], x[j][t][h], acc[t][1]);
-        }
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -828,72 +904,6 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(Product p) {
   }
 }
 
-template <typename T, int MODE>
-hipError_t launch_few_rows(const Product& p, hipStream_t s) {
-  const int64_t cols = MODE == kRecompute ? p.half : p.C;
-  const dim3 g((unsigned)((cols + 15) / 16));
-  if (p.R <= 16) k_few_rows<T, MODE, 1><<<g, dim3(kFewThreads), 0, s>>>(p);
-  else if (p.R <= 32) k_few_rows<T, MODE, 2><<<g, dim3(kFewThreads), 0, s>>>(p);
-  else k_few_rows<T, MODE, 4><<<g, dim3(kFewThreads), 0, s>>>(p);
-  return hipGetLastError();
-}
-
-template <int MODE>
-hipError_t launch_few(int dtype, const Product& p, hipStream_t s) {
-  return dtype == MSAMP_F16 ? launch_few_rows<f16, MODE>(p, s) : launch_few_rows<bf16, MODE>(p, s);
-}
-
-// The gate and up projections by the kernel that suits the number of tokens.
-// Every workgroup of k_few_rows reads all of x, from L2: with more than about
-// 8e8 products (100 MB of it) that costs more than the partial sums of the
-// tiled kernel save. Measured at hidden 4096, 11008 inner units: 16 tokens
-// 39.9 us against 50.3 us by tiles, 24 tokens 49.5 against 50.5, 64 tokens 79.5
-// against 57.8; at 768 and 2048, 64 tokens 8.3 against 11.2.
-template <int MODE>
-msamp_status projections(msamp_kernel_kind kind, int dtype, const Product& p, Arena& ws, bool run, hipStream_t s) {
-  if (p.R > kFewRows || (double)p.R * (double)p.C * (double)p.K > 8e8) return product<MODE>(kind, dtype, p, ws, run, s);
-  if (run) MSAMP_LAUNCH(kind, s, launch_few<MODE>(dtype, p, s));
-  return MSAMP_OK;
-}
-
-// ---------------------------------------------------------------- layout ---
-
-// out [rows, ld] <- src [rows, cols] or a checkpoint's values, zeros behind the
-// last column.
-template <typename T>
-__global__ __launch_bounds__(256) void k_layout(int64_t rows, int64_t cols, const T* src, int64_t lds, CkptRef ck,
-                                                T* out, int64_t ld) {
-  const int64_t per = ld / 8, total = rows * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / per, col = (i - row * per) * 8;
-    const int64_t left = cols - col;
-    const int n = left < 0 ? 0 : (left < 8 ? (int)left : 8);
-    float f[8];
-    if (src != nullptr) {
-      load8(src + row * lds + col, n, f);
-    } else {
-      load_ckpt8(ck.fmt, ck.codes + row * ck.ld, ck.scales + row * ck.ld_scales, col, n, f);
-      const float lim = __is_same(T, f16) ? kF16Max : kBf16Max;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = clamp_finite(f[k], lim);
-    }
-    store8(out + row * ld + col, 8, f);
-  }
-}
-
-hipError_t launch_layout(int dtype, int64_t rows, int64_t cols, const void* src, int64_t lds, const CkptRef& ck,
-                         void* out, int64_t ld, hipStream_t s) {
-  const int64_t blocks = (rows * (ld / 8) + 255) / 256;
-  const dim3 g((unsigned)(blocks < 65536 ? blocks : 65536));
-  if (dtype == MSAMP_F16) k_layout<f16><<<g, dim3(256), 0, s>>>(rows, cols, (const f16*)src, lds, ck, (f16*)out, ld);
-  else k_layout<bf16><<<g, dim3(256), 0, s>>>(rows, cols, (const bf16*)src, lds, ck, (bf16*)out, ld);
-  return hipGetLastError();
-}
-
-// ------------------------------------------------------------------ plan ---
-
-int64_t round64(int64_t n) { return (n + 63) / 64 * 64; }
-
 // Whether the matrix kernels can read an operand where it lies: 16-byte
 // aligned rows of whole 16-byte pieces, and a tile of 256 rows within the 2^31
 // bytes of a buffer.
@@ -901,25 +911,122 @@ bool direct(const void* p, int64_t ld, int64_t cols) {
   return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0 && cols % 8 == 0 && ld >= cols && ld < (1 << 22);
 }
 
+template <typename T, int MODE, bool ALIGNED>
+hipError_t launch_few_rows(const Product& p, hipStream_t s) {
+  const int64_t cols = MODE == kRecompute ? p.half : p.C;
+  const dim3 g((unsigned)((cols + 15) / 16)), b(kFewThreads);
+  if (p.R <= 16) k_few_rows<T, MODE, 1, ALIGNED><<<g, b, 0, s>>>(p);
+  else if (p.R <= 32) k_few_rows<T, MODE, 2, ALIGNED><<<g, b, 0, s>>>(p);
+  else k_few_rows<T, MODE, 4, ALIGNED><<<g, b, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <int MODE>
+hipError_t launch_few(int dtype, const Product& p, hipStream_t s) {
+  if constexpr (MODE == kForward) {  // the backward pass lays its operands out anyway
+    if (!direct(p.r0, p.ldr, p.K) || !direct(p.c0, p.ldc0, p.K) || !direct(p.c1, p.ldc1, p.K))
+      return dtype == MSAMP_F16 ? launch_few_rows<f16, MODE, false>(p, s) : launch_few_rows<bf16, MODE, false>(p, s);
+  }
+  return dtype == MSAMP_F16 ? launch_few_rows<f16, MODE, true>(p, s) : launch_few_rows<bf16, MODE, true>(p, s);
+}
+
+// Whether the kernel for few tokens takes the gate and up projections. Every
+// workgroup of it reads all of x, from L2: with more than about 8e8 products
+// (100 MB of it) that costs more than the partial sums of the tiled kernel
+// save. Measured at hidden 4096, 11008 inner units: 16 tokens 39.9 us against
+// 50.3 us by tiles, 24 tokens 49.5 against 50.5, 64 tokens 79.5 against 57.8;
+// at 768 and 2048, 64 tokens 8.3 against 11.2. Its waves take their parts of k
+// one after another, with several blocks of tokens 128 k at a time: beyond a
+// hidden size of 1024 that takes longer than a split sum (56 tokens at 3136
+// and 1920: 18.5 us).
+bool few_rows(int64_t R, int64_t C, int64_t K) {
+  return R <= kFewRows && (double)R * (double)C * (double)K <= 8e8 && (R <= 16 || K <= 1024);
+}
+
+// The gate and up projections by the kernel that suits the number of tokens.
+template <int MODE>
+msamp_status projections(msamp_kernel_kind kind, int dtype, const Product& p, Arena& ws, bool run, hipStream_t s) {
+  if (!few_rows(p.R, p.C, p.K)) return product<MODE>(kind, dtype, p, ws, run, s);
+  if (run) MSAMP_LAUNCH(kind, s, launch_few<MODE>(dtype, p, s));
+  return MSAMP_OK;
+}
+
+// ---------------------------------------------------------------- layout ---
+
+// out [rows, ld] <- src [rows, cols] or a checkpoint's values, zeros behind the
+// last column; up to three matrices in one launch.
+struct Layout {
+  int64_t rows, cols;
+  const void* src;  // null: ck
+  int64_t lds;
+  CkptRef ck;
+  void* out;
+  int64_t ld;
+};
+struct Layouts {
+  Layout job[3];
+  int n;
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_layout(Layouts all) {
+  const Layout a = all.job[blockIdx.y];
+  const int64_t per = a.ld / 8, total = a.rows * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = (uint64_t)total <= UINT32_MAX ? (int64_t)((uint32_t)i / (uint32_t)per) : i / per;
+    const int64_t col = (i - row * per) * 8, left = a.cols - col;
+    const int n = left < 0 ? 0 : (left < 8 ? (int)left : 8);
+    float f[8];
+    if (a.src != nullptr) {
+      load8((const T*)a.src + row * a.lds + col, n, f);
+    } else {
+      load_ckpt8(a.ck.fmt, a.ck.codes + row * a.ck.ld, a.ck.scales + row * a.ck.ld_scales, col, n, f);
+      const float lim = __is_same(T, f16) ? kF16Max : kBf16Max;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = clamp_finite(f[k], lim);
+    }
+    store8((T*)a.out + row * a.ld + col, 8, f);
+  }
+}
+
+hipError_t launch_layout(int dtype, const Layouts& all, hipStream_t s) {
+  int64_t blocks = 1;
+  for (int i = 0; i < all.n; ++i) {
+    const int64_t b = (all.job[i].rows * (all.job[i].ld / 8) + 255) / 256;
+    blocks = b > blocks ? b : blocks;
+  }
+  const dim3 g((unsigned)(blocks < 65536 ? blocks : 65536), (unsigned)all.n);
+  if (dtype == MSAMP_F16) k_layout<f16><<<g, dim3(256), 0, s>>>(all);
+  else k_layout<bf16><<<g, dim3(256), 0, s>>>(all);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ plan ---
+
+int64_t round64(int64_t n) { return (n + 63) / 64 * 64; }
+
 struct Operand {
   const void* p;
   int64_t ld;
 };
 
-// An operand [rows, cols], laid out in the workspace when it has to be.
-msamp_status lay_out(int dtype, int64_t rows, int64_t cols, const void* p, int64_t ld, const msamp_checkpoint* ck,
-                     Arena& ws, bool run, hipStream_t s, Operand* out) {
+// An operand [rows, cols]: where it lies, or its place in the workspace with
+// the job that lays it out there.
+msamp_status lay_out(int64_t rows, int64_t cols, const void* p, int64_t ld, const msamp_checkpoint* ck, Arena& ws,
+                     Layouts& jobs, Operand* out) {
   *out = {p, ld};
-  if (rows == 0 || cols == 0 || (ck == nullptr && direct(p, ld, cols))) return MSAMP_OK;
+  if (ck == nullptr && direct(p, ld, cols)) return MSAMP_OK;
   const int64_t lp = round64(cols);
   if (lp >= (1 << 22)) return fail(MSAMP_E_INVALID_ARG, "rows longer than 2^22 elements have to be 16-byte aligned");
-  void* q = ws.take(rows * lp * 2);
-  *out = {q, lp};
-  CkptRef c;
-  if (ck != nullptr) c = {ck->codes, ck->ld, ck->scales, ck->ld_scales, (int)ck->fmt};
-  if (run)
-    MSAMP_LAUNCH(MSAMP_KERNEL_FFN_LAYOUT, s,
-                 launch_layout(dtype, rows, cols, ck == nullptr ? p : nullptr, ld, c, q, lp, s));
+  Layout& j = jobs.job[jobs.n++];
+  j = {rows, cols, ck == nullptr ? p : nullptr, ld, CkptRef{}, ws.take(rows * lp * 2), lp};
+  if (ck != nullptr) j.ck = {ck->codes, ck->ld, ck->scales, ck->ld_scales, (int)ck->fmt};
+  *out = {j.out, lp};
+  return MSAMP_OK;
+}
+
+msamp_status run_layouts(int dtype, const Layouts& jobs, hipStream_t s) {
+  if (jobs.n > 0) MSAMP_LAUNCH(MSAMP_KERNEL_FFN_LAYOUT, s, launch_layout(dtype, jobs, s));
   return MSAMP_OK;
 }
 
@@ -948,10 +1055,14 @@ msamp_status fill_zero(int dtype, int64_t rows, int64_t cols, void* out, int64_t
 msamp_status forward(const msamp_gated_ffn& a, Arena& ws, bool run, hipStream_t s) {
   if (a.tokens == 0 || a.ffn == 0) return MSAMP_OK;
   if (a.hidden == 0) return run ? fill_zero(a.dtype, a.tokens, a.ffn, a.h, a.ldh, s) : MSAMP_OK;
-  Operand x, g, u;
-  MSAMP_TRY(lay_out(a.dtype, a.tokens, a.hidden, a.x, a.ldx, nullptr, ws, run, s, &x));
-  MSAMP_TRY(lay_out(a.dtype, a.ffn, a.hidden, a.w_gate, a.ld_gate, nullptr, ws, run, s, &g));
-  MSAMP_TRY(lay_out(a.dtype, a.ffn, a.hidden, a.w_up, a.ld_up, nullptr, ws, run, s, &u));
+  Operand x = {a.x, a.ldx}, g = {a.w_gate, a.ld_gate}, u = {a.w_up, a.ld_up};
+  if (!few_rows(a.tokens, a.ffn, a.hidden)) {
+    Layouts jobs = {};
+    MSAMP_TRY(lay_out(a.tokens, a.hidden, a.x, a.ldx, nullptr, ws, jobs, &x));
+    MSAMP_TRY(lay_out(a.ffn, a.hidden, a.w_gate, a.ld_gate, nullptr, ws, jobs, &g));
+    MSAMP_TRY(lay_out(a.ffn, a.hidden, a.w_up, a.ld_up, nullptr, ws, jobs, &u));
+    if (run) MSAMP_TRY(run_layouts(a.dtype, jobs, s));
+  }
   Product p = {};
   p.R = a.tokens, p.C = a.ffn, p.K = a.hidden;
   p.r0 = x.p, p.ldr = x.ld;
@@ -972,9 +1083,11 @@ msamp_status backward(const msamp_gated_ffn& a, Arena& ws, bool run, hipStream_t
     return fill_zero(a.dw_dtype, F, K, a.dw_up, a.ld_dw_up, s);
   }
   Operand x, g, u;
-  MSAMP_TRY(lay_out(a.dtype, T, K, a.x, a.ldx, a.x_ckpt, ws, run, s, &x));
-  MSAMP_TRY(lay_out(a.dtype, F, K, a.w_gate, a.ld_gate, nullptr, ws, run, s, &g));
-  MSAMP_TRY(lay_out(a.dtype, F, K, a.w_up, a.ld_up, nullptr, ws, run, s, &u));
+  Layouts jobs = {};
+  MSAMP_TRY(lay_out(T, K, a.x, a.ldx, a.x_ckpt, ws, jobs, &x));
+  MSAMP_TRY(lay_out(F, K, a.w_gate, a.ld_gate, nullptr, ws, jobs, &g));
+  MSAMP_TRY(lay_out(F, K, a.w_up, a.ld_up, nullptr, ws, jobs, &u));
+  if (run) MSAMP_TRY(run_layouts(a.dtype, jobs, s));
   const int64_t half = round64(F);
   if (2 * half >= (1 << 22)) return fail(MSAMP_E_INVALID_ARG, "ffn exceeds 2^21 - 64");
   char* dgu = (char*)ws.take(T * 2 * half * 2);  // null while only counting

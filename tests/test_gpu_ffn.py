@@ -166,6 +166,26 @@ def test_weights_with_rows_of_different_length(pads):
     check(["h", "dx", "dw_gate", "dw_up"], got, val, err, torch.float16)
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("t,k,f,pads", [(1, 4242, 50, (0, 0, 0)), (2, 640, 33, (3, 0, 0)), (16, 777, 40, (0, 1, 5)),
+                                        (17, 129, 70, (1, 1, 1)), (40, 1000, 31, (0, 3, 0)), (64, 65, 130, (7, 0, 2)),
+                                        (5, 8192, 17, (8, 16, 24)), (60, 2000, 100, (1, 0, 0))])
+def test_few_tokens_at_any_alignment(t, k, f, pads, dtype):
+    dt = DT[dtype]
+    x, wg, wu = (matrix(r, k, dt, pad, 3 * k + i, s) for i, (r, pad, s) in
+                 enumerate(((t, pads[0], 1.0), (f, pads[1], k ** -0.5), (f, pads[2], k ** -0.5))))
+    dh = matrix(t, f, dt, pads[0], 9, 0.1)
+    val, err = R.ffn(x.cpu(), wg.cpu(), wu.cpu(), "silu", dh.cpu(), dt)
+    buf, h = out(t, f, dt)
+    M.gated_ffn_forward(x, wg, wu, h)
+    assert untouched(buf, t, f)
+    check(["h"], {"h": h}, val, err, dt)
+    got = {"h": torch.empty_like(h), "dx": torch.empty(t, k, dtype=dt, device="cuda"),
+           "dw_gate": torch.empty(f, k, device="cuda"), "dw_up": torch.empty(f, k, device="cuda")}
+    M.gated_ffn_backward(dh, x, wg, wu, got["dx"], got["dw_gate"], got["dw_up"], h=got["h"])
+    check(["h", "dx", "dw_gate", "dw_up"], got, val, err, dt)
+
+
 def test_special_values_stay_in_their_token():
     """A token of NaN or infinity leaves the other tokens' rows as they are."""
     x, wg, wu, dh = problem(140, 200, 300, torch.bfloat16)
