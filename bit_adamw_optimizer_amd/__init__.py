@@ -67,7 +67,7 @@ PROBE_F16_TO_F32 = 5
 KERNELS = ["amax", "quantize_fp8", "dequantize_fp8", "step_pass1", "o2_pass2", "o3_pass2",
            "o3_pass3", "finalize", "amax_finalize", "o2_delayed", "rmw_probe", "quantize_pass1",
            "read_probe", "copy_probe", "qp1_probe", "checkpoint_save", "checkpoint_load",
-           "norm_forward", "norm_backward", "norm_reduce", "ffn_forward", "ffn_recompute", "ffn_dx", "ffn_dw",
+           "norm_forward", "norm_backward", "norm_reduce", "ffn_forward", "ffn_recompute", "ffn_gradients",
            "ffn_layout", "ffn_reduce"]
 
 # msamp_activation by name
@@ -844,24 +844,29 @@ class Checkpoint:
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: int = E4M3):
         cols = int(cols)
-        for t, need, name in ((codes, cols, "codes"), (scales, -(-cols // GROUP), "scales")):
-            _device_of(t, name)
-            if t.element_size() != 1:
-                raise TypeError("%s has dtype %s, expected bytes" % (name, t.dtype))
-            if cols < 0 or t.dim() != 2 or t.shape[1] < need:
-                raise ValueError("%s has shape %s, expected at least %d columns" % (name, tuple(t.shape), need))
-            if t.stride(1) != 1 and t.shape[1] > 1:
-                raise ValueError("%s: the elements of a row must be consecutive" % name)
-        if codes.shape[0] != scales.shape[0]:
-            raise ValueError("codes has %d rows, scales %d" % (codes.shape[0], scales.shape[0]))
-        if codes.device != scales.device:
+        groups = -(-cols // GROUP)
+        dev = _device_of(codes, "codes")
+        if _device_of(scales, "scales") != dev:
             raise ValueError("scales is on %s, expected %s" % (scales.device, codes.device))
-        self.codes, self.scales, self.cols, self.fmt = codes, scales, cols, int(fmt)
-        self.rows, self.device = codes.shape[0], codes.get_device()
-        empty = self.rows == 0 or cols == 0
-        self._c = _Checkpoint(None if empty else codes.data_ptr(), codes.stride(0),
-                              None if empty else scales.data_ptr(), scales.stride(0), self.fmt)
-        self._flat = self.rows <= 1 or (codes.stride(0) >= cols and scales.stride(0) >= -(-cols // GROUP))
+        if codes.element_size() != 1 or scales.element_size() != 1:
+            raise TypeError("codes and scales must be bytes, not %s and %s" % (codes.dtype, scales.dtype))
+        if codes.dim() != 2 or scales.dim() != 2:
+            raise ValueError("codes and scales must have two dimensions")
+        (rows, width), (srows, swidth) = codes.shape, scales.shape
+        (ld, inner), (lds, sinner) = codes.stride(), scales.stride()
+        if cols < 0 or width < cols or swidth < groups:
+            raise ValueError("%d columns need codes of at least as many and scales of at least %d, not %d and %d"
+                             % (cols, groups, width, swidth))
+        if srows != rows:
+            raise ValueError("codes has %d rows, scales %d" % (rows, srows))
+        if (inner != 1 and width > 1) or (sinner != 1 and swidth > 1):
+            raise ValueError("the elements of a row of codes and scales must be consecutive")
+        self.codes, self.scales, self.cols, self.fmt, self.rows, self.device = codes, scales, cols, int(fmt), rows, dev
+        self._flat = rows <= 1 or (ld >= cols and lds >= groups)
+        if rows == 0 or cols == 0:
+            self._c = _Checkpoint(None, ld, None, lds, self.fmt)
+        else:
+            self._c = _Checkpoint(codes.data_ptr(), ld, scales.data_ptr(), lds, self.fmt)
 
     def _arg(self, name: str, device: int, shape, written: bool = False):
         if self.device != device:

@@ -1089,8 +1089,7 @@ const char* msamp_kernel_name(msamp_kernel_kind kind) {
     case MSAMP_KERNEL_NORM_REDUCE: return "norm_reduce";
     case MSAMP_KERNEL_FFN_FORWARD: return "ffn_forward";
     case MSAMP_KERNEL_FFN_RECOMPUTE: return "ffn_recompute";
-    case MSAMP_KERNEL_FFN_DX: return "ffn_dx";
-    case MSAMP_KERNEL_FFN_DW: return "ffn_dw";
+    case MSAMP_KERNEL_FFN_GRADIENTS: return "ffn_gradients";
     case MSAMP_KERNEL_FFN_LAYOUT: return "ffn_layout";
     case MSAMP_KERNEL_FFN_REDUCE: return "ffn_reduce";
     default: return "";

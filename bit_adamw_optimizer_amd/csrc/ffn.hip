@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+#include <iterator>
 #include <type_traits>
 
 #include "checkpoint.hpp"
@@ -113,7 +115,7 @@ struct Product {
   int64_t ldc0, ldc1;
   uint32_t tiles_r, tiles_c;
   // The sum over k in 'splits' parts of 'part' steps each: their sums go to
-  // 'partial', one tile after another, and are joined by k_product_sum.
+  // 'partial', one unit after another, and are joined by a second launch.
   uint32_t splits;
   int64_t part;
   float* partial;
@@ -532,14 +534,19 @@ __device__ __forceinline__ void finish(const Product& p, LDS char* lds, int64_t 
   }
 }
 
+// Bytes of LDS of a workgroup: two stages; they also hold the outgoing tiles.
+template <int FR>
+constexpr int stage_bytes() {
+  return FR * 64 * 128 + kTileC * 128;
+}
+
+// Unit 'id' of the 'n' of a product.
 template <typename T, int MODE, int FR>
-__global__ __launch_bounds__(kThreads) void k_product(Product p) {
+__device__ __forceinline__ void run_unit(const Product& p, LDS char* lds, uint32_t id, uint32_t n) {
   constexpr bool kPair = is_pair(MODE);
-  constexpr int kStage = FR * 64 * 128 + kTileC * 128;
-  __shared__ __attribute__((aligned(16))) char smem[2 * kStage];  // also holds the outgoing tiles
-  LDS char* lds = (LDS char*)smem;
+  constexpr int kStage = stage_bytes<FR>();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const Place at = place_of(p, blockIdx.x, gridDim.x);
+  const Place at = place_of(p, id, n);
   const int z = MODE == kDw ? (int)at.z : 0;
   const int64_t row0 = (int64_t)at.tr * (64 * FR), col0 = (int64_t)at.tc * (kPair ? 128 : 256);
   Along<FR> ra;
@@ -601,15 +608,15 @@ __global__ __launch_bounds__(kThreads) void k_product(Product p) {
   finish<T, MODE, FR>(p, lds, row0, col0, z, wave, lane, acc, dh);
 }
 
-// Joins the parts of a split sum, in their order, and finishes the tile.
+// Joins the parts of a split sum, in their order, and finishes the tile: unit
+// 'id' of the 'n' tiles.
 template <typename T, int MODE, int FR>
-__global__ __launch_bounds__(kThreads) void k_product_sum(Product p) {
+__device__ __forceinline__ void join_unit(const Product& p, LDS char* lds, uint32_t id, uint32_t n) {
   constexpr bool kPair = is_pair(MODE);
-  __shared__ __attribute__((aligned(16))) char smem[64 * FR * 512];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   Product one = p;
   one.splits = 1;
-  const Place at = place_of(one, blockIdx.x, gridDim.x);
+  const Place at = place_of(one, id, n);
   const int z = MODE == kDw ? (int)at.z : 0;
   const int64_t row0 = (int64_t)at.tr * (64 * FR), col0 = (int64_t)at.tc * (kPair ? 128 : 256);
   const uint32_t tiles = p.tiles_r * p.tiles_c;
@@ -643,72 +650,194 @@ __global__ __launch_bounds__(kThreads) void k_product_sum(Product p) {
               for (int e = 0; e < 4; ++e) acc.v[r][q >> 2][(q & 3) * 4 + e] += v[k][q][e];
           }
       }
-  finish<T, MODE, FR>(p, (LDS char*)smem, row0, col0, z, wave, lane, acc, dh);
+  finish<T, MODE, FR>(p, lds, row0, col0, z, wave, lane, acc, dh);
 }
 
-// How a product is cut: rows of a tile (64 * fr) and parts of the sum over k.
-struct Cut {
-  int fr;
-  uint32_t tiles_r, tiles_c, splits;
-  int64_t part;
-  int64_t partial_bytes;
-};
-
-// A part takes a workgroup of the joining kernel this long at least.
-double join_us(int fr, int64_t splits, int64_t bytes) {
-  const double each = splits * (fr == 4 ? 2.0 : (fr == 2 ? 0.6 : 0.25)), all = bytes * 2 / 8e6;
-  return 3.5 + (each > all ? each : all);
-}
-
-// The cut with the least estimated time, by constants fitted to measurements
-// of every cut of 14 problems (tokens 64 to 8192, hidden 128 to 8192, 128 to
-// 13824 inner units; on these the chosen cut is within 2% of the best one on
-// average, 18% at most): a step of a tile of 64, 128 or 256 rows takes 0.8, 1.05
-// or 1.8 us, its start and finish 2, 7.5 or 13 us, and joining parts 3 us and
-// two passes over them at 8 TB/s. One workgroup a compute unit runs at a time.
-Cut choose_cut(int mode, int64_t R, int64_t C, int64_t K) {
-  Cut best = {};
-  double least = 1e30;
-  const int64_t steps = (K + kStepK - 1) / kStepK * (mode == kDx ? 2 : 1);
-  const int tc = is_pair(mode) ? 128 : 256;
-  const int64_t nc = (C + tc - 1) / tc, zs = mode == kDw ? 2 : 1;
-  for (int fr = 4; fr >= 1; fr /= 2) {
-    const int64_t nr = (R + 64 * fr - 1) / (64 * fr), tiles = nr * nc * zs;
-    const double step_us = fr == 4 ? 1.8 : (fr == 2 ? 1.05 : 0.8), ends_us = fr == 4 ? 13.0 : (fr == 2 ? 7.5 : 2.0);
-    const int64_t slots = 256;
-    for (int64_t splits = 1; splits <= 64 && (splits == 1 || steps / splits >= 2); ++splits) {
-      const int64_t part = (steps + splits - 1) / splits;
-      const int64_t used = (steps + part - 1) / part;
-      if (used != splits) continue;
-      const int64_t rounds = (tiles * splits + slots - 1) / slots;
-      const int64_t bytes = splits == 1 ? 0 : tiles * splits * (64 * fr * kTileC * 4);
-      if (bytes > (int64_t)1 << 30) break;
-      const double t = rounds * (part * step_us + ends_us) + (splits == 1 ? 0.0 : join_us(fr, splits, bytes));
-      if (t < least) {
-        least = t;
-        best = {fr, (uint32_t)nr, (uint32_t)nc, (uint32_t)splits, part, bytes};
-      }
-      if (splits > 1 && rounds > 4) break;
-    }
-  }
-  return best;
+// Gate and up projections (kForward, kRecompute).
+template <typename T, int MODE, int FR>
+__global__ __launch_bounds__(kThreads) void k_projections(Product p) {
+  __shared__ __attribute__((aligned(16))) char smem[2 * stage_bytes<FR>()];
+  run_unit<T, MODE, FR>(p, (LDS char*)smem, blockIdx.x, gridDim.x);
 }
 
 template <typename T, int MODE, int FR>
-hipError_t launch_tiles(const Product& p, bool sum, hipStream_t s) {
-  const uint32_t tiles = p.tiles_r * p.tiles_c * (MODE == kDw ? 2 : 1);
-  if (sum) k_product_sum<T, MODE, FR><<<dim3(tiles), dim3(kThreads), 0, s>>>(p);
-  else k_product<T, MODE, FR><<<dim3(tiles * p.splits), dim3(kThreads), 0, s>>>(p);
+__global__ __launch_bounds__(kThreads) void k_projections_join(Product p) {
+  __shared__ __attribute__((aligned(16))) char smem[64 * FR * 512];
+  join_unit<T, MODE, FR>(p, (LDS char*)smem, blockIdx.x, gridDim.x);
+}
+
+// dx and the weights' gradients in one launch: nx units of dx first (their sums
+// are the longer ones), then those of the weights.
+template <typename T, int FR>
+__global__ __launch_bounds__(kThreads) void k_gradients(Product x, Product w, uint32_t nx) {
+  __shared__ __attribute__((aligned(16))) char smem[2 * stage_bytes<FR>()];
+  if (blockIdx.x < nx) run_unit<T, kDx, FR>(x, (LDS char*)smem, blockIdx.x, nx);
+  else run_unit<T, kDw, FR>(w, (LDS char*)smem, blockIdx.x - nx, gridDim.x - nx);
+}
+
+// The same for the tiles whose sums were split (none of dx: nx = 0; none of the
+// weights: all of the grid is nx).
+template <typename T, int FR>
+__global__ __launch_bounds__(kThreads) void k_gradients_join(Product x, Product w, uint32_t nx) {
+  __shared__ __attribute__((aligned(16))) char smem[64 * FR * 512];
+  if (blockIdx.x < nx) join_unit<T, kDx, FR>(x, (LDS char*)smem, blockIdx.x, nx);
+  else join_unit<T, kDw, FR>(w, (LDS char*)smem, blockIdx.x - nx, gridDim.x - nx);
+}
+
+// How a product is cut: its tiles, and parts of the sum over k.
+struct Cut {
+  uint32_t tiles_r, tiles_c, splits;
+  int64_t part;
+  int64_t bytes;  // of partial sums
+};
+
+int64_t steps_of(int mode, int64_t K) { return (K + kStepK - 1) / kStepK * (mode == kDx ? 2 : 1); }
+
+// Units (workgroups) of a cut, and tiles.
+int64_t tiles_of(int mode, const Cut& c) { return (int64_t)c.tiles_r * c.tiles_c * (mode == kDw ? 2 : 1); }
+
+// The cut with tiles of 64 * fr rows and the sums in 'splits' parts of whole
+// steps (false: there is none).
+bool cut_of(int mode, int fr, int64_t splits, int64_t R, int64_t C, int64_t K, Cut* c) {
+  const int64_t steps = steps_of(mode, K), tc = is_pair(mode) ? 128 : 256;
+  const int64_t part = (steps + splits - 1) / splits;
+  if ((steps + part - 1) / part != splits || (splits > 1 && part < 2)) return false;
+  *c = {(uint32_t)((R + 64 * fr - 1) / (64 * fr)), (uint32_t)((C + tc - 1) / tc), (uint32_t)splits, part, 0};
+  if (splits > 1) c->bytes = tiles_of(mode, *c) * splits * (64 * fr * kTileC * 4);
+  return c->bytes <= (int64_t)1 << 30;
+}
+
+// Times in us, fitted to measurements of every cut of 14 problems (tokens 64 to
+// 8192, hidden 128 to 8192, 128 to 13824 inner units; on these the cut they
+// choose is within 2% of the best one on average, 18% at most). One workgroup
+// a compute unit runs at a time.
+double unit_us(int fr, const Cut& c) {
+  return c.part * (fr == 4 ? 1.8 : (fr == 2 ? 1.05 : 0.8)) + (fr == 4 ? 13.0 : (fr == 2 ? 7.5 : 2.0));
+}
+// Joining parts: each takes a workgroup so long at least, and all pass twice
+// through memory at 8 TB/s.
+double join_us(int fr, const Cut& c) {
+  if (c.splits == 1) return 0.0;
+  const double each = c.splits * (fr == 4 ? 2.0 : (fr == 2 ? 0.6 : 0.25)), all = c.bytes * 2 / 8e6;
+  return 3.5 + (each > all ? each : all);
+}
+
+constexpr int kUnits = 256;
+// Numbers of parts that are looked at (a plan is made on the host at each
+// call, in about a microsecond).
+constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+
+struct Candidate {
+  Cut cut;
+  double units, unit, join;
+};
+
+// The cuts with tiles of 64 * fr rows that fill the device at most four times
+// over when they split sums.
+int candidates(int mode, int fr, int64_t R, int64_t C, int64_t K, Candidate* out) {
+  int n = 0;
+  for (int splits : kSplits) {
+    Candidate& c = out[n];
+    if (!cut_of(mode, fr, splits, R, C, K, &c.cut)) continue;
+    c.units = (double)tiles_of(mode, c.cut) * splits;
+    if (splits > 1 && c.units > 4 * kUnits) break;
+    c.unit = unit_us(fr, c.cut);
+    c.join = join_us(fr, c.cut);
+    ++n;
+  }
+  return n;
+}
+
+// The cut of a projection with the least estimated time, and its fr.
+int choose_projection(int mode, int64_t R, int64_t C, int64_t K, Cut* best) {
+  double least = 1e30;
+  int fr_best = 4;
+  Candidate c[std::size(kSplits)];
+  for (int fr = 4; fr >= 1; fr /= 2) {
+    const int n = candidates(mode, fr, R, C, K, c);
+    for (int i = 0; i < n; ++i) {
+      const double t = std::ceil(c[i].units / kUnits) * c[i].unit + c[i].join;
+      if (t < least) {
+        least = t;
+        *best = c[i].cut;
+        fr_best = fr;
+      }
+    }
+  }
+  return fr_best;
+}
+
+// The cuts of both gradients, which run side by side with the same fr: the
+// time of the longer unit, or of all of them and a quarter of the longer one
+// (fitted to 18 problems: within 7% of the best cut on average, 27% at most).
+int choose_gradients(int64_t T, int64_t K, int64_t F, Cut* x, Cut* w) {
+  double least = 1e30;
+  int fr_best = 4;
+  Candidate cx[std::size(kSplits)], cw[std::size(kSplits)];
+  for (int fr = 4; fr >= 1; fr /= 2) {
+    const int nx = candidates(kDx, fr, T, K, F, cx), nw = candidates(kDw, fr, F, K, T, cw);
+    for (int i = 0; i < nx; ++i)
+      for (int j = 0; j < nw; ++j) {
+        double t = cx[i].unit > cw[j].unit ? cx[i].unit : cw[j].unit;
+        if (cx[i].units + cw[j].units > kUnits) {
+          const double all = (cx[i].units * cx[i].unit + cw[j].units * cw[j].unit) / kUnits + 0.25 * t;
+          t = all > t ? all : t;
+        }
+        t += cx[i].join > cw[j].join ? cx[i].join : cw[j].join;
+        if (t < least) {
+          least = t;
+          *x = cx[i].cut;
+          *w = cw[j].cut;
+          fr_best = fr;
+        }
+      }
+  }
+  return fr_best;
+}
+
+void apply(const Cut& c, float* partial, Product* p) {
+  p->tiles_r = c.tiles_r, p->tiles_c = c.tiles_c, p->splits = c.splits, p->part = c.part, p->partial = partial;
+}
+
+template <typename T, int MODE, int FR>
+hipError_t launch_projections(const Product& p, bool join, hipStream_t s) {
+  const uint32_t tiles = p.tiles_r * p.tiles_c;
+  if (join) k_projections_join<T, MODE, FR><<<dim3(tiles), dim3(kThreads), 0, s>>>(p);
+  else k_projections<T, MODE, FR><<<dim3(tiles * p.splits), dim3(kThreads), 0, s>>>(p);
   return hipGetLastError();
 }
 
 template <int MODE>
-hipError_t launch_product(int dtype, int fr, const Product& p, bool sum, hipStream_t s) {
+hipError_t launch_projections(int dtype, int fr, const Product& p, bool join, hipStream_t s) {
   if (dtype == MSAMP_F16)
-    return fr == 4 ? launch_tiles<f16, MODE, 4>(p, sum, s)
-                   : (fr == 2 ? launch_tiles<f16, MODE, 2>(p, sum, s) : launch_tiles<f16, MODE, 1>(p, sum, s));
-  return fr == 4 ? launch_tiles<bf16, MODE, 4>(p, sum, s)
-                 : (fr == 2 ? launch_tiles<bf16, MODE, 2>(p, sum, s) : launch_tiles<bf16, MODE, 1>(p, sum, s));
+    return fr == 4 ? launch_projections<f16, MODE, 4>(p, join, s)
+                   : (fr == 2 ? launch_projections<f16, MODE, 2>(p, join, s) : launch_projections<f16, MODE, 1>(p, join, s));
+  return fr == 4 ? launch_projections<bf16, MODE, 4>(p, join, s)
+                 : (fr == 2 ? launch_projections<bf16, MODE, 2>(p, join, s) : launch_projections<bf16, MODE, 1>(p, join, s));
+}
+
+template <typename T, int FR>
+hipError_t launch_gradients(const Product& x, const Product& w, bool join, hipStream_t s) {
+  uint32_t nx = x.tiles_r * x.tiles_c, nw = 2 * w.tiles_r * w.tiles_c;
+  if (join) {
+    nx = x.splits > 1 ? nx : 0;
+    nw = w.splits > 1 ? nw : 0;
+    k_gradients_join<T, FR><<<dim3(nx + nw), dim3(kThreads), 0, s>>>(x, w, nx);
+  } else {
+    nx *= x.splits;
+    k_gradients<T, FR><<<dim3(nx + nw * w.splits), dim3(kThreads), 0, s>>>(x, w, nx);
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_gradients(int fr, const Product& x, const Product& w, bool join, hipStream_t s) {
+  return fr == 4 ? launch_gradients<T, 4>(x, w, join, s)
+                 : (fr == 2 ? launch_gradients<T, 2>(x, w, join, s) : launch_gradients<T, 1>(x, w, join, s));
+}
+
+hipError_t launch_gradients(int dtype, int fr, const Product& x, const Product& w, bool join, hipStream_t s) {
+  return dtype == MSAMP_F16 ? launch_gradients<f16>(fr, x, w, join, s) : launch_gradients<bf16>(fr, x, w, join, s);
 }
 
 // Hands out pieces of the workspace (or only counts them).
@@ -723,17 +852,34 @@ struct Arena {
   }
 };
 
-// Plans a product (taking its partial sums' workspace) and runs it.
+constexpr int64_t kMaxUnits = UINT32_MAX / kThreads;
+
+// Plans the tiled projections (taking their partial sums' workspace) and runs
+// them.
 template <int MODE>
-msamp_status product(msamp_kernel_kind kind, int dtype, Product p, Arena& ws, bool run, hipStream_t s) {
-  const Cut c = choose_cut(MODE, p.R, p.C, p.K);
-  if ((int64_t)c.tiles_r * c.tiles_c * c.splits * 2 > (int64_t)UINT32_MAX / kThreads)
-    return fail(MSAMP_E_INVALID_ARG, "the product has too many tiles");
-  p.tiles_r = c.tiles_r, p.tiles_c = c.tiles_c, p.splits = c.splits, p.part = c.part;
-  p.partial = (float*)ws.take(c.partial_bytes);
+msamp_status tiled_projections(msamp_kernel_kind kind, int dtype, Product p, Arena& ws, bool run, hipStream_t s) {
+  Cut c;
+  const int fr = choose_projection(MODE, p.R, p.C, p.K, &c);
+  if (tiles_of(MODE, c) * c.splits > kMaxUnits) return fail(MSAMP_E_INVALID_ARG, "the product has too many tiles");
+  apply(c, (float*)ws.take(c.bytes), &p);
   if (!run) return MSAMP_OK;
-  MSAMP_LAUNCH(kind, s, launch_product<MODE>(dtype, c.fr, p, false, s));
-  if (c.splits > 1) MSAMP_LAUNCH(MSAMP_KERNEL_FFN_REDUCE, s, launch_product<MODE>(dtype, c.fr, p, true, s));
+  MSAMP_LAUNCH(kind, s, launch_projections<MODE>(dtype, fr, p, false, s));
+  if (c.splits > 1) MSAMP_LAUNCH(MSAMP_KERNEL_FFN_REDUCE, s, launch_projections<MODE>(dtype, fr, p, true, s));
+  return MSAMP_OK;
+}
+
+// The same for both gradients.
+msamp_status gradients(int dtype, Product x, Product w, Arena& ws, bool run, hipStream_t s) {
+  Cut cx, cw;
+  const int fr = choose_gradients(x.R, x.C, x.K, &cx, &cw);
+  if (tiles_of(kDx, cx) * cx.splits + tiles_of(kDw, cw) * cw.splits > kMaxUnits)
+    return fail(MSAMP_E_INVALID_ARG, "the product has too many tiles");
+  apply(cx, (float*)ws.take(cx.bytes), &x);
+  apply(cw, (float*)ws.take(cw.bytes), &w);
+  if (!run) return MSAMP_OK;
+  MSAMP_LAUNCH(MSAMP_KERNEL_FFN_GRADIENTS, s, launch_gradients(dtype, fr, x, w, false, s));
+  if (cx.splits > 1 || cw.splits > 1)
+    MSAMP_LAUNCH(MSAMP_KERNEL_FFN_REDUCE, s, launch_gradients(dtype, fr, x, w, true, s));
   return MSAMP_OK;
 }
 
@@ -791,6 +937,16 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(Product p) {
   // rows of this block's weights that exist (none: columns that pad dg | du)
   const int64_t left = p.C - col0, cols = left < 0 ? 0 : (left < 16 ? left : 16);
   const int piece = (lane >> 4) * 16;  // this lane's 16 k of a chunk of 64
+  constexpr int kOuts = (NT * 256 + kFewThreads - 1) / kFewThreads;  // values of h a thread ends with
+  T dh[MODE == kRecompute ? kOuts : 1];
+  if constexpr (MODE == kRecompute) {  // here early, as the sums
+#pragma unroll
+    for (int k = 0; k < kOuts; ++k) {
+      const int i = threadIdx.x + k * kFewThreads;
+      const int64_t row = 16 * (i / 256) + ((i / 16) & 15), col = col0 + (i & 15);
+      dh[k] = i < NT * 256 && row < p.R && col < p.C ? ((const GLOBAL T*)p.dh)[row * p.lddh + col] : (T)0.0f;
+    }
+  }
   f32x4 acc[NT][2] = {};
   const int chunks = (int)(ALIGNED ? (p.K + 63) / 64 : p.K / 64);
   auto multiply = [&](const u32x4(&g)[2], const u32x4(&u)[2], const u32x4(&x)[NT][2]) {
@@ -881,7 +1037,10 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(Product p) {
   }
   __syncthreads();
   // element e of sums[..][lane]: inner unit 4 * (lane / 16) + e, token lane % 16
-  for (int i = threadIdx.x; i < NT * 256; i += kFewThreads) {
+#pragma unroll
+  for (int k = 0; k < kOuts; ++k) {
+    const int i = threadIdx.x + k * kFewThreads;
+    if (i >= NT * 256) break;
     const int t = i / 256, token = (i / 16) & 15, unit = i & 15;
     const int64_t row = 16 * t + token, col = col0 + unit;
     if (row >= p.R) continue;
@@ -896,10 +1055,9 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(Product p) {
     with_act(p.act, [&](auto act) { act_and_grad<decltype(act)::value>(g, &a, &d); });
     if (col < p.C && p.out0 != nullptr) ((GLOBAL T*)p.out0)[row * p.ldo0 + col] = from_f32<T>(a * u);
     if constexpr (MODE == kRecompute) {
-      const float dh = col < p.C ? to_f32(((const GLOBAL T*)p.dh)[row * p.lddh + col]) : 0.0f;
       GLOBAL T* o = (GLOBAL T*)p.dgu + row * (2 * p.half) + col;
-      o[0] = from_f32<T>(dh * u * d);
-      o[p.half] = from_f32<T>(dh * a);
+      o[0] = from_f32<T>(to_f32(dh[k]) * u * d);
+      o[p.half] = from_f32<T>(to_f32(dh[k]) * a);
     }
   }
 }
@@ -946,7 +1104,7 @@ bool few_rows(int64_t R, int64_t C, int64_t K) {
 // The gate and up projections by the kernel that suits the number of tokens.
 template <int MODE>
 msamp_status projections(msamp_kernel_kind kind, int dtype, const Product& p, Arena& ws, bool run, hipStream_t s) {
-  if (!few_rows(p.R, p.C, p.K)) return product<MODE>(kind, dtype, p, ws, run, s);
+  if (!few_rows(p.R, p.C, p.K)) return tiled_projections<MODE>(kind, dtype, p, ws, run, s);
   if (run) MSAMP_LAUNCH(kind, s, launch_few<MODE>(dtype, p, s));
   return MSAMP_OK;
 }
@@ -1099,29 +1257,25 @@ msamp_status backward(const msamp_gated_ffn& a, Arena& ws, bool run, hipStream_t
   p.out0 = a.h, p.ldo0 = a.ldh;
   p.dh = a.dh, p.lddh = a.lddh;
   p.dgu = dgu, p.half = half;
-  // the three products' partial sums take turns in the same memory
+  // the partial sums of both launches take turns in the same memory
   const int64_t mark = ws.used;
-  int64_t most = mark;
   MSAMP_TRY(projections<kRecompute>(MSAMP_KERNEL_FFN_RECOMPUTE, a.dtype, p, ws, run, s));
-  most = ws.used > most ? ws.used : most;
+  const int64_t most = ws.used;
   ws.used = mark;
 
-  p = {};
-  p.R = T, p.C = K, p.K = F;
-  p.r0 = dgu, p.r1 = run ? dgu + half * 2 : nullptr, p.ldr = 2 * half;
-  p.c0 = g.p, p.ldc0 = g.ld, p.c1 = u.p, p.ldc1 = u.ld;
-  p.out0 = a.dx, p.ldo0 = a.lddx;
-  MSAMP_TRY(product<kDx>(MSAMP_KERNEL_FFN_DX, a.dtype, p, ws, run, s));
-  most = ws.used > most ? ws.used : most;
-  ws.used = mark;
+  Product dx = {};
+  dx.R = T, dx.C = K, dx.K = F;
+  dx.r0 = dgu, dx.r1 = run ? dgu + half * 2 : nullptr, dx.ldr = 2 * half;
+  dx.c0 = g.p, dx.ldc0 = g.ld, dx.c1 = u.p, dx.ldc1 = u.ld;
+  dx.out0 = a.dx, dx.ldo0 = a.lddx;
 
-  p = {};
-  p.R = F, p.C = K, p.K = T;
-  p.r0 = dgu, p.r1 = run ? dgu + half * 2 : nullptr, p.ldr = 2 * half;
-  p.c0 = x.p, p.ldc0 = x.ld;
-  p.out0 = a.dw_gate, p.ldo0 = a.ld_dw_gate, p.out1 = a.dw_up, p.ldo1 = a.ld_dw_up;
-  p.out_f32 = a.dw_dtype == MSAMP_F32, p.accumulate = a.dw_accumulate;
-  MSAMP_TRY(product<kDw>(MSAMP_KERNEL_FFN_DW, a.dtype, p, ws, run, s));
+  Product dw = {};
+  dw.R = F, dw.C = K, dw.K = T;
+  dw.r0 = dx.r0, dw.r1 = dx.r1, dw.ldr = dx.ldr;
+  dw.c0 = x.p, dw.ldc0 = x.ld;
+  dw.out0 = a.dw_gate, dw.ldo0 = a.ld_dw_gate, dw.out1 = a.dw_up, dw.ldo1 = a.ld_dw_up;
+  dw.out_f32 = a.dw_dtype == MSAMP_F32, dw.accumulate = a.dw_accumulate;
+  MSAMP_TRY(gradients(a.dtype, dx, dw, ws, run, s));
   ws.used = ws.used > most ? ws.used : most;
   return MSAMP_OK;
 }

@@ -79,13 +79,25 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// Sums of a and b over the WAVES waves of a row, GROUPS rows side by side in
-// the workgroup. 'turn' alternates between two sets of partials, so that one
-// barrier a sum is enough.
-template <int WAVES, int GROUPS>
-__device__ __forceinline__ void group_sum2(float& a, float& b, int turn) {
-  a = wave_sum(a);
-  b = wave_sum(b);
+// Sum over each 16 or 32 neighbouring lanes, given to all of them.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (LANES == 64) return wave_sum(v);
+  v = add_dpp<0xB1, 0xf>(v);   // quad_perm: 1 0 3 2
+  v = add_dpp<0x4E, 0xf>(v);   // quad_perm: 2 3 0 1
+  v = add_dpp<0x141, 0xf>(v);  // row_half_mirror: the other four of eight
+  v = add_dpp<0x140, 0xf>(v);  // row_mirror: the other eight
+  if constexpr (LANES == 32) v += __shfl_xor(v, 16, 64);
+  return v;
+}
+
+// Sums of a and b over the lanes of a row: LANES neighbours of a wave, or (64)
+// WAVES whole waves, GROUPS rows side by side in the workgroup. 'turn'
+// alternates between two sets of partials, so that one barrier a sum is enough.
+template <int LANES, int WAVES, int GROUPS>
+__device__ __forceinline__ void row_sum2(float& a, float& b, int turn) {
+  a = lanes_sum<LANES>(a);
+  b = lanes_sum<LANES>(b);
   if constexpr (WAVES > 1) {
     __shared__ float part[2][GROUPS][2][WAVES];
     const int wave = threadIdx.x >> 6, group = wave / WAVES;
@@ -130,13 +142,14 @@ __device__ __forceinline__ void load_x8(const NormArgs& a, int64_t row, int64_t 
     load_ckpt8(a.ck.fmt, a.ck.codes + row * a.ck.ld, a.ck.scales + row * a.ck.ld_scales, col, n, f);
 }
 
-// One row per WAVES waves; a lane holds NCH pieces of 8 columns.
-template <typename T, int WAVES, int NCH>
+// One row per LANES lanes of a wave or per WAVES waves; a lane holds NCH pieces
+// of 8 columns.
+template <typename T, int LANES, int WAVES, int NCH>
 __global__ __launch_bounds__(norm_block<WAVES>()) void k_norm_forward(NormArgs a) {
-  constexpr int kLanes = WAVES * 64;
-  const int lane = WAVES == 1 ? (threadIdx.x & 63) : threadIdx.x;
-  const int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-  if (row >= a.rows) return;  // whole waves; with WAVES > 1 no row is beyond
+  constexpr int kLanes = WAVES * LANES;
+  const int lane = threadIdx.x % kLanes;
+  const int64_t row = (int64_t)blockIdx.x * (norm_block<WAVES>() / kLanes) + threadIdx.x / kLanes;
+  if (row >= a.rows) return;  // all lanes of a row; with WAVES > 1 no row is beyond
   float v[NCH][8];
   int n[NCH];
   float sum = 0.0f, sq = 0.0f;
@@ -160,7 +173,7 @@ __global__ __launch_bounds__(norm_block<WAVES>()) void k_norm_forward(NormArgs a
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
       for (int k = 0; k < 8; ++k) sum += v[c][k];
-    group_sum2<WAVES, 1>(sum, sq, 0);
+    row_sum2<LANES, WAVES, 1>(sum, sq, 0);
     mu = sum * inv;
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
@@ -172,7 +185,7 @@ __global__ __launch_bounds__(norm_block<WAVES>()) void k_norm_forward(NormArgs a
   for (int c = 0; c < NCH; ++c)
 #pragma unroll
     for (int k = 0; k < 8; ++k) sq = __builtin_fmaf(v[c][k], v[c][k], sq);
-  group_sum2<WAVES, 1>(sq, sum, 1);
+  row_sum2<LANES, WAVES, 1>(sq, sum, 1);
   const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(sq, inv, a.eps));
   if (lane == 0) {
     if (a.mean != nullptr) a.mean[row] = mu;
@@ -252,27 +265,33 @@ __device__ __forceinline__ void unpack(const RawRow<T, true, NCH>& r, int fmt, i
   decode_group8(fmt, r.q[c], r.s[c], f);
 }
 
-// Each workgroup walks over rows, GROUPS at a time, one per WAVES waves; a
-// lane holds the same NCH pieces of 8 columns throughout and sums their share
+// Each workgroup walks over rows: GROUPS sets of WAVES waves, each with a row,
+// or with 64 / LANES rows of LANES lanes. A lane holds the same NCH pieces of 8 columns throughout and sums their share
 // of dweight and dbias in registers. The next row is loaded while the current
 // one is worked on. TAIL: the columns end inside a piece. Lanes behind the
 // last column work on zeros, which add nothing to a row's sums (x and dy are
 // 0 there, so dy * xh is 0 or, in a row whose statistics are not finite
 // anyway, NaN).
-template <typename T, bool CK, bool TAIL, int WAVES, int NCH, int GROUPS>
+template <typename T, bool CK, bool TAIL, int LANES, int WAVES, int NCH, int GROUPS>
 __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a) {
-  constexpr int kLanes = WAVES * 64;
-  const int group = (int)threadIdx.x / kLanes, lane = (int)threadIdx.x % kLanes;
-  const int64_t stride = (int64_t)gridDim.x * GROUPS;
+  constexpr int kLanes = WAVES * LANES, kRows = WAVES * GROUPS * 64 / kLanes;
+  const int lane = (int)threadIdx.x % kLanes;
+  const int64_t stride = (int64_t)gridDim.x * kRows;
   const int cols = (int)a.cols;
   const float inv = 1.0f / (float)cols;
   const bool centered = a.mean != nullptr, bias = a.dbias != nullptr;
+  // With several pieces a lane, registers are short: the weights are then read
+  // for every row (from cache), and the next row is not loaded ahead.
+  constexpr bool kKeep = NCH == 1;
   float w[NCH][8], sw[NCH][8], sb[NCH][8];
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
+  auto load_weights = [&](int c) {
     const int col = (c * kLanes + lane) * 8;
     const int n = cols - col < 8 ? (cols > col ? cols - col : 0) : 8;
     load_weight8<T>(a.weight, a.weight_f32, col, n, 1.0f, w[c]);
+  };
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    if constexpr (kKeep) load_weights(c);
 #pragma unroll
     for (int k = 0; k < 8; ++k) sw[c][k] = sb[c][k] = 0.0f;
   }
@@ -287,13 +306,14 @@ __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a
     if (centered) m = a.mean[row];
     r = a.rstd[row];
   };
-  int64_t row = (int64_t)blockIdx.x * GROUPS + group;
-  fetch(row, rx, rg, mu, rstd);
-  // every group makes the same number of turns: the sums have a barrier
+  int64_t row = (int64_t)blockIdx.x * kRows + (int)threadIdx.x / kLanes;
+  if constexpr (kKeep) fetch(row, rx, rg, mu, rstd);
+  // all rows of a workgroup make the same number of turns: the sums have a barrier
   int turn = 0;
-  for (int64_t base = (int64_t)blockIdx.x * GROUPS; base < a.rows; base += stride, row += stride) {
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows; base += stride, row += stride) {
     const bool live = row < a.rows;
-    fetch(row + stride, nx, ng, nmu, nrstd);
+    if constexpr (kKeep) fetch(row + stride, nx, ng, nmu, nrstd);
+    else fetch(row, rx, rg, mu, rstd);
     float xh[NCH][8], g[NCH][8];
     float c1 = 0.0f, c2 = 0.0f;
     if (live) {
@@ -301,6 +321,7 @@ __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a
       for (int c = 0; c < NCH; ++c) {
         unpack<T, NCH>(rx, a.ck.fmt, c, xh[c]);
         unpack<T, NCH>(rg, 0, c, g[c]);
+        if constexpr (!kKeep) load_weights(c);
         if (centered) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) xh[c][k] -= mu;
@@ -322,7 +343,7 @@ __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a
         }
       }
     }
-    group_sum2<WAVES, GROUPS>(c1, c2, turn);
+    row_sum2<LANES, WAVES, GROUPS>(c1, c2, turn);
     turn ^= 1;
     if (live) {
       c1 *= inv * rstd;
@@ -338,16 +359,30 @@ __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a
         }
       }
     }
-    rx = nx;
-    rg = ng;
-    mu = nmu;
-    rstd = nrstd;
+    if constexpr (kKeep) {
+      rx = nx;
+      rg = ng;
+      mu = nmu;
+      rstd = nrstd;
+    }
   }
-  if (a.partial == nullptr) return;
+  if (a.dweight == nullptr && a.dbias == nullptr) return;
+  const int group = (int)threadIdx.x / (WAVES * 64);
+  if constexpr (LANES < 64) {  // a wave's rows
+#pragma unroll
+    for (int off = LANES; off < 64; off *= 2)
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          sw[c][k] += __shfl_xor(sw[c][k], off, 64);
+          sb[c][k] += __shfl_xor(sb[c][k], off, 64);
+        }
+  }
   if constexpr (GROUPS > 1) {  // the groups' sums of the same columns, in a fixed order
     __shared__ float acc[2][NCH * kLanes * 8];
     for (int t = 0; t < GROUPS; ++t) {
-      if (group == t) {
+      if (group == t && (LANES == 64 || (int)(threadIdx.x & 63) < LANES)) {
 #pragma unroll
         for (int c = 0; c < NCH; ++c)
 #pragma unroll
@@ -363,17 +398,34 @@ __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a
       }
       __syncthreads();
     }
-    if (group != GROUPS - 1) return;
+    if (group != GROUPS - 1 || (LANES < 64 && (int)(threadIdx.x & 63) >= LANES)) return;
   }
-  float* pw = a.partial + (int64_t)blockIdx.x * a.cols;
-  float* pb = pw + a.nparts * a.cols;
+  // one workgroup alone has the whole sums; several leave theirs for k_norm_reduce
+  const bool alone = a.partial == nullptr;
+  float* pw = alone ? a.dweight : a.partial + (int64_t)blockIdx.x * a.cols;
+  float* pb = alone ? a.dbias : pw + a.nparts * a.cols;
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int col = (c * kLanes + lane) * 8;
     const int n = TAIL && cols - col < 8 ? cols - col : 8;
     if (col < cols) {
-      if (a.dweight != nullptr) store8(pw + col, n, sw[c]);
-      if (a.dbias != nullptr) store8(pb + col, n, sb[c]);
+      float old[8];
+      if (a.dweight != nullptr) {
+        if (alone && a.accumulate) {
+          load8(pw + col, n, old);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sw[c][k] += old[k];
+        }
+        store8(pw + col, n, sw[c]);
+      }
+      if (a.dbias != nullptr) {
+        if (alone && a.accumulate) {
+          load8(pb + col, n, old);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sb[c][k] += old[k];
+        }
+        store8(pb + col, n, sb[c]);
+      }
     }
   }
 }
@@ -400,32 +452,35 @@ __global__ __launch_bounds__(1024) void k_norm_reduce(NormArgs a) {
   }
 }
 
-template <typename T, int WAVES, int NCH>
+template <typename T, int LANES, int WAVES, int NCH>
 void norm_fwd(const NormArgs& a, hipStream_t s) {
-  const int64_t blocks = WAVES == 1 ? (a.rows + 3) / 4 : a.rows;
-  k_norm_forward<T, WAVES, NCH><<<dim3((unsigned)blocks), dim3(norm_block<WAVES>()), 0, s>>>(a);
+  constexpr int kRows = norm_block<WAVES>() / (WAVES * LANES);
+  k_norm_forward<T, LANES, WAVES, NCH>
+      <<<dim3((unsigned)((a.rows + kRows - 1) / kRows)), dim3(norm_block<WAVES>()), 0, s>>>(a);
 }
-template <typename T, bool CK, int WAVES, int NCH, int GROUPS>
+template <typename T, bool CK, int LANES, int WAVES, int NCH, int GROUPS>
 void norm_bwd_of(const NormArgs& a, hipStream_t s) {
   const dim3 g((unsigned)a.nparts), b(WAVES * GROUPS * 64);
-  if (a.cols % 8 == 0) k_norm_backward<T, CK, false, WAVES, NCH, GROUPS><<<g, b, 0, s>>>(a);
-  else k_norm_backward<T, CK, true, WAVES, NCH, GROUPS><<<g, b, 0, s>>>(a);
+  if (a.cols % 8 == 0) k_norm_backward<T, CK, false, LANES, WAVES, NCH, GROUPS><<<g, b, 0, s>>>(a);
+  else k_norm_backward<T, CK, true, LANES, WAVES, NCH, GROUPS><<<g, b, 0, s>>>(a);
 }
-template <typename T, int WAVES, int NCH, int GROUPS>
+template <typename T, int LANES, int WAVES, int NCH, int GROUPS>
 void norm_bwd(const NormArgs& a, hipStream_t s) {
-  if (a.x != nullptr) norm_bwd_of<T, false, WAVES, NCH, GROUPS>(a, s);
-  else norm_bwd_of<T, true, WAVES, NCH, GROUPS>(a, s);
+  if (a.x != nullptr) norm_bwd_of<T, false, LANES, WAVES, NCH, GROUPS>(a, s);
+  else norm_bwd_of<T, true, LANES, WAVES, NCH, GROUPS>(a, s);
 }
 
 template <typename T>
 void norm_fwd_any(const NormArgs& a, hipStream_t s) {
-  if (a.cols <= 512) norm_fwd<T, 1, 1>(a, s);
-  else if (a.cols <= 1024) norm_fwd<T, 1, 2>(a, s);
-  else if (a.cols <= 2048) norm_fwd<T, 1, 4>(a, s);
-  else if (a.cols <= 4096) norm_fwd<T, 4, 2>(a, s);
-  else if (a.cols <= 8192) norm_fwd<T, 4, 4>(a, s);
-  else if (a.cols <= 16384) norm_fwd<T, 16, 2>(a, s);
-  else norm_fwd<T, 16, 4>(a, s);
+  if (a.cols <= 128) norm_fwd<T, 16, 1, 1>(a, s);
+  else if (a.cols <= 256) norm_fwd<T, 32, 1, 1>(a, s);
+  else if (a.cols <= 512) norm_fwd<T, 64, 1, 1>(a, s);
+  else if (a.cols <= 1024) norm_fwd<T, 64, 1, 2>(a, s);
+  else if (a.cols <= 2048) norm_fwd<T, 64, 1, 4>(a, s);
+  else if (a.cols <= 4096) norm_fwd<T, 64, 4, 2>(a, s);
+  else if (a.cols <= 8192) norm_fwd<T, 64, 4, 4>(a, s);
+  else if (a.cols <= 16384) norm_fwd<T, 64, 16, 2>(a, s);
+  else norm_fwd<T, 64, 16, 4>(a, s);
 }
 // Waves of a row, pieces of a lane and rows side by side of the backward pass:
 // one piece of 8 columns a lane wherever a workgroup can be wide enough (with
@@ -433,17 +488,22 @@ void norm_fwd_any(const NormArgs& a, hipStream_t s) {
 // 8,192 rows of 768 columns took 22 us against 15). At most 256 workgroups of
 // wide rows (one per compute unit, whose partial sums are 3% of the traffic),
 // 512 of narrow ones.
-int norm_groups(int64_t cols) { return cols <= 512 ? 8 : (cols <= 2048 ? 4 : (cols <= 4096 ? 2 : 1)); }
+int norm_rows(int64_t cols) {
+  if (cols <= 512) return cols <= 128 ? 32 : (cols <= 256 ? 16 : 8);
+  return cols <= 2048 ? 4 : (cols <= 4096 ? 2 : 1);
+}
 
 template <typename T>
 void norm_bwd_any(const NormArgs& a, hipStream_t s) {
-  if (a.cols <= 512) norm_bwd<T, 1, 1, 8>(a, s);
-  else if (a.cols <= 1024) norm_bwd<T, 2, 1, 4>(a, s);
-  else if (a.cols <= 2048) norm_bwd<T, 4, 1, 4>(a, s);
-  else if (a.cols <= 4096) norm_bwd<T, 8, 1, 2>(a, s);
-  else if (a.cols <= 8192) norm_bwd<T, 16, 1, 1>(a, s);
-  else if (a.cols <= 16384) norm_bwd<T, 16, 2, 1>(a, s);
-  else norm_bwd<T, 16, 4, 1>(a, s);
+  if (a.cols <= 128) norm_bwd<T, 16, 1, 1, 8>(a, s);
+  else if (a.cols <= 256) norm_bwd<T, 32, 1, 1, 8>(a, s);
+  else if (a.cols <= 512) norm_bwd<T, 64, 1, 1, 8>(a, s);
+  else if (a.cols <= 1024) norm_bwd<T, 64, 2, 1, 4>(a, s);
+  else if (a.cols <= 2048) norm_bwd<T, 64, 4, 1, 4>(a, s);
+  else if (a.cols <= 4096) norm_bwd<T, 64, 8, 1, 2>(a, s);
+  else if (a.cols <= 8192) norm_bwd<T, 64, 16, 1, 1>(a, s);
+  else if (a.cols <= 16384) norm_bwd<T, 64, 16, 2, 1>(a, s);
+  else norm_bwd<T, 64, 16, 4, 1>(a, s);
 }
 
 constexpr int64_t kSlabUnits = (int64_t)1 << 30;
@@ -525,7 +585,7 @@ hipError_t launch_norm_forward(int dtype, const NormArgs& all, hipStream_t s) {
 }
 
 int64_t norm_backward_parts(int64_t rows, int64_t cols) {
-  const int64_t g = norm_groups(cols), blocks = (rows + g - 1) / g, most = cols <= 1024 ? 512 : 256;
+  const int64_t g = norm_rows(cols), blocks = (rows + g - 1) / g, most = cols <= 1024 ? 512 : 256;
   return blocks < most ? blocks : most;
 }
 

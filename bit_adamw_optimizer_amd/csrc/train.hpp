@@ -41,7 +41,7 @@ struct NormArgs {
   float* dweight;
   float* dbias;
   int accumulate;
-  float* partial;    // [2][nparts][cols]: each workgroup's sums over its rows
+  float* partial;    // [2][nparts][cols]: each workgroup's sums over its rows (null: nparts <= 1)
   int64_t nparts;
 };
 

@@ -98,7 +98,8 @@ msamp_status check_norm(int64_t rows, int64_t cols, int dtype, const void* weigh
   return MSAMP_OK;
 }
 
-// The bytes of the partial sums: two sums a column from each workgroup.
+// The bytes of the partial sums: two sums a column from each workgroup. (One
+// alone writes the gradients itself and leaves them unused.)
 int64_t norm_workspace(int64_t rows, int64_t cols) { return 2 * norm_backward_parts(rows, cols) * cols * 4; }
 
 msamp_status check_ffn(const msamp_gated_ffn* a, bool backward) {
@@ -236,10 +237,10 @@ msamp_status msamp_layernorm_backward(int64_t rows, int64_t cols, const void* dy
     a.dy = dy, a.lddy = lddy, a.dx = dx, a.lddx = lddx;
     a.dweight = dweight, a.dbias = dbias, a.accumulate = accumulate;
     a.nparts = norm_backward_parts(rows, cols);
-    a.partial = sums ? (float*)workspace : nullptr;
+    a.partial = sums && a.nparts > 1 ? (float*)workspace : nullptr;
     hipStream_t s = (hipStream_t)stream;
     if (rows > 0) MSAMP_LAUNCH(MSAMP_KERNEL_NORM_BACKWARD, s, launch_norm_backward(dtype, a, s));
-    if (sums) MSAMP_LAUNCH(MSAMP_KERNEL_NORM_REDUCE, s, launch_norm_reduce(a, s));
+    if (sums && a.nparts != 1) MSAMP_LAUNCH(MSAMP_KERNEL_NORM_REDUCE, s, launch_norm_reduce(a, s));
     return MSAMP_OK;
   });
 }

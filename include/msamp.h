@@ -763,11 +763,10 @@ typedef enum {
   MSAMP_KERNEL_NORM_REDUCE = 19,   /* its weight and bias gradients */
   MSAMP_KERNEL_FFN_FORWARD = 20,   /* gate and up projections, activation, product */
   MSAMP_KERNEL_FFN_RECOMPUTE = 21, /* the same in the backward pass, giving dg and du */
-  MSAMP_KERNEL_FFN_DX = 22,        /* dx = dg w_gate + du w_up */
-  MSAMP_KERNEL_FFN_DW = 23,        /* dw_gate, dw_up */
-  MSAMP_KERNEL_FFN_LAYOUT = 24,    /* operands laid out for the matrix kernels */
-  MSAMP_KERNEL_FFN_REDUCE = 25,    /* partial sums of a split product */
-  MSAMP_KERNEL_COUNT = 26
+  MSAMP_KERNEL_FFN_GRADIENTS = 22, /* dx, dw_gate and dw_up */
+  MSAMP_KERNEL_FFN_LAYOUT = 23,    /* operands laid out for the matrix kernels */
+  MSAMP_KERNEL_FFN_REDUCE = 24,    /* partial sums of a split product */
+  MSAMP_KERNEL_COUNT = 25
 } msamp_kernel_kind;
 
 /* on != 0 starts recording (and discards earlier records; the events for

@@ -105,6 +105,24 @@ def test_through_checkpoints(rows, cols, dtype, centered, fmt):
     check_forward(xv, w, b, centered, y2, mean2, rstd2)
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows,cols,pad", [(1, 128, 0), (33, 127, 1), (1000, 64, 0), (257, 33, 0), (15, 8, 8), (700, 129, 0),
+                                           (50, 256, 0), (2, 255, 3), (1234, 200, 0)])
+def test_short_rows(rows, cols, pad, dtype):
+    """Several rows to a wave (up to 128 and 256 columns), numbers of rows that fill no workgroup."""
+    dt = DT[dtype]
+    x, dy = matrix(rows, cols, dt, pad, 1, offset=0.3), matrix(rows, cols, dt, pad, 2, size=0.1)
+    w, b = weights(cols, dt, 3)
+    for centered in (True, False):
+        ck = M.new_checkpoint(rows, cols)
+        y, mean, rstd = forward(x, w, b if centered else None, centered, save=ck)
+        check_forward(x, w, b if centered else None, centered, y, mean, rstd)
+        check_backward(dy, x, w, mean, rstd, backward(dy, x, w, mean, rstd))
+        xv = torch.empty(rows, cols, device="cuda")
+        M.checkpoint_load(ck, xv)
+        check_backward(dy, xv, w, mean, rstd, backward(dy, ck, w, mean, rstd))
+
+
 def test_no_weight_no_bias_and_one_gradient():
     x, dy = matrix(37, 300, torch.float16, 0, 1), matrix(37, 300, torch.float16, 0, 2)
     y, mean, rstd = forward(x, None, None, True)
@@ -129,6 +147,18 @@ def test_many_rows_accumulate_and_repeat(rows, cols):
     check_backward(dy, x, w, mean, rstd, first)
     again = backward(dy, x, w, mean, rstd)
     assert all(torch.equal(p, q) for p, q in zip(first, again))  # the same sums in the same order
+    dw, db = torch.full((cols,), 2.0, device="cuda"), torch.full((cols,), -3.0, device="cuda")
+    _, dw2, db2 = backward(dy, x, w, mean, rstd, True, dw, db)
+    assert torch.equal(dw2, 2.0 + first[1]) and torch.equal(db2, -3.0 + first[2])
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 40), (20, 128), (4, 2048), (2, 4096), (1, 9000), (1, 20001)])
+def test_one_workgroup_accumulates(rows, cols):
+    x, dy = matrix(rows, cols, torch.float16, 0, 1, offset=1.0), matrix(rows, cols, torch.float16, 0, 2)
+    w, _ = weights(cols, torch.float16, 3)
+    _, mean, rstd = forward(x, w, None, True)
+    first = backward(dy, x, w, mean, rstd)
+    check_backward(dy, x, w, mean, rstd, first)
     dw, db = torch.full((cols,), 2.0, device="cuda"), torch.full((cols,), -3.0, device="cuda")
     _, dw2, db2 = backward(dy, x, w, mean, rstd, True, dw, db)
     assert torch.equal(dw2, 2.0 + first[1]) and torch.equal(db2, -3.0 + first[2])
