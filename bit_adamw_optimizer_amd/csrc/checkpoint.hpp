@@ -64,8 +64,13 @@ __device__ __forceinline__ void load8(const T* p, int n, float* f) {
   }
 }
 
-template <typename T>
+// STREAM: past the caches.
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ void store8(T* p, int n, const float* f) {
+  auto put = [](u32x4 v, GLOBAL u32x4_any* q) {
+    if constexpr (STREAM) __builtin_nontemporal_store(v, q);
+    else *q = v;
+  };
   if (n >= 8) {
     if constexpr (sizeof(T) == 4) {
       u32x4 a, b;
@@ -74,14 +79,14 @@ __device__ __forceinline__ void store8(T* p, int n, const float* f) {
         a[k] = __float_as_uint(f[k]);
         b[k] = __float_as_uint(f[k + 4]);
       }
-      *(GLOBAL u32x4_any*)p = a;
-      *((GLOBAL u32x4_any*)p + 1) = b;
+      put(a, (GLOBAL u32x4_any*)p);
+      put(b, (GLOBAL u32x4_any*)p + 1);
     } else {
       typedef T t8 __attribute__((ext_vector_type(8)));
       t8 v;
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = from_f32<T>(f[k]);
-      *(GLOBAL u32x4_any*)p = __builtin_bit_cast(u32x4, v);
+      put(__builtin_bit_cast(u32x4, v), (GLOBAL u32x4_any*)p);
     }
   } else {
 #pragma unroll

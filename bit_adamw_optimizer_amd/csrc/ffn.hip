@@ -1098,7 +1098,7 @@ hipError_t launch_few(int dtype, const Product& p, hipStream_t s) {
 // hidden size of 1024 that takes longer than a split sum (56 tokens at 3136
 // and 1920: 18.5 us).
 bool few_rows(int64_t R, int64_t C, int64_t K) {
-  return R <= kFewRows && (double)R * (double)C * (double)K <= 8e8 && (R <= 16 || K <= 1024);
+  return R <= kFewRows && C <= (1 << 22) && (double)R * (double)C * (double)K <= 8e8 && (R <= 16 || K <= 1024);
 }
 
 // The gate and up projections by the kernel that suits the number of tokens.

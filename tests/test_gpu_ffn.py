@@ -113,6 +113,53 @@ def test_accumulate_and_repeat():
     assert torch.equal(dx, first) and torch.equal(a2, 0.5 + a) and torch.equal(b2, -2.0 + b)
 
 
+@pytest.mark.parametrize("t,k,f", [(1500, 200, 130), (3000, 72, 80), (40, 300, 700)])
+def test_accumulate_over_split_sums_and_into_wide_rows(t, k, f):
+    """Long sums over tokens are joined from parts before they are added; the gradients' rows lie apart."""
+    x, wg, wu, dh = problem(t, k, f, torch.bfloat16)
+    dx = torch.empty(t, k, dtype=torch.bfloat16, device="cuda")
+    a, b = torch.empty(f, k, device="cuda"), torch.empty(f, k, device="cuda")
+    M.gated_ffn_backward(dh, x, wg, wu, dx, a, b)
+    val, err = R.ffn(x.cpu(), wg.cpu(), wu.cpu(), "silu", dh.cpu(), torch.bfloat16)
+    check(["dx", "dw_gate", "dw_up"], {"dx": dx, "dw_gate": a, "dw_up": b}, val, err, torch.bfloat16)
+    (buf, a2), (buf2, b2) = out(f, k, torch.float32, 0.5), out(f, k, torch.float32, -2.0)
+    M.gated_ffn_backward(dh, x, wg, wu, dx, a2, b2, accumulate=True)
+    assert torch.equal(a2, 0.5 + a) and torch.equal(b2, -2.0 + b)
+    assert untouched(buf, f, k, 0.5) and untouched(buf2, f, k, -2.0)
+
+
+def test_repeated_rows_of_dh_and_x():
+    """Broadcast inputs (rows at distance 0): the sums of their gradients are the caller's."""
+    t, k, f = 90, 136, 200
+    x, wg, wu, dh = problem(t, k, f, torch.float16)
+    xe, de = x[:1].expand(t, k), dh[:1].expand(t, f)
+    dx, a, b = torch.empty_like(x), torch.empty(f, k, device="cuda"), torch.empty(f, k, device="cuda")
+    M.gated_ffn_backward(de, xe, wg, wu, dx, a, b)
+    val, err = R.ffn(xe.cpu(), wg.cpu(), wu.cpu(), "silu", de.cpu(), torch.float16)
+    check(["dx", "dw_gate", "dw_up"], {"dx": dx, "dw_gate": a, "dw_up": b}, val, err, torch.float16)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap have workspaces of their own."""
+    dt = torch.bfloat16
+    probs = [problem(400, 512, 1200, dt, seed=s) for s in (1, 2)]
+    outs, want = [], []
+    for x, wg, wu, dh in probs:
+        o = (torch.empty_like(dh), torch.empty_like(x), torch.empty(1200, 512, device="cuda"), torch.empty(1200, 512, device="cuda"))
+        M.gated_ffn_backward(dh, x, wg, wu, o[1], o[2], o[3], h=o[0])
+        want.append([v.clone() for v in o])
+        outs.append(o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        for s, (x, wg, wu, dh), o in zip(streams, probs, outs):
+            with torch.cuda.stream(s):
+                M.gated_ffn_backward(dh, x, wg, wu, o[1], o[2], o[3], h=o[0])
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(p, q) for p, q in zip(o, w))
+
+
 def test_empty_calls():
     f16 = torch.float16
     e = lambda r, c: torch.empty(r, c, dtype=f16, device="cuda")  # noqa: E731
