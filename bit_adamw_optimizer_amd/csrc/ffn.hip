@@ -684,6 +684,8 @@ __global__ __launch_bounds__(kThreads) void k_gradients_join(Product x, Product 
   else join_unit<T, kDw, FR>(w, (LDS char*)smem, blockIdx.x - nx, gridDim.x - nx);
 }
 
+constexpr int kUnits = 256;  // workgroups that run at a time, one a compute unit
+
 // How a product is cut: its tiles, and parts of the sum over k.
 struct Cut {
   uint32_t tiles_r, tiles_c, splits;
@@ -697,20 +699,21 @@ int64_t steps_of(int mode, int64_t K) { return (K + kStepK - 1) / kStepK * (mode
 int64_t tiles_of(int mode, const Cut& c) { return (int64_t)c.tiles_r * c.tiles_c * (mode == kDw ? 2 : 1); }
 
 // The cut with tiles of 64 * fr rows and the sums in 'splits' parts of whole
-// steps (false: there is none).
+// steps (false: there is none, or it fills the device more than four times).
 bool cut_of(int mode, int fr, int64_t splits, int64_t R, int64_t C, int64_t K, Cut* c) {
   const int64_t steps = steps_of(mode, K), tc = is_pair(mode) ? 128 : 256;
   const int64_t part = (steps + splits - 1) / splits;
   if ((steps + part - 1) / part != splits || (splits > 1 && part < 2)) return false;
   *c = {(uint32_t)((R + 64 * fr - 1) / (64 * fr)), (uint32_t)((C + tc - 1) / tc), (uint32_t)splits, part, 0};
-  if (splits > 1) c->bytes = tiles_of(mode, *c) * splits * (64 * fr * kTileC * 4);
-  return c->bytes <= (int64_t)1 << 30;
+  if (splits == 1) return true;
+  if (tiles_of(mode, *c) > 4 * kUnits / splits) return false;
+  c->bytes = tiles_of(mode, *c) * splits * (64 * fr * kTileC * 4);
+  return true;
 }
 
 // Times in us, fitted to measurements of every cut of 14 problems (tokens 64 to
 // 8192, hidden 128 to 8192, 128 to 13824 inner units; on these the cut they
-// choose is within 2% of the best one on average, 18% at most). One workgroup
-// a compute unit runs at a time.
+// choose is within 2% of the best one on average, 18% at most).
 double unit_us(int fr, const Cut& c) {
   return c.part * (fr == 4 ? 1.8 : (fr == 2 ? 1.05 : 0.8)) + (fr == 4 ? 13.0 : (fr == 2 ? 7.5 : 2.0));
 }
@@ -722,7 +725,6 @@ double join_us(int fr, const Cut& c) {
   return 3.5 + (each > all ? each : all);
 }
 
-constexpr int kUnits = 256;
 // Numbers of parts that are looked at (a plan is made on the host at each
 // call, in about a microsecond).
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
@@ -732,15 +734,13 @@ struct Candidate {
   double units, unit, join;
 };
 
-// The cuts with tiles of 64 * fr rows that fill the device at most four times
-// over when they split sums.
+// The cuts with tiles of 64 * fr rows.
 int candidates(int mode, int fr, int64_t R, int64_t C, int64_t K, Candidate* out) {
   int n = 0;
   for (int splits : kSplits) {
     Candidate& c = out[n];
     if (!cut_of(mode, fr, splits, R, C, K, &c.cut)) continue;
     c.units = (double)tiles_of(mode, c.cut) * splits;
-    if (splits > 1 && c.units > 4 * kUnits) break;
     c.unit = unit_us(fr, c.cut);
     c.join = join_us(fr, c.cut);
     ++n;
@@ -1177,7 +1177,7 @@ msamp_status lay_out(int64_t rows, int64_t cols, const void* p, int64_t ld, cons
   *out = {p, ld};
   if (ck == nullptr && direct(p, ld, cols)) return MSAMP_OK;
   const int64_t lp = round64(cols);
-  if (lp >= (1 << 22)) return fail(MSAMP_E_INVALID_ARG, "rows longer than 2^22 elements have to be 16-byte aligned");
+  if (lp >= (1 << 22)) return fail(MSAMP_E_INVALID_ARG, "hidden exceeds 2^22 - 64");
   Layout& j = jobs.job[jobs.n++];
   j = {rows, cols, ck == nullptr ? p : nullptr, ld, CkptRef{}, ws.take(rows * lp * 2), lp};
   if (ck != nullptr) j.ck = {ck->codes, ck->ld, ck->scales, ck->ld_scales, (int)ck->fmt};

@@ -529,28 +529,28 @@ int64_t slab_rows(int64_t cols) {
 template <typename T>
 hipError_t checkpoint_save(int64_t rows, int64_t cols, const T* x, int64_t ldx, CkptRef ck, hipStream_t s) {
   const int64_t slab = slab_rows(cols);
-  for (; rows > 0; rows -= slab) {
+  for (;; rows -= slab) {
     const Units u = units_of(rows < slab ? rows : slab, cols);
     k_checkpoint_save<T><<<dim3((u.total + kCkBlock - 1) / kCkBlock), dim3(kCkBlock), 0, s>>>(u, cols, x, ldx, ck);
+    if (rows <= slab) return hipGetLastError();
     x += slab * ldx;
     ck.codes += slab * ck.ld;
     ck.scales += slab * ck.ld_scales;
   }
-  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t checkpoint_load(int64_t rows, int64_t cols, CkptRef ck, T* out, int64_t ldout, hipStream_t s) {
   const int64_t slab = slab_rows(cols);
-  for (; rows > 0; rows -= slab) {
+  for (;; rows -= slab) {
     const Units u = units_of(rows < slab ? rows : slab, cols);
     k_checkpoint_load<T><<<dim3((u.total + kCkBlock - 1) / kCkBlock), dim3(kCkBlock), 0, s>>>(u, cols, ck, out,
                                                                                              ldout);
+    if (rows <= slab) return hipGetLastError();
     out += slab * ldout;
     ck.codes += slab * ck.ld;
     ck.scales += slab * ck.ld_scales;
   }
-  return hipGetLastError();
 }
 
 }  // namespace
@@ -579,6 +579,7 @@ hipError_t launch_norm_forward(int dtype, const NormArgs& all, hipStream_t s) {
     if (dtype == MSAMP_F32) norm_fwd_any<float>(a, s);
     else if (dtype == MSAMP_F16) norm_fwd_any<f16>(a, s);
     else norm_fwd_any<bf16>(a, s);
+    if (a.rows < kSlab) break;
     if (a.x != nullptr) a.x = (const char*)a.x + kSlab * a.ldx * es;
     a.ck.codes += kSlab * a.ck.ld;
     a.ck.scales += kSlab * a.ck.ld_scales;

@@ -62,6 +62,55 @@ msamp_status check_checkpoint(const msamp_checkpoint* c, int64_t rows, int64_t c
   return check_matrix(c->scales, rows, groups, c->ld_scales, 1, written, (std::string(role) + ".scales").c_str());
 }
 
+// The memory of a call's arguments. What is written may share none with
+// anything else (the kernels write some rows while they still read others),
+// but a norm's output may be its input ('in_place': equal matrices, whose rows
+// are read whole before they are written).
+class Regions {
+ public:
+  void add(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size, bool written, const char* role,
+           bool in_place = false) {
+    if (p == nullptr || rows == 0 || cols == 0) return;
+    r_[n_++] = {(uintptr_t)p, (uintptr_t)p + (uintptr_t)(((rows - 1) * ld + cols) * size), cols * size, ld * size,
+                rows == 1, written, in_place, role};
+  }
+  void vector(const void* p, int64_t n, int64_t size, bool written, const char* role) {
+    add(p, 1, n, n, size, written, role);
+  }
+  void checkpoint(const msamp_checkpoint* c, int64_t rows, int64_t cols, bool written, const char* role) {
+    if (c == nullptr) return;
+    add(c->codes, rows, cols, c->ld, 1, written, role);
+    add(c->scales, rows, (cols + MSAMP_CHECKPOINT_GROUP - 1) / MSAMP_CHECKPOINT_GROUP, c->ld_scales, 1, written, role);
+  }
+  msamp_status check() const {
+    for (int i = 1; i < n_; ++i)
+      for (int j = 0; j < i; ++j)
+        if ((r_[i].written || r_[j].written) && overlap(r_[i], r_[j]))
+          return invalid(std::string(r_[j].role) + " and " + r_[i].role + " overlap");
+    return MSAMP_OK;
+  }
+
+ private:
+  struct Region {
+    uintptr_t lo, hi;
+    int64_t row, ld;
+    bool one, written, in_place;
+    const char* role;
+  };
+  static bool overlap(const Region& a, const Region& b) {
+    if (a.hi <= b.lo || b.hi <= a.lo) return false;
+    if (a.in_place && b.in_place && a.lo == b.lo && a.row == b.row && (a.ld == b.ld || a.one)) return false;
+    // rows side by side at the same distance (columns of one buffer)
+    const int64_t ld = a.one ? b.ld : a.ld;
+    if ((a.one && b.one) || (!a.one && !b.one && a.ld != b.ld) || ld == 0) return true;
+    const int64_t d = b.lo >= a.lo ? (int64_t)((b.lo - a.lo) % (uintptr_t)ld)
+                                   : (ld - (int64_t)((a.lo - b.lo) % (uintptr_t)ld)) % ld;
+    return d < a.row || d + b.row > ld;
+  }
+  Region r_[16];
+  int n_ = 0;
+};
+
 CkptRef ref(const msamp_checkpoint* c) {
   CkptRef r;
   if (c != nullptr) r = {c->codes, c->ld, c->scales, c->ld_scales, (int)c->fmt};
@@ -125,6 +174,25 @@ msamp_status check_ffn(const msamp_gated_ffn* a, bool backward) {
   return check_matrix(a->dw_up, F, K, a->ld_dw_up, elem_size(a->dw_dtype), true, "dw_up");
 }
 
+msamp_status check_ffn_memory(const msamp_gated_ffn* a, bool backward, const void* workspace, int64_t bytes) {
+  const int64_t T = a->tokens, K = a->hidden, F = a->ffn;
+  Regions m;
+  if (a->x_ckpt == nullptr) m.add(a->x, T, K, a->ldx, 2, false, "x");
+  else m.checkpoint(a->x_ckpt, T, K, false, "x_ckpt");
+  m.add(a->w_gate, F, K, a->ld_gate, 2, false, "w_gate");
+  m.add(a->w_up, F, K, a->ld_up, 2, false, "w_up");
+  m.add(a->h, T, F, a->ldh, 2, true, "h");
+  if (backward) {
+    const int64_t size = elem_size(a->dw_dtype);
+    m.add(a->dh, T, F, a->lddh, 2, false, "dh");
+    m.add(a->dx, T, K, a->lddx, 2, true, "dx");
+    m.add(a->dw_gate, F, K, a->ld_dw_gate, size, true, "dw_gate");
+    m.add(a->dw_up, F, K, a->ld_dw_up, size, true, "dw_up");
+  }
+  m.vector(workspace, bytes, 1, true, "workspace");
+  return m.check();
+}
+
 template <typename F>
 int64_t workspace_of(F&& f) {
   int64_t bytes = -1;
@@ -151,6 +219,10 @@ msamp_status msamp_checkpoint_save(int64_t rows, int64_t cols, const void* x, in
     MSAMP_TRY(check_checkpoint(ckpt, rows, cols, true, "ckpt"));
     MSAMP_TRY(check_matrix(x, rows, cols, ldx, elem_size(dtype), false, "x"));
     if (rows == 0 || cols == 0) return MSAMP_OK;
+    Regions m;
+    m.add(x, rows, cols, ldx, elem_size(dtype), false, "x");
+    m.checkpoint(ckpt, rows, cols, true, "ckpt");
+    MSAMP_TRY(m.check());
     hipStream_t s = (hipStream_t)stream;
     MSAMP_LAUNCH(MSAMP_KERNEL_CHECKPOINT_SAVE, s,
                  launch_checkpoint_save(dtype, rows, cols, x, ldx, ref(ckpt), s));
@@ -167,6 +239,10 @@ msamp_status msamp_checkpoint_load(int64_t rows, int64_t cols, const msamp_check
     MSAMP_TRY(check_checkpoint(ckpt, rows, cols, false, "ckpt"));
     MSAMP_TRY(check_matrix(out, rows, cols, ldout, elem_size(dtype), true, "out"));
     if (rows == 0 || cols == 0) return MSAMP_OK;
+    Regions m;
+    m.checkpoint(ckpt, rows, cols, false, "ckpt");
+    m.add(out, rows, cols, ldout, elem_size(dtype), true, "out");
+    MSAMP_TRY(m.check());
     hipStream_t s = (hipStream_t)stream;
     MSAMP_LAUNCH(MSAMP_KERNEL_CHECKPOINT_LOAD, s,
                  launch_checkpoint_load(dtype, rows, cols, ref(ckpt), out, ldout, s));
@@ -185,12 +261,23 @@ msamp_status msamp_layernorm_forward(int64_t rows, int64_t cols, const void* x, 
     MSAMP_TRY(check_matrix(y, rows, cols, ldy, elem_size(dtype), true, "y"));
     if (mean != nullptr) MSAMP_TRY(check_vector(mean, rows, 4, "mean"));
     MSAMP_TRY(check_vector(rstd, rows, 4, "rstd"));
-    if (!std::isfinite(eps) || eps < 0.0) return invalid("eps must be finite and >= 0");
+    if (!std::isfinite((float)eps) || eps < 0.0) return invalid("eps must be finite in binary32 and >= 0");
     if (save != nullptr) {
       if (x_ckpt != nullptr) return invalid("save: x is a checkpoint already");
       MSAMP_TRY(check_checkpoint(save, rows, cols, true, "save"));
     }
     if (rows == 0 || cols == 0) return MSAMP_OK;
+    const int64_t size = elem_size(dtype), wsize = elem_size(weight_dtype);
+    Regions m;
+    m.add(x, rows, cols, ldx, size, false, "x", true);
+    m.checkpoint(x_ckpt, rows, cols, false, "x_ckpt");
+    m.vector(weight, cols, wsize, false, "weight");
+    m.vector(bias, cols, wsize, false, "bias");
+    m.add(y, rows, cols, ldy, size, true, "y", true);
+    m.vector(mean, rows, 4, true, "mean");
+    m.vector(rstd, rows, 4, true, "rstd");
+    m.checkpoint(save, rows, cols, true, "save");
+    MSAMP_TRY(m.check());
     NormArgs a = {};
     a.rows = rows, a.cols = cols;
     a.x = x, a.ldx = ldx, a.ck = ref(x_ckpt);
@@ -229,6 +316,19 @@ msamp_status msamp_layernorm_backward(int64_t rows, int64_t cols, const void* dy
     const bool sums = dweight != nullptr || dbias != nullptr;
     if (sums) MSAMP_TRY(check_workspace(workspace, workspace_bytes, norm_workspace(rows, cols)));
     if (cols == 0) return MSAMP_OK;
+    const int64_t size = elem_size(dtype);
+    Regions m;
+    m.add(dy, rows, cols, lddy, size, false, "dy", true);
+    m.add(x, rows, cols, ldx, size, false, "x", true);
+    m.checkpoint(x_ckpt, rows, cols, false, "x_ckpt");
+    m.vector(weight, cols, elem_size(weight_dtype), false, "weight");
+    m.vector(mean, rows, 4, false, "mean");
+    m.vector(rstd, rows, 4, false, "rstd");
+    m.add(dx, rows, cols, lddx, size, true, "dx", true);
+    m.vector(dweight, cols, 4, true, "dweight");
+    m.vector(dbias, cols, 4, true, "dbias");
+    if (sums) m.vector(workspace, norm_workspace(rows, cols), 1, true, "workspace");
+    if (rows > 0) MSAMP_TRY(m.check());  // of no rows nothing is read
     NormArgs a = {};
     a.rows = rows, a.cols = cols;
     a.x = x, a.ldx = ldx, a.ck = ref(x_ckpt);
@@ -267,6 +367,7 @@ msamp_status msamp_gated_ffn_forward(const msamp_gated_ffn* args, void* workspac
     int64_t need = 0;
     MSAMP_TRY(ffn_forward_workspace(*args, &need));
     MSAMP_TRY(check_workspace(workspace, workspace_bytes, need));
+    MSAMP_TRY(check_ffn_memory(args, false, workspace, need));
     return ffn_forward(*args, workspace, (hipStream_t)stream);
   });
 }
@@ -279,6 +380,7 @@ msamp_status msamp_gated_ffn_backward(const msamp_gated_ffn* args, void* workspa
     int64_t need = 0;
     MSAMP_TRY(ffn_backward_workspace(*args, &need));
     MSAMP_TRY(check_workspace(workspace, workspace_bytes, need));
+    MSAMP_TRY(check_ffn_memory(args, true, workspace, need));
     return ffn_backward(*args, workspace, (hipStream_t)stream);
   });
 }

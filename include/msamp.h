@@ -503,6 +503,10 @@ msamp_status msamp_adamw_o3_step_phase3(int32_t n, const int64_t* numel, const u
  * unspecified before and after. Calls that may run at the same time need
  * workspaces of their own. Results do not depend on other work on the
  * device: no sum is formed with atomics, so equal calls give equal bits.
+ * What a call writes (the workspace included) shares no memory with its other
+ * arguments, except where a norm's output may be its input; such calls are
+ * refused. Columns of one buffer are apart when their rows have the same
+ * distance.
  * ---------------------------------------------------------------------- */
 
 typedef enum { MSAMP_F32 = 0, MSAMP_F16 = 1, MSAMP_BF16 = 2 } msamp_dtype;
@@ -562,10 +566,10 @@ msamp_status msamp_checkpoint_load(int64_t rows, int64_t cols, const msamp_check
  *              read in its place (values in binary32, clamped to its range)
  *   weight     device [cols] of weight_dtype, or NULL for 1
  *   bias       device [cols] of weight_dtype, or NULL for 0
- *   y          device, dtype, out
+ *   y          device, dtype, out; may be x (the same matrix)
  *   mean       device float[rows], out; NULL: RMS norm
  *   rstd       device float[rows], out
- *   eps        >= 0, finite
+ *   eps        >= 0, finite in binary32
  *   save       NULL, or a checkpoint that receives x in the same pass
  *              (x must then not be a checkpoint itself)
  * weight_dtype is dtype or MSAMP_F32. cols <= MSAMP_NORM_MAX_COLS.
@@ -583,7 +587,7 @@ msamp_status msamp_layernorm_forward(int64_t rows, int64_t cols, const void* x, 
  *   dweight = sum over rows of dy * xh        dbias = sum over rows of dy
  * dweight and dbias are binary32 (what msamp_amax takes); with accumulate
  * they are added to what is there. Either may be NULL.
- *   dy, dx     device, dtype
+ *   dy, dx     device, dtype; dx may be dy or x (the same matrix)
  *   x, x_ckpt  as in the forward pass; the checkpoint saved there serves
  *   weight     as in the forward pass, or NULL for 1
  *   workspace  msamp_layernorm_backward_workspace bytes (0: may be NULL)
@@ -603,7 +607,8 @@ typedef enum { MSAMP_ACT_SILU = 0, MSAMP_ACT_GELU = 1, MSAMP_ACT_GELU_TANH = 2 }
  * Arguments of the gated feed-forward block (host struct, read during the
  * call). x [tokens, hidden]; w_gate, w_up [ffn, hidden], as the gate and up
  * projections are stored; h, dh [tokens, ffn]; all of dtype, MSAMP_F16 or
- * MSAMP_BF16. Every size is at most 2^31 - 1.
+ * MSAMP_BF16. Every size is at most 2^31 - 1; hidden is at most 2^22 - 64 and,
+ * in the backward pass, ffn at most 2^21 - 64.
  *   forward:   g = x w_gate^T, u = x w_up^T, h = act(g) * u
  *   backward:  from dh: du = dh * act(g), dg = dh * u * act'(g),
  *              dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x

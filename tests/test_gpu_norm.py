@@ -226,6 +226,47 @@ def test_repeated_rows_and_refusals():
         M.layernorm_forward(dy, None, None, dy, None, r4, eps=-1.0)
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows,cols,pad", [(300, 40, 0), (1000, 200, 3), (700, 513, 1), (600, 1030, 0), (530, 4096, 0), (300, 9001, 0)])
+def test_in_place(rows, cols, pad, dtype):
+    """y in x's place, dx in dy's and in x's: the bits of a call with outputs of their own."""
+    dt = DT[dtype]
+    x, dy = matrix(rows, cols, dt, pad, 1, offset=0.5), matrix(rows, cols, dt, pad, 2, size=0.1)
+    w, b = weights(cols, dt, 3)
+    y, mean, rstd = forward(x, w, b, True)
+    ref = backward(dy, x, w, mean, rstd)
+
+    def copy(t):
+        buf = torch.full((rows, cols + pad), 7.0, dtype=dt, device="cuda")
+        buf[:, :cols] = t
+        return buf, buf[:, :cols]
+
+    buf, at = copy(x)
+    M.layernorm_forward(at, w, b, at, mean, rstd, eps=EPS)
+    assert torch.equal(at, y) and (buf[:, cols:] == 7).all()
+    for over in ("dy", "x"):
+        buf, at = copy(dy if over == "dy" else x)
+        dw, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+        M.layernorm_backward(at if over == "dy" else dy, at if over == "x" else x, w, mean, rstd, at, dw, db)
+        assert torch.equal(at, ref[0]) and torch.equal(dw, ref[1]) and torch.equal(db, ref[2])
+        assert (buf[:, cols:] == 7).all()
+
+
+def test_columns_of_one_buffer():
+    """Input and output side by side in the rows of one buffer, the statistics behind them."""
+    buf = torch.zeros(64, 80, device="cuda")
+    x = matrix(64, 32, torch.float32, 0, 1)
+    buf[:, 4:36] = x
+    rstd = torch.empty(64, device="cuda")
+    M.layernorm_forward(buf[:, 4:36], None, None, buf[:, 36:68], None, rstd, eps=EPS)
+    y, _, r = forward(x, None, None, False)
+    assert torch.equal(buf[:, 36:68], y) and torch.equal(rstd, r) and torch.equal(buf[:, 4:36], x)
+    assert not buf[:, :4].any() and not buf[:, 68:].any()
+    with pytest.raises(M.MsampError):
+        M.layernorm_forward(buf[:, 4:36], None, None, buf[:, 35:67], None, rstd, eps=EPS)
+    assert torch.equal(buf[:, 4:36], x)
+
+
 def test_backward_against_differences():
     """dx and dweight against central differences of the kernel's own binary32 forward pass."""
     rows, cols, step = 3, 40, 2.0 ** -7

@@ -121,6 +121,52 @@ def test_ffn_refuses():
     assert _run(_ffn(tokens=0, x=0, h=0), "forward") == 0 and _run(_ffn(ffn=0, h=0), "forward") == 0
 
 
+def test_shared_memory_is_refused():
+    assert _save(x=0x10010) == 1 and "x and ckpt overlap" in _err()
+    assert _save(x=0x20004) == 1
+    L = M.lib().msamp_checkpoint_load
+    assert L(4, 64, _ck(), P(0x10000 - 2), 64, F16, None) == 1 and "ckpt and out overlap" in _err()
+    # a checkpoint whose scales lie in its codes' rows: apart behind the columns, not within them
+    assert L(4, 64, _ck(scales=0x10020), P(0x1000A), 80, F16, None) == 1
+    assert _save(ck=_ck(ld=66, scales=0x1003F, lds=66)) == 1 and "ckpt and ckpt overlap" in _err()
+    for role, at in (("x and y", 0x30040), ("weight and y", 0x40000 - 64), ("y and mean", 0x70000), ("y and rstd", 0x80000)):
+        assert _fwd(y=at) == 1 and role + " overlap" in _err(), role
+    assert _fwd(mean=0x80000) == 1 and _fwd(save=_ck(codes=0x30000)) == 1 and _fwd(save=_ck(scales=0x60000)) == 1
+    # y in x's place, but not with other rows
+    assert _fwd(y=0x30000, ldy=65) == 1 and _fwd(y=0x30000, ldx=0) == 1
+    # columns of one buffer whose rows have the same distance, overlapping by one
+    assert _fwd(y=0x30000 + 126, ldx=128, ldy=128) == 1 and _fwd(y=0x30000 - 126, ldx=128, ldy=128) == 1
+    for role, kw in (("dy and dx", dict(dx=0x30002)), ("x and dx", dict(dx=0x90002)), ("weight and dweight", dict(dw=0x40000)),
+                     ("dweight and dbias", dict(db=0xA0000)), ("rstd and dbias", dict(db=0x80000)),
+                     ("dx and workspace", dict(ws=0x60000))):
+        assert _bwd(**kw) == 1 and role + " overlap" in _err(), role
+    for which in ("forward", "backward"):
+        assert _run(_ffn(h=0x10000), which) == 1 and "x and h overlap" in _err()
+        assert _run(_ffn(h=0x20000), which) == 1 and _run(_ffn(h=0x30002), which) == 1
+    for kw in (dict(dx=0x10000), dict(dx=0x20000), dict(dw_gate=0x80000), dict(dw_up=0x30000), dict(dh=0x40000),
+               dict(dx=0x50000)):
+        assert _run(_ffn(**kw), "backward") == 1 and "overlap" in _err(), kw
+    assert _run(_ffn(), "backward", ws=0x80000) == 1 and "workspace overlap" in _err()
+
+
+def test_eps_beyond_binary32_is_refused():
+    assert _fwd(eps=1e39) == 1 and "eps" in _err()
+
+
+def test_sizes_beyond_the_matrix_kernels_are_refused():
+    big = dict(hidden=1 << 22, ldx=1 << 22, ld_gate=1 << 22, ld_up=1 << 22, lddx=1 << 22, ld_dw_gate=1 << 22,
+               ld_dw_up=1 << 22, tokens=100, ffn=96)
+    assert M.lib().msamp_gated_ffn_forward_workspace(ctypes.byref(_ffn(**big))) == -1 and "2^22" in _err()
+    assert M.lib().msamp_gated_ffn_backward_workspace(ctypes.byref(_ffn(**big))) == -1 and "2^22" in _err()
+    wide = dict(ffn=1 << 21, ldh=1 << 21, lddh=1 << 21)
+    assert M.lib().msamp_gated_ffn_backward_workspace(ctypes.byref(_ffn(**wide))) == -1 and "2^21" in _err()
+    # as many rows as an int takes: a plan, or a refusal
+    for t in (1 << 24, (1 << 31) - 1):
+        for which in ("forward", "backward"):
+            W = getattr(M.lib(), "msamp_gated_ffn_%s_workspace" % which)
+            assert W(ctypes.byref(_ffn(tokens=t, ffn=1, ldh=1, lddh=1))) >= -1
+
+
 def test_binding_refuses_host_tensors_and_bad_types():
     x = torch.zeros(4, 64, dtype=torch.float16)
     with pytest.raises(ValueError):
