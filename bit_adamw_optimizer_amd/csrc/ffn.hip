@@ -893,7 +893,11 @@ msamp_status gradients(int dtype, Product x, Product w, Arena& ws, bool run, hip
 // straight into the operands of 16x16x32 MFMA, 128 bytes of every row at a
 // time (k is taken in the order of the bytes a lane holds, the same for x), so
 // no LDS and no barrier stand between the loads. The waves' sums are joined
-// through LDS.
+// through LDS. At 1 token, 4096 and 11008 (180 MB of weights): 34.7 us, 5.2
+// TB/s. With one token the rate of the memory bounds it: 4, 8 or 16 waves and
+// 2, 4 or 8 chunks of loads under way all take 34.2 to 37.4 us there and 50.2
+// to 52.1 us at 8192 and 8192; 8 waves with 2 chunks are within 2% of the best
+// at every size tried.
 
 template <typename T>
 struct Frag16;
@@ -932,7 +936,7 @@ __device__ __forceinline__ u32x4 load_piece(const T* p, int64_t n) {
 // is read on its own.
 template <typename T, int MODE, int NT, bool ALIGNED>
 __global__ __launch_bounds__(kFewThreads) void k_few_rows(Product p) {
-  constexpr int kUnroll = NT == 1 ? 4 : 2;  // chunks of 64 k whose loads are under way at a time
+  constexpr int kUnroll = 2;  // chunks of 64 k whose loads are under way at a time (see above)
   __shared__ f32x4 sums[kFewWaves][NT][2][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t col0 = (int64_t)blockIdx.x * 16;
@@ -1093,7 +1097,7 @@ hipError_t launch_few(int dtype, const Product& p, hipStream_t s) {
 // Whether the kernel for few tokens takes the gate and up projections. Every
 // workgroup of it reads all of x, from L2: with more than about 8e8 products
 // (100 MB of it) that costs more than the partial sums of the tiled kernel
-// save. Measured at hidden 4096, 11008 inner units: 16 tokens 39.9 us against
+// save. Measured at hidden 4096, 11008 inner units: 16 tokens 40.1 us against
 // 50.3 us by tiles, 24 tokens 49.5 against 50.5, 64 tokens 79.5 against 57.8;
 // at 768 and 2048, 64 tokens 8.3 against 11.2. Its waves take their parts of k
 // one after another, with several blocks of tokens 128 k at a time: beyond a
