@@ -209,7 +209,8 @@ __global__ __launch_bounds__(norm_block<WAVES>()) void k_norm_forward(NormArgs a
 }
 
 // A lane's pieces of a row as they lie in memory: of a matrix of T, or of a
-// checkpoint's codes with their scales.
+// checkpoint's codes with their scales. Pieces behind the last column hold
+// anything (the row's first piece, loaded without a branch, or zeros).
 template <typename T, bool CK, int NCH>
 struct RawRow {
   typedef T t8 __attribute__((ext_vector_type(8)));
@@ -225,10 +226,12 @@ __device__ __forceinline__ void load_raw(const T* row, int cols, int lane, RawRo
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int col = (c * LANES + lane) * 8;
-    r.v[c] = t8{};
-    if (TAIL ? col + 8 <= cols : col < cols) {
+    if constexpr (!TAIL) {
+      r.v[c] = *(const GLOBAL t8_any*)(row + (col < cols ? col : 0));
+    } else if (col + 8 <= cols) {
       r.v[c] = *(const GLOBAL t8_any*)(row + col);
-    } else if (TAIL) {
+    } else {
+      r.v[c] = t8{};
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (col + k < cols) r.v[c][k] = ((const GLOBAL T*)row)[col + k];
@@ -243,18 +246,19 @@ __device__ __forceinline__ void load_raw(const CkptRef& ck, int64_t row, int col
   const uint8_t* scales = ck.scales + row * ck.ld_scales;
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int col = (c * LANES + lane) * 8;
-    r.q[c] = u32x2{0u, 0u};
-    r.s[c] = 127;
-    if (TAIL ? col + 8 <= cols : col < cols) {
+    const int col = (c * LANES + lane) * 8, at = col < cols ? col : 0;
+    r.s[c] = ((const GLOBAL uint8_t*)scales)[at / kGroup];
+    if constexpr (!TAIL) {
+      r.q[c] = *(const GLOBAL u32x2_any*)(codes + at);
+    } else if (col + 8 <= cols) {
       r.q[c] = *(const GLOBAL u32x2_any*)(codes + col);
-    } else if (TAIL) {
+    } else {
+      r.q[c] = u32x2{0u, 0u};
       for (int k = 0; k < 8 && col + k < cols; ++k) {
         const uint32_t b = (uint32_t)((const GLOBAL uint8_t*)codes)[col + k] << (8 * (k & 3));
         if (k < 4) r.q[c].x |= b; else r.q[c].y |= b;
       }
     }
-    if (col < cols) r.s[c] = ((const GLOBAL uint8_t*)scales)[col / kGroup];
   }
 }
 
@@ -269,12 +273,18 @@ __device__ __forceinline__ void unpack(const RawRow<T, true, NCH>& r, int fmt, i
 }
 
 // Each workgroup walks over rows: GROUPS sets of WAVES waves, each with a row,
-// or with 64 / LANES rows of LANES lanes. A lane holds the same NCH pieces of 8 columns throughout and sums their share
-// of dweight and dbias in registers. The next rows (two of 16 bits) are on their
-// way while one is worked on (16,384 x 4,096 from a checkpoint: 66 us, against 77 with one). TAIL: the columns end inside a piece. Lanes behind the
-// last column work on zeros, which add nothing to a row's sums (x and dy are
-// 0 there, so dy * xh is 0 or, in a row whose statistics are not finite
-// anyway, NaN).
+// or with 64 / LANES rows of LANES lanes. A lane holds the same NCH pieces of 8
+// columns throughout and sums their share of dweight and dbias in registers.
+// The next row is on its way while one is worked on; two rows where several
+// waves share one of a 16-bit checkpoint, whose rows are the shortest in bytes
+// (from a checkpoint, 16,384 x 2,560: 54 us with two, 58 with one; 65,536 x 512:
+// 39.7 and 38.2; from a matrix, 8,192 x 768: 15.9 and 14.9). They lie in a ring
+// of buffers that the unrolled loop names one after another, and are loaded
+// without branches (behind the last row the last again): where buffers are
+// copied, the compiler waits for every load under way.
+// TAIL: the columns end inside a piece. Lanes behind the last column work on
+// dy = 0, which adds nothing to a row's sums (dy * xh is 0 or, in a row whose
+// statistics are not finite anyway, NaN).
 template <typename T, bool CK, bool TAIL, int LANES, int WAVES, int NCH, int GROUPS>
 __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a) {
   constexpr int kLanes = WAVES * LANES, kRows = WAVES * GROUPS * 64 / kLanes;
@@ -286,7 +296,7 @@ __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a
   // With several pieces a lane, registers are short: the weights are then read
   // for every row (from cache), and no row is loaded ahead.
   constexpr bool kKeep = NCH == 1;
-  constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;  // rows on their way (two of binary32 take too many registers)
+  constexpr int kAhead = !kKeep ? 0 : (CK && sizeof(T) == 2 && WAVES >= 4 ? 2 : 1);
   float w[NCH][8], sw[NCH][8], sb[NCH][8];
   auto load_weights = [&](int c) {
     const int col = (c * kLanes + lane) * 8;
@@ -299,35 +309,36 @@ __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a
 #pragma unroll
     for (int k = 0; k < 8; ++k) sw[c][k] = sb[c][k] = 0.0f;
   }
-  RawRow<T, CK, NCH> rx, nx, mx;
-  RawRow<T, false, NCH> rg, ng, mg;
-  float mu = 0.0f, rstd = 0.0f, nmu = 0.0f, nrstd = 0.0f, mmu = 0.0f, mrstd = 0.0f;
-  auto fetch = [&](int64_t row, RawRow<T, CK, NCH>& x, RawRow<T, false, NCH>& g, float& m, float& r) {
-    if (row >= a.rows) return;
-    if constexpr (CK) load_raw<T, NCH, kLanes, TAIL>(a.ck, row, cols, lane, x);
-    else load_raw<T, NCH, kLanes, TAIL>((const T*)a.x + row * a.ldx, cols, lane, x);
-    load_raw<T, NCH, kLanes, TAIL>((const T*)a.dy + row * a.lddy, cols, lane, g);
-    if (centered) m = a.mean[row];
-    r = a.rstd[row];
+  struct Row {
+    RawRow<T, CK, NCH> x;
+    RawRow<T, false, NCH> g;
+    float mu, rstd;
   };
-  int64_t row = (int64_t)blockIdx.x * kRows + (int)threadIdx.x / kLanes;
-  if constexpr (kKeep) {
-    fetch(row, rx, rg, mu, rstd);
-    if constexpr (kAhead == 2) fetch(row + stride, nx, ng, nmu, nrstd);
-  }
-  // all rows of a workgroup make the same number of turns: the sums have a barrier
+  Row ring[kAhead + 1];
+  const float* mean = centered ? a.mean : a.rstd;  // read in any case, used if centered
+  auto fetch = [&](int64_t row, Row& r) {
+    row = row < a.rows ? row : a.rows - 1;
+    if constexpr (CK) load_raw<T, NCH, kLanes, TAIL>(a.ck, row, cols, lane, r.x);
+    else load_raw<T, NCH, kLanes, TAIL>((const T*)a.x + row * a.ldx, cols, lane, r.x);
+    load_raw<T, NCH, kLanes, TAIL>((const T*)a.dy + row * a.lddy, cols, lane, r.g);
+    r.mu = mean[row];
+    r.rstd = a.rstd[row];
+  };
   int turn = 0;
-  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows; base += stride, row += stride) {
+  auto work = [&](int64_t row, const Row& in) {
     const bool live = row < a.rows;
-    if constexpr (kKeep) fetch(row + kAhead * stride, mx, mg, mmu, mrstd);
-    else fetch(row, rx, rg, mu, rstd);
+    const float mu = in.mu, rstd = in.rstd;
     float xh[NCH][8], g[NCH][8];
     float c1 = 0.0f, c2 = 0.0f;
     if (live) {
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
-        unpack<T, NCH>(rx, a.ck.fmt, c, xh[c]);
-        unpack<T, NCH>(rg, 0, c, g[c]);
+        unpack<T, NCH>(in.x, a.ck.fmt, c, xh[c]);
+        unpack<T, NCH>(in.g, 0, c, g[c]);
+        if ((c * kLanes + lane) * 8 >= cols) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) g[c][k] = 0.0f;
+        }
         if constexpr (!kKeep) load_weights(c);
         if (centered) {
 #pragma unroll
@@ -366,13 +377,18 @@ __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a
         }
       }
     }
-    if constexpr (kKeep) {
-      if constexpr (kAhead == 2) {
-        rx = nx, rg = ng, mu = nmu, rstd = nrstd;
-        nx = mx, ng = mg, nmu = mmu, nrstd = mrstd;
-      } else {
-        rx = mx, rg = mg, mu = mmu, rstd = mrstd;
-      }
+  };
+  int64_t row = (int64_t)blockIdx.x * kRows + (int)threadIdx.x / kLanes;
+#pragma unroll
+  for (int b = 0; b < kAhead; ++b) fetch(row + b * stride, ring[b]);
+  // all rows of a workgroup make the same number of turns: the sums have a barrier
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows;) {
+#pragma unroll
+    for (int b = 0; b <= kAhead; ++b) {
+      fetch(row + kAhead * stride, ring[(b + kAhead) % (kAhead + 1)]);
+      work(row, ring[b]);
+      base += stride, row += stride;
+      if (base >= a.rows) break;
     }
   }
   if (a.dweight == nullptr && a.dbias == nullptr) return;
@@ -388,54 +404,50 @@ __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a
           sb[c][k] += __shfl_xor(sb[c][k], off, 64);
         }
   }
-  if constexpr (GROUPS > 1) {  // the groups' sums of the same columns, in a fixed order
-    __shared__ float acc[2][NCH * kLanes * 8];
-    for (int t = 0; t < GROUPS; ++t) {
-      if (group == t && (LANES == 64 || (int)(threadIdx.x & 63) < LANES)) {
-#pragma unroll
-        for (int c = 0; c < NCH; ++c)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int i = (c * 8 + k) * kLanes + lane;
-            if (t != 0) {
-              sw[c][k] += acc[0][i];
-              sb[c][k] += acc[1][i];
-            }
-            acc[0][i] = sw[c][k];
-            acc[1][i] = sb[c][k];
-          }
-      }
-      __syncthreads();
-    }
-    if (group != GROUPS - 1 || (LANES < 64 && (int)(threadIdx.x & 63) >= LANES)) return;
-  }
   // one workgroup alone has the whole sums; several leave theirs for k_norm_reduce
   const bool alone = a.partial == nullptr;
   float* pw = alone ? a.dweight : a.partial + (int64_t)blockIdx.x * a.cols;
   float* pb = alone ? a.dbias : pw + a.nparts * a.cols;
+  const bool add = alone && a.accumulate;
+  if constexpr (GROUPS > 1) {  // the groups' sums of the same columns meet in LDS, and are added in order
+    __shared__ __attribute__((aligned(16))) float acc[GROUPS][NCH * kLanes * 8];
+    auto join = [&](const float(&sums)[NCH][8], float* out) {
+      __syncthreads();  // acc has been read
+      if (LANES == 64 || (int)(threadIdx.x & 63) < LANES) {
 #pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int col = (c * kLanes + lane) * 8;
-    const int n = TAIL && cols - col < 8 ? cols - col : 8;
-    if (col < cols) {
-      float old[8];
-      if (a.dweight != nullptr) {
-        if (alone && a.accumulate) {
-          load8(pw + col, n, old);
+        for (int c = 0; c < NCH; ++c)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sw[c][k] += old[k];
-        }
-        store8(pw + col, n, sw[c]);
+          for (int k = 0; k < 8; ++k) acc[group][(c * kLanes + lane) * 8 + k] = sums[c][k];
       }
-      if (a.dbias != nullptr) {
-        if (alone && a.accumulate) {
-          load8(pb + col, n, old);
+      __syncthreads();
+      for (int col = threadIdx.x; col < cols; col += WAVES * GROUPS * 64) {
+        float t = acc[0][col];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sb[c][k] += old[k];
-        }
-        store8(pb + col, n, sb[c]);
+        for (int g = 1; g < GROUPS; ++g) t += acc[g][col];
+        out[col] = add ? out[col] + t : t;
       }
-    }
+    };
+    if (a.dweight != nullptr) join(sw, pw);
+    if (bias) join(sb, pb);
+  } else {
+    auto store = [&](float(&sums)[NCH][8], float* out) {
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const int col = (c * kLanes + lane) * 8;
+        const int n = TAIL && cols - col < 8 ? cols - col : 8;
+        if (col < cols) {
+          if (add) {
+            float old[8];
+            load8(out + col, n, old);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sums[c][k] += old[k];
+          }
+          store8(out + col, n, sums[c]);
+        }
+      }
+    };
+    if (a.dweight != nullptr) store(sw, pw);
+    if (bias) store(sb, pb);
   }
 }
 
