@@ -71,8 +71,8 @@ class Regions {
   void add(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size, bool written, const char* role,
            bool in_place = false) {
     if (p == nullptr || rows == 0 || cols == 0) return;
-    r_[n_++] = {(uintptr_t)p, (uintptr_t)p + (uintptr_t)(((rows - 1) * ld + cols) * size), cols * size, ld * size,
-                rows == 1, written, in_place, role};
+    r_[n_++] = {(uintptr_t)p, (uintptr_t)p + (uintptr_t)(((rows - 1) * ld + cols) * size), cols * size,
+                rows == 1 ? cols * size : ld * size, rows == 1, written, in_place, role};
   }
   void vector(const void* p, int64_t n, int64_t size, bool written, const char* role) {
     add(p, 1, n, n, size, written, role);

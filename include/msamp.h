@@ -496,7 +496,7 @@ msamp_status msamp_adamw_o3_step_phase3(int32_t n, const int64_t* numel, const u
  * when it has more than one row. Bases need the alignment of their elements
  * only; 16-byte aligned rows are read and written fastest. Sizes of zero are
  * allowed: NULL is then accepted for the empty matrices. Unlike the list
- * entry points these build no tables: they allocate nothing, take no lock,
+ * entry points these build no tables: they allocate nothing, keep nothing,
  * and can be captured into a graph on the first call. Where a workspace is
  * taken, it is device memory, 16-byte aligned, of at least the size that the
  * _workspace function gives for the same arguments; its contents are

@@ -226,6 +226,24 @@ def test_repeated_rows_and_refusals():
         M.layernorm_forward(dy, None, None, dy, None, r4, eps=-1.0)
 
 
+def test_more_rows_than_one_launch_takes():
+    """2^22 wide rows: a launch of all of them would have 2^32 threads."""
+    rows, cols = (1 << 22) + 5, 8200
+    if torch.cuda.mem_get_info()[0] < rows * cols * 2 * 1.2:
+        pytest.skip("needs 83 GB of GPU memory")
+    row = matrix(1, cols, torch.float16, 0, 1)
+    y = torch.empty(rows, cols, dtype=torch.float16, device="cuda")
+    rstd = torch.zeros(rows, device="cuda")
+    M.layernorm_forward(row.expand(rows, cols), None, None, y, None, rstd)
+    one, r = torch.empty_like(row), torch.empty(1, device="cuda")
+    M.layernorm_forward(row, None, None, one, None, r)
+    assert (rstd == r).all()
+    for at in (0, (1 << 21) - 2, (1 << 22) - 2, rows - 4):
+        assert torch.equal(y[at:at + 4], one.expand(4, cols))
+    del y
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("rows,cols,pad", [(300, 40, 0), (1000, 200, 3), (700, 513, 1), (600, 1030, 0), (530, 4096, 0), (300, 9001, 0)])
 def test_in_place(rows, cols, pad, dtype):

@@ -140,6 +140,8 @@ def test_shared_memory_is_refused():
                      ("dweight and dbias", dict(db=0xA0000)), ("rstd and dbias", dict(db=0x80000)),
                      ("dx and workspace", dict(ws=0x60000))):
         assert _bwd(**kw) == 1 and role + " overlap" in _err(), role
+    # one row may name any distance to the next
+    assert _fwd(rows=1, ldx=1 << 62, ldy=1 << 62, y=0x30040) == 1 and "x and y overlap" in _err()
     for which in ("forward", "backward"):
         assert _run(_ffn(h=0x10000), which) == 1 and "x and h overlap" in _err()
         assert _run(_ffn(h=0x20000), which) == 1 and _run(_ffn(h=0x30002), which) == 1
