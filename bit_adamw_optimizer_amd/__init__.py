@@ -27,6 +27,7 @@ reserved]`` per tensor.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -981,7 +982,7 @@ def layernorm_backward(dy: torch.Tensor, x, weight, mean, rstd: torch.Tensor, dx
     db = None if dbias is None else _vector(dbias, "dbias", dev, torch.float32, cols)
     n, ws = 0, None
     if dw is not None or db is not None:
-        n = _workspace_bytes(lib().msamp_layernorm_backward_workspace(rows, cols))
+        n = _norm_workspace_bytes(rows, cols)
         ws = _workspace(n, dev)
     _run(dev, lib().msamp_layernorm_backward, rows, cols, pdy, lddy, px, ldx, ck, d, w, wd, m, r, pdx, lddx, dw, db,
          1 if accumulate else 0, None if ws is None else ws.data_ptr(), n)
@@ -991,6 +992,11 @@ def _workspace_bytes(n: int) -> int:
     if n < 0:
         raise MsampError(1, lib().msamp_last_error().decode())
     return n
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace_bytes(rows: int, cols: int) -> int:
+    return _workspace_bytes(lib().msamp_layernorm_backward_workspace(rows, cols))
 
 
 def _workspace(n: int, device: int):

@@ -164,6 +164,25 @@ def test_one_workgroup_accumulates(rows, cols):
     assert torch.equal(dw2, 2.0 + first[1]) and torch.equal(db2, -3.0 + first[2])
 
 
+@pytest.mark.parametrize("rows,cols", [(128, 64), (129, 64), (64, 250), (65, 250), (32, 500), (33, 500), (16, 768), (17, 768),
+                                       (8, 2048), (9, 2048), (4, 4095), (5, 4095), (2, 8192), (3, 8192), (2, 20000)])
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_on_both_sides_of_one_workgroup(rows, cols, ckpt):
+    """Several turns of one workgroup, and the fewest rows that several share."""
+    x, dy = matrix(rows, cols, torch.bfloat16, 0, 1, offset=0.5), matrix(rows, cols, torch.bfloat16, 0, 2, size=0.1)
+    w, _ = weights(cols, torch.bfloat16, 3)
+    ck = M.new_checkpoint(rows, cols)
+    _, mean, rstd = forward(x, w, None, True, save=ck)
+    if ckpt:
+        x = torch.empty(rows, cols, device="cuda")
+        M.checkpoint_load(ck, x)
+    first = backward(dy, ck if ckpt else x, w, mean, rstd)
+    check_backward(dy, x, w, mean, rstd, first)
+    dw, db = torch.full((cols,), 2.0, device="cuda"), torch.full((cols,), -3.0, device="cuda")
+    _, dw2, db2 = backward(dy, ck if ckpt else x, w, mean, rstd, True, dw, db)
+    assert torch.equal(dw2, 2.0 + first[1]) and torch.equal(db2, -3.0 + first[2])
+
+
 def test_empty_calls():
     dw, db = torch.full((40,), 7.0, device="cuda"), torch.full((40,), 7.0, device="cuda")
     none, r = torch.empty(0, 40, device="cuda"), torch.empty(0, device="cuda")
