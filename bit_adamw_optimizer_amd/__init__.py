@@ -839,21 +839,38 @@ class Checkpoint:
     codes is a byte tensor (uint8, or a float8 one read as bytes) of at least
     cols columns, scales uint8 of at least ceil(cols / 32), both with
     consecutive rows' elements; what lies behind them is neither read nor
-    written."""
+    written. The fields may be assigned: every call takes the tensors, their
+    addresses and their shapes as they are then."""
 
-    __slots__ = ("codes", "scales", "cols", "fmt", "rows", "device", "_c", "_flat")
+    __slots__ = ("codes", "scales", "cols", "fmt")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: int = E4M3):
-        cols = int(cols)
-        groups = -(-cols // GROUP)
-        dev = _device_of(codes, "codes")
-        if _device_of(scales, "scales") != dev:
+        self.codes, self.scales, self.cols, self.fmt = codes, scales, int(cols), int(fmt)
+        _device_of(scales, "scales")
+        self._arg("codes", _device_of(codes, "codes"))
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def device(self) -> int:
+        return self.codes.get_device()
+
+    def _arg(self, name: str, device: int, shape=None, written: bool = False) -> _Checkpoint:
+        """The fields as the library takes them, checked against the call's device and shape."""
+        codes, scales, cols = self.codes, self.scales, self.cols
+        groups = (cols + GROUP - 1) // GROUP
+        if codes.get_device() != device:
+            raise ValueError("%s is on %s, expected cuda:%d" % (name, codes.device, device))
+        if scales.get_device() != device:
             raise ValueError("scales is on %s, expected %s" % (scales.device, codes.device))
         if codes.element_size() != 1 or scales.element_size() != 1:
             raise TypeError("codes and scales must be bytes, not %s and %s" % (codes.dtype, scales.dtype))
-        if codes.dim() != 2 or scales.dim() != 2:
+        cshape, sshape = codes.shape, scales.shape
+        if len(cshape) != 2 or len(sshape) != 2:
             raise ValueError("codes and scales must have two dimensions")
-        (rows, width), (srows, swidth) = codes.shape, scales.shape
+        (rows, width), (srows, swidth) = cshape, sshape
         (ld, inner), (lds, sinner) = codes.stride(), scales.stride()
         if cols < 0 or width < cols or swidth < groups:
             raise ValueError("%d columns need codes of at least as many and scales of at least %d, not %d and %d"
@@ -862,21 +879,13 @@ class Checkpoint:
             raise ValueError("codes has %d rows, scales %d" % (rows, srows))
         if (inner != 1 and width > 1) or (sinner != 1 and swidth > 1):
             raise ValueError("the elements of a row of codes and scales must be consecutive")
-        self.codes, self.scales, self.cols, self.fmt, self.rows, self.device = codes, scales, cols, int(fmt), rows, dev
-        self._flat = rows <= 1 or (ld >= cols and lds >= groups)
-        if rows == 0 or cols == 0:
-            self._c = _Checkpoint(None, ld, None, lds, self.fmt)
-        else:
-            self._c = _Checkpoint(codes.data_ptr(), ld, scales.data_ptr(), lds, self.fmt)
-
-    def _arg(self, name: str, device: int, shape, written: bool = False):
-        if self.device != device:
-            raise ValueError("%s is on cuda:%d, expected cuda:%d" % (name, self.device, device))
-        if (self.rows, self.cols) != shape:
-            raise ValueError("%s has shape %s, expected %s" % (name, (self.rows, self.cols), tuple(shape)))
-        if written and not self._flat:
+        if shape is not None and (rows, cols) != shape:
+            raise ValueError("%s has shape %s, expected %s" % (name, (rows, cols), tuple(shape)))
+        if written and rows > 1 and (ld < cols or lds < groups):
             raise ValueError("%s: its rows overlap" % name)
-        return ctypes.byref(self._c)
+        if rows == 0 or cols == 0:
+            return _Checkpoint(None, ld, None, lds, self.fmt)
+        return _Checkpoint(codes.data_ptr(), ld, scales.data_ptr(), lds, self.fmt)
 
 
 def new_checkpoint(rows: int, cols: int, fmt: int = E4M3, device="cuda") -> Checkpoint:
@@ -1017,8 +1026,7 @@ def _gated_ffn(x, w_gate, w_up, act: str, dev: int, dt, tokens: int) -> _GatedFf
     a.tokens, a.hidden, a.ffn = tokens, hidden, ffn
     a.dtype, a.act = _DTYPES[dt], ACTIVATIONS[act]
     if isinstance(x, Checkpoint):
-        x._arg("x", dev, (tokens, hidden))
-        a.x_ckpt = ctypes.pointer(x._c)
+        a.x_ckpt = ctypes.pointer(x._arg("x", dev, (tokens, hidden)))
     else:
         a.x, a.ldx = _matrix(x, "x", dev, dt, (tokens, hidden))
     a.w_gate, a.ld_gate = _matrix(w_gate, "w_gate", dev, dt, (ffn, hidden))

@@ -166,3 +166,31 @@ def test_on_another_stream_and_in_a_graph():
         eager = torch.empty_like(x)
         M.checkpoint_load(ref, eager)
         assert torch.equal(out, eager) and torch.equal(ck.scales, ref.scales)
+
+
+def test_fields_that_were_assigned_are_the_ones_a_call_takes():
+    """After the tensors of a checkpoint were replaced, calls read and write the new ones."""
+    x = torch.randn(5, 70, device="cuda", dtype=torch.bfloat16)
+    ck = M.new_checkpoint(5, 70)
+    M.checkpoint_save(x, ck)
+    old = ck.codes, ck.scales
+    kept = old[0].clone(), old[1].clone()
+    # to the host and back, as a program that frees the card's memory in between does
+    ck.codes, ck.scales = old[0].cpu().cuda(), old[1].cpu().cuda()
+    old[0].fill_(0x7F)
+    v = torch.empty_like(x)
+    M.checkpoint_load(ck, v)
+    want = torch.empty_like(x)
+    M.checkpoint_load(M.Checkpoint(kept[0], kept[1], 70), want)
+    assert torch.equal(v, want) and torch.isfinite(v).all()
+    M.checkpoint_save(-x, ck)
+    assert (old[0] == 0x7F).all() and torch.equal(old[1], kept[1])
+    M.checkpoint_load(ck, v)
+    assert torch.equal(v, -want)
+    y, rstd, dx = torch.empty_like(x), torch.empty(5, device="cuda"), torch.empty_like(x)
+    M.layernorm_forward(ck, None, None, y, None, rstd)
+    M.layernorm_backward(x, ck, None, None, rstd, dx, None, None)
+    y2, dx2 = torch.empty_like(x), torch.empty_like(x)
+    M.layernorm_forward(v, None, None, y2, None, rstd)
+    M.layernorm_backward(x, v, None, None, rstd, dx2, None, None)
+    assert torch.equal(y, y2) and torch.equal(dx, dx2)

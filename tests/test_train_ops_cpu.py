@@ -226,3 +226,83 @@ def test_reference_norm_gradients_agree_with_autograd(centered):
     dx, dw, db, *_ = R.norm_backward(dy, x.detach(), w.detach(), mu.detach(), rstd.detach(), centered)
     for got, ref in ((dx, gx), (dw, gw), (db, gb)):
         assert torch.allclose(got, ref, rtol=1e-12, atol=1e-12)
+
+
+def _bytes(rows, cols):
+    return torch.zeros(rows, cols, dtype=torch.uint8)
+
+
+@pytest.mark.parametrize("call", ["save", "load", "norm saves", "norm reads", "norm backward", "block backward"])
+def test_a_checkpoint_is_taken_as_its_fields_are_at_the_call(call, monkeypatch):
+    """Host tensors stand for the GPU's; what would go to the library is looked at instead of run."""
+    sent = []
+    monkeypatch.setattr(M, "_device_of", lambda t, name: t.get_device())
+    monkeypatch.setattr(M, "_workspace", lambda n, dev: torch.empty(n + 16, dtype=torch.uint8))
+    monkeypatch.setattr(M, "_run", lambda dev, entry, *args: sent.append(args))
+    rows, cols, f16 = 4, 64, torch.float16
+    x, y, vec = torch.zeros(rows, cols, dtype=f16), torch.zeros(rows, cols, dtype=f16), torch.zeros(rows)
+    w = torch.zeros(32, cols, dtype=f16)
+    ck = M.Checkpoint(_bytes(rows, cols), _bytes(rows, 2), cols)
+
+    def struct():
+        del sent[:]
+        if call == "save":
+            M.checkpoint_save(x, ck)
+        elif call == "load":
+            M.checkpoint_load(ck, x)
+        elif call == "norm saves":
+            M.layernorm_forward(x, None, None, y, None, vec, save=ck)
+        elif call == "norm reads":
+            M.layernorm_forward(ck, None, None, y, None, vec)
+        elif call == "norm backward":
+            M.layernorm_backward(x, ck, None, None, vec, y, None, None)
+        else:
+            M.gated_ffn_backward(torch.zeros(rows, 32, dtype=f16), ck, w, w, y, w.clone(), w.clone())
+        for a in sent[0]:
+            a = getattr(a, "_obj", a)  # a byref
+            if isinstance(a, M._GatedFfn):
+                return a.x_ckpt.contents
+            if isinstance(a, M._Checkpoint):
+                return a
+        raise AssertionError("no checkpoint among the arguments")
+
+    def same():
+        c = struct()
+        return (c.codes, c.ld, c.scales, c.ld_scales, c.fmt) == (
+            ck.codes.data_ptr(), ck.codes.stride(0), ck.scales.data_ptr(), ck.scales.stride(0), ck.fmt)
+
+    first = ck.codes, ck.scales  # alive: no address is used twice
+    assert same()
+    ck.codes = _bytes(rows, cols + 5)
+    assert same() and ck.codes.data_ptr() != first[0].data_ptr()
+    ck.scales = _bytes(rows, 7)
+    assert same()
+    ck.codes.data = _bytes(rows, cols + 32)
+    assert same()
+    ck.codes.set_(_bytes(rows, cols + 64))
+    assert same()
+    ck.scales.resize_(rows, 100000)
+    assert same()
+    ck.fmt = M.E5M2
+    assert same()
+    # what no longer fits is refused, not read with the shape it had
+    ck.codes = _bytes(rows + 1, cols)
+    with pytest.raises(ValueError):
+        struct()
+    ck.codes = _bytes(rows, cols).expand(rows, cols)[:, :cols - 1]
+    with pytest.raises(ValueError):
+        struct()
+    ck.codes, ck.scales = _bytes(1, cols).expand(rows, cols), _bytes(rows, 2)
+    if call in ("save", "norm saves"):
+        with pytest.raises(ValueError):
+            struct()
+    else:
+        assert same()
+    ck.codes, ck.cols = _bytes(rows, cols), 63
+    with pytest.raises(ValueError):
+        struct()
+    ck.codes, ck.cols = torch.zeros(rows, cols, dtype=f16), cols
+    with pytest.raises(TypeError):
+        struct()
+    ck.codes = first[0]
+    assert same() and (ck.rows, ck.device) == (rows, -1)
