@@ -45,8 +45,9 @@ struct Frag<bf16> {
 
 // ------------------------------------------------------------ activation ---
 
-// act(g) and act'(g). The exponential and the reciprocal are the hardware's
-// (one unit in the last place of binary32 each).
+// act(g) and act'(g). The exponential (of the argument times log2 e, which makes
+// the result off by about |argument| units in the last place of binary32) and
+// the reciprocal (one unit) are the hardware's.
 template <int ACT>
 __device__ __forceinline__ void act_and_grad(float g, float* a, float* d) {
   if constexpr (ACT == MSAMP_ACT_SILU) {
@@ -54,7 +55,8 @@ __device__ __forceinline__ void act_and_grad(float g, float* a, float* d) {
     *a = g * s;
     *d = s * __builtin_fmaf(g, 1.0f - s, 1.0f);
   } else if constexpr (ACT == MSAMP_ACT_GELU) {
-    const float phi = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+    // erfc keeps the digits of the left tail, which 1 + erf cancels (none left from -5.5 on)
+    const float phi = 0.5f * erfcf(g * -0.70710678118654752f);
     *a = g * phi;
     *d = phi + g * 0.39894228040143268f * __expf(-0.5f * g * g);
   } else {

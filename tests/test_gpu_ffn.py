@@ -403,3 +403,39 @@ def test_every_cut(t, k, f, dtype, act):
             first = {n: v.clone() for n, v in got.items()}
             M.gated_ffn_backward(dh, x, wg, wu, got["dx"], got["dw_gate"], got["dw_up"], act=act, h=got["h"])
             assert all(torch.equal(first[n], got[n]) for n in got)
+
+
+@pytest.mark.parametrize("tokens", [41, 300])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("act", list(M.ACTIVATIONS))
+def test_activations_keep_their_digits_in_the_tails(act, dtype, tokens):
+    """Gates from -8 to 6, each exact (x = [gate, 1], one inner unit that copies the gate and has u = 1), so that h
+    and du are act(g), and dg is act'(g), with bounds relative to their values."""
+    dt = DT[dtype]
+    g = torch.linspace(-8, 6, tokens, dtype=torch.float64).to(dt)
+    x = torch.stack([g, torch.ones_like(g)], 1).cuda()
+    one = torch.tensor([[1.0, 0.0]], dtype=dt, device="cuda")
+    up = torch.tensor([[0.0, 1.0]], dtype=dt, device="cuda")
+    dh = torch.ones(tokens, 1, dtype=dt, device="cuda")
+    h, h2, dx = torch.empty_like(dh), torch.empty_like(dh), torch.empty_like(x)
+    dw = torch.empty(1, 2, device="cuda"), torch.empty(1, 2, device="cuda")
+    M.gated_ffn_forward(x, one, up, h, act=act)
+    M.gated_ffn_backward(dh, x, one, up, dx, *dw, act=act, h=h2)
+    g = g.double()
+    a, d, _ = R.act_parts(g, act)
+    if act == "gelu":
+        # phi: two roundings of erfc's argument z, to which its value is g^2 + 2 times as sensitive, and 16 units
+        # (32 U) for erfc itself. The density: |g|^2 / 2 loses one rounding, the exponential 2 |argument| + 4.
+        phi, slope = a.abs() / g.abs().clamp_min(1e-300), (d - torch.where(g == 0, 0.5, a / g)).abs()
+        ea = (2 * (g * g + 2) + 36) * R.U * a.abs()
+        ed = (2 * (g * g + 2) + 36) * R.U * phi + (2 * g * g + 16) * R.U * slope + R.U * d.abs()
+    else:
+        # s = 1 / (1 + e^-E): E is off by at most 4 U relative, the exponential by 2 |E| + 4, reciprocal and
+        # products by a few more; both terms of the slope carry them, the second through s (1 - s)
+        E = g.abs() if act == "silu" else 1.6 * (g + 0.044715 * g ** 3).abs()
+        s = torch.where(g == 0, 0.5, a / g)
+        ea = (8 * E + 40) * R.U * a.abs()
+        ed = (8 * E + 40) * R.U * (s + (d - s).abs()) + 4 * R.U * g.abs() * s * (1 + g * g)
+    for name, got, ref, err in (("h", h[:, 0], a, ea), ("h again", h2[:, 0], a, ea), ("du", dx[:, 1], a, ea),
+                                ("dg", dx[:, 0], d, ed)):
+        R.assert_near(got, ref, err, act + " " + name)
