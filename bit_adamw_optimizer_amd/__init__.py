@@ -235,6 +235,8 @@ def lib():
         for f in ("msamp_gated_ffn_forward_workspace", "msamp_gated_ffn_backward_workspace"):
             getattr(L, f).argtypes = [ffn]
             getattr(L, f).restype = i64
+        L.msamp_gated_ffn_plan.argtypes = [ffn, ctypes.c_int, ctypes.POINTER(i32)]
+        L.msamp_gated_ffn_plan.restype = st
         for f in ("msamp_gated_ffn_forward", "msamp_gated_ffn_backward"):
             getattr(L, f).argtypes = [ffn, vp, i64, vp]
             getattr(L, f).restype = st

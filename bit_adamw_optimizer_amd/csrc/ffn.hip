@@ -1319,6 +1319,20 @@ msamp_status ffn_backward_workspace(const msamp_gated_ffn& a, int64_t* bytes) {
   return MSAMP_OK;
 }
 
+void ffn_plan(const msamp_gated_ffn& a, bool backward, int32_t* plan) {
+  const int64_t T = a.tokens, K = a.hidden, F = a.ffn;
+  for (int i = 0; i < 6; ++i) plan[i] = 0;
+  if (T == 0 || K == 0 || F == 0) return;
+  Cut x, w;
+  if (!few_rows(T, F, K)) {
+    plan[0] = 64 * choose_projection(backward ? kRecompute : kForward, T, F, K, &x);
+    plan[1] = (int32_t)x.splits;
+  }
+  if (!backward) return;
+  plan[2] = plan[4] = 64 * choose_gradients(T, K, F, &x, &w);
+  plan[3] = (int32_t)x.splits, plan[5] = (int32_t)w.splits;
+}
+
 msamp_status ffn_forward(const msamp_gated_ffn& a, void* ws, hipStream_t s) {
   Arena arena = {(char*)ws};
   return forward(a, arena, true, s);

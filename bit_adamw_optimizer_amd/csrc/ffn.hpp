@@ -13,6 +13,8 @@ namespace msamp {
 // Bytes of workspace of a call, and the call itself (arguments checked).
 msamp_status ffn_forward_workspace(const msamp_gated_ffn& a, int64_t* bytes);
 msamp_status ffn_backward_workspace(const msamp_gated_ffn& a, int64_t* bytes);
+// msamp_gated_ffn_plan's numbers.
+void ffn_plan(const msamp_gated_ffn& a, bool backward, int32_t* plan);
 msamp_status ffn_forward(const msamp_gated_ffn& a, void* ws, hipStream_t s);
 msamp_status ffn_backward(const msamp_gated_ffn& a, void* ws, hipStream_t s);
 

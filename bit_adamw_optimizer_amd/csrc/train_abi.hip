@@ -359,6 +359,16 @@ int64_t msamp_gated_ffn_backward_workspace(const msamp_gated_ffn* args) {
   });
 }
 
+msamp_status msamp_gated_ffn_plan(const msamp_gated_ffn* args, int backward, int32_t* plan) {
+  return guarded([&]() -> msamp_status {
+    clear_error();
+    MSAMP_TRY(check_ffn(args, backward != 0));
+    if (plan == nullptr) return invalid("plan is NULL");
+    ffn_plan(*args, backward != 0, plan);
+    return MSAMP_OK;
+  });
+}
+
 msamp_status msamp_gated_ffn_forward(const msamp_gated_ffn* args, void* workspace, int64_t workspace_bytes,
                                      void* stream) {
   return guarded([&]() -> msamp_status {

@@ -659,6 +659,16 @@ msamp_status msamp_gated_ffn_forward(const msamp_gated_ffn* args, void* workspac
 msamp_status msamp_gated_ffn_backward(const msamp_gated_ffn* args, void* workspace, int64_t workspace_bytes,
                                       void* stream);
 
+/*
+ * msamp_gated_ffn_plan -- TEST AID (host only): how the library cuts the
+ * products of a call with these arguments, so that a test knows which kernels
+ * it runs. plan[0], plan[1]: rows of a tile and parts of the sum of the gate
+ * and up projections; of the backward pass also plan[2], plan[3] of dx and
+ * plan[4], plan[5] of the weights' gradients. A tile of 0 rows: the kernel for
+ * few tokens, or a product that is not formed.
+ */
+msamp_status msamp_gated_ffn_plan(const msamp_gated_ffn* args, int backward, int32_t plan[6]);
+
 /* Frees every cached device table of the library (all devices) that is not
  * pinned by a graph capture, after waiting for the devices to finish. Safe to
  * call at any time from one thread while no other library call runs. */

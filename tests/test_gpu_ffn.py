@@ -378,7 +378,7 @@ def test_in_a_graph_and_on_another_stream():
         assert all(torch.equal(p, q) for p, q in zip(got, outs))
 
 
-# sizes that are cut in each way: tiles of 64, 128 and 256 rows, sums over k in one part and in several
+# sizes with tiles of 64 and 128 rows, sums over k in one part and in several (test_gpu_ffn_cuts.py: every cut)
 @pytest.mark.parametrize("t,k,f,dtype,act", [(70, 2600, 200, "f16", "silu"), (1500, 200, 130, "bf16", "silu"),
                                              (200, 130, 2100, "f16", "gelu"), (300, 264, 9000, "bf16", "gelu_tanh"),
                                              (2050, 264, 4100, "bf16", "silu"), (64, 1500, 1030, "f16", "silu"),
