@@ -300,7 +300,11 @@ __global__ __launch_bounds__(WAVES* GROUPS * 64) void k_norm_backward(NormArgs a
   const float inv = 1.0f / (float)cols;
   const bool centered = a.mean != nullptr, bias = a.dbias != nullptr;
   // With several pieces a lane, registers are short: the weights are then read
-  // for every row (from cache), and no row is loaded ahead.
+  // for every row (from cache), and no row is loaded ahead. A thread of 1,024
+  // has 128 registers, and what it holds of four pieces (beyond 16,384 columns)
+  // does not fit: 106 to 179 registers go through scratch (264 to 512 bytes a
+  // lane), of two pieces up to 16. 4,096 rows, bfloat16: 16,384 columns take 96
+  // us (4.2 TB/s), 32,768 columns 501 us (1.6 TB/s); binary32 159 and 634 us.
   constexpr bool kKeep = NCH == 1;
   constexpr int kAhead = !kKeep ? 0 : (CK && sizeof(T) == 2 && WAVES >= 4 ? 2 : 1);
   float w[NCH][8], sw[NCH][8], sb[NCH][8];

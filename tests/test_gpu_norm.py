@@ -348,3 +348,25 @@ def test_in_a_graph_with_eager_work_between():
         torch.cuda.synchronize()
         for p, q in zip(got, (y, mean, rstd, dx, dw, db, ck.codes, ck.scales)):
             assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows,cols", [(3, 8200), (300, 12007), (700, 16384), (3, 16392), (5, 16385), (256, 20001),
+                                       (257, 24000), (600, 16390), (3, 32761), (300, 32768), (515, 32767)])
+def test_wide_rows_over_several_workgroups(rows, cols, dtype):
+    """Two and four pieces of 8 columns a lane, one and several rows a workgroup, sums joined from their parts: from a
+    matrix and from a checkpoint, added to what is there."""
+    dt = DT[dtype]
+    x, dy = matrix(rows, cols, dt, 0, 1, offset=0.5), matrix(rows, cols, dt, 0, 2, size=0.1)
+    w, _ = weights(cols, dt, 3)
+    ck = M.new_checkpoint(rows, cols, M.E5M2 if rows % 2 else M.E4M3)
+    for centered in (True, False):
+        _, mean, rstd = forward(x, w, None, centered, save=ck)
+        xv = torch.empty(rows, cols, device="cuda")
+        M.checkpoint_load(ck, xv)
+        for src, val in ((x, x), (ck, xv)):
+            first = backward(dy, src, w, mean, rstd)
+            check_backward(dy, val, w, mean, rstd, first)
+            dw, db = torch.full((cols,), 2.0, device="cuda"), torch.full((cols,), -3.0, device="cuda")
+            dx, dw2, db2 = backward(dy, src, w, mean, rstd, True, dw, db)
+            assert torch.equal(dx, first[0]) and torch.equal(dw2, 2.0 + first[1]) and torch.equal(db2, -3.0 + first[2])
