@@ -1060,7 +1060,11 @@ def gated_ffn_backward(dh: torch.Tensor, x, w_gate: torch.Tensor, w_up: torch.Te
     Checkpoint of it; gate and up are formed again. dw_gate and dw_up are
     float32 (what amax and the quantizing steps take; accumulate adds to what
     is there) or of the weights' dtype. h, if given, receives the forward
-    pass's product again (the next projection's gradient needs it)."""
+    pass's product again (the next projection's gradient needs it).
+
+    The gradients of gate and up are rounded to dh's dtype before they are
+    summed: in float16 values beyond 65504 become infinite and those of 2^-25
+    or less 0, so dh has to carry a loss scale that keeps them between."""
     dev, _, _ = _leading(dh, "dh")
     dt = dh.dtype
     a = _gated_ffn(x, w_gate, w_up, act, dev, dt, dh.shape[0])

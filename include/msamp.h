@@ -561,7 +561,10 @@ msamp_status msamp_checkpoint_load(int64_t rows, int64_t cols, const msamp_check
  *   rstd = 1 / sqrt(sum((x - mu)^2) / cols + eps)
  *   y = (x - mu) * rstd * weight + bias
  * in binary32, the row held in registers (the variance is taken around the
- * mean), y rounded once to dtype.
+ * mean), y rounded once to dtype. The sums have binary32's range: a row of
+ * finite values whose squares sum to 2^128 or more gets rstd 0, and with it
+ * y = bias and, in the backward pass, dx = 0 (RMS norm, or a finite mean). With
+ * cols 0 nothing is written.
  *   x          device, dtype; or NULL, with x_ckpt the checkpoint that is
  *              read in its place (values in binary32, clamped to its range)
  *   weight     device [cols] of weight_dtype, or NULL for 1
@@ -617,7 +620,12 @@ typedef enum { MSAMP_ACT_SILU = 0, MSAMP_ACT_GELU = 1, MSAMP_ACT_GELU_TANH = 2 }
  * pass takes x only). The products are summed in binary32; g and u stay in
  * binary32; dg and du are rounded to dtype, as operands of the matrix
  * instructions; a checkpoint's values are rounded to dtype. h and dx are
- * rounded once.
+ * rounded once. With MSAMP_F16 that costs range as well as digits: a value of
+ * dg or du beyond 65504 becomes infinite, one below 2^-14 loses digits and one
+ * of 2^-25 or less becomes 0 before it is summed, also where the weights'
+ * gradients are binary32, so dh has to be scaled (as a loss is) to keep them
+ * between; a checkpoint's value is clamped to +-65504 and loses digits below
+ * 2^-14. MSAMP_BF16 has binary32's range.
  *   h          forward: out. Backward: out, the same product again (the down
  *              projection's gradient needs it), or NULL
  *   dx         backward: out

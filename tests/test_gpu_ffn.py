@@ -439,3 +439,19 @@ def test_activations_keep_their_digits_in_the_tails(act, dtype, tokens):
     for name, got, ref, err in (("h", h[:, 0], a, ea), ("h again", h2[:, 0], a, ea), ("du", dx[:, 1], a, ea),
                                 ("dg", dx[:, 0], d, ed)):
         R.assert_near(got, ref, err, act + " " + name)
+
+
+@pytest.mark.parametrize("dtype,gate,dh,want", [
+    ("f16", 64.0, 2.0 ** 9, 2.0 ** 15), ("f16", 64.0, 2.0 ** 10, float("inf")),
+    ("bf16", 64.0, 2.0 ** 10, 2.0 ** 16), ("bf16", 64.0, 2.0 ** -40, 2.0 ** -34),
+    # silu(0.5) = 0.311: of the smallest float16 it leaves less than half, of four of them 1.24
+    ("f16", 0.5, 2.0 ** -24, 0.0), ("f16", 0.5, 2.0 ** -22, 2.0 ** -24)])
+def test_gradients_of_gate_and_up_have_the_range_of_their_type(dtype, gate, dh, want):
+    """du = dh act(g) is rounded to the type before it is summed, here into a binary32 gradient of one token."""
+    dt = DT[dtype]
+    x = torch.tensor([[gate, 1.0]], dtype=dt, device="cuda")
+    wg = torch.tensor([[1.0, 0.0]], dtype=dt, device="cuda")
+    wu = torch.tensor([[0.0, 2.0 ** -14]], dtype=dt, device="cuda")
+    a, b = torch.empty(1, 2, device="cuda"), torch.empty(1, 2, device="cuda")
+    M.gated_ffn_backward(torch.full((1, 1), dh, dtype=dt, device="cuda"), x, wg, wu, torch.empty_like(x), a, b)
+    assert b[0, 1].item() == want

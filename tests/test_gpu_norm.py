@@ -370,3 +370,27 @@ def test_wide_rows_over_several_workgroups(rows, cols, dtype):
             dw, db = torch.full((cols,), 2.0, device="cuda"), torch.full((cols,), -3.0, device="cuda")
             dx, dw2, db2 = backward(dy, src, w, mean, rstd, True, dw, db)
             assert torch.equal(dx, first[0]) and torch.equal(dw2, 2.0 + first[1]) and torch.equal(db2, -3.0 + first[2])
+
+
+def test_rows_whose_squares_leave_binary32():
+    """The sums are binary32's: where the sum of the squares exceeds it, rstd is 0, and so are y (without a bias) and
+    dx. The other rows are as they are without it."""
+    x, dy = matrix(8, 700, torch.float32, 0, 1), matrix(8, 700, torch.float32, 0, 2)
+    _, b = weights(700, torch.float32, 3)
+    keep = [0, 1, 3, 4, 5, 7]
+    big = x.clone()
+    big[2], big[6, 9] = torch.finfo(torch.float32).max, 1e20
+    for bias in (None, b):
+        clean, _, r = forward(x, None, bias, False)
+        y, _, rstd = forward(big, None, bias, False)
+        assert (rstd[[2, 6]] == 0).all() and torch.equal(rstd[keep], r[keep]) and torch.equal(y[keep], clean[keep])
+        want = torch.zeros(700, device="cuda") if bias is None else bias
+        assert torch.equal(y[2], want) and torch.equal(y[6], want)
+    dx, dw, _ = backward(dy, big, None, None, rstd)
+    ref = backward(dy, x, None, None, r)
+    assert not dx[[2, 6]].any() and torch.equal(dx[keep], ref[0][keep]) and torch.isfinite(dw).all()
+    # around the mean, as long as their sum is within binary32
+    big[2] = torch.where(torch.arange(700, device="cuda") % 2 == 0, 1e20, -1e20)
+    y, mean, rstd = forward(big, None, None, True)
+    assert (rstd[[2, 6]] == 0).all() and torch.isfinite(mean).all() and not y[[2, 6]].any()
+    assert not backward(dy, big, None, mean, rstd)[0][[2, 6]].any()
