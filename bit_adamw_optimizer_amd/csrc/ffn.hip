@@ -699,6 +699,7 @@ __global__ __launch_bounds__(kThreads) void k_gradients_join(Product x, Product 
 }
 
 constexpr int kUnits = 256;  // workgroups that run at a time, one a compute unit
+constexpr int64_t kMaxUnits = UINT32_MAX / kThreads;  // of a launch
 
 // How a product is cut: its tiles, and parts of the sum over k.
 struct Cut {
@@ -713,13 +714,14 @@ int64_t steps_of(int mode, int64_t K) { return (K + kStepK - 1) / kStepK * (mode
 int64_t tiles_of(int mode, const Cut& c) { return (int64_t)c.tiles_r * c.tiles_c * (mode == kDw ? 2 : 1); }
 
 // The cut with tiles of 64 * fr rows and the sums in 'splits' parts of whole
-// steps (false: there is none, or it fills the device more than four times).
+// steps (false: there is none, or it fills the device more than four times, or
+// has more units than a launch).
 bool cut_of(int mode, int fr, int64_t splits, int64_t R, int64_t C, int64_t K, Cut* c) {
   const int64_t steps = steps_of(mode, K), tc = is_pair(mode) ? 128 : 256;
   const int64_t part = (steps + splits - 1) / splits;
   if ((steps + part - 1) / part != splits || (splits > 1 && part < 2)) return false;
   *c = {(uint32_t)((R + 64 * fr - 1) / (64 * fr)), (uint32_t)((C + tc - 1) / tc), (uint32_t)splits, part, 0};
-  if (splits == 1) return true;
+  if (splits == 1) return tiles_of(mode, *c) <= kMaxUnits;
   if (tiles_of(mode, *c) > 4 * kUnits / splits) return false;
   c->bytes = tiles_of(mode, *c) * splits * (64 * fr * kTileC * 4);
   return true;
@@ -762,10 +764,10 @@ int candidates(int mode, int fr, int64_t R, int64_t C, int64_t K, Candidate* out
   return n;
 }
 
-// The cut of a projection with the least estimated time, and its fr.
+// The cut of a projection with the least estimated time, and its fr (0: none).
 int choose_projection(int mode, int64_t R, int64_t C, int64_t K, Cut* best) {
   double least = 1e30;
-  int fr_best = 4;
+  int fr_best = 0;
   Candidate c[std::size(kSplits)];
   for (int fr = 4; fr >= 1; fr /= 2) {
     const int n = candidates(mode, fr, R, C, K, c);
@@ -785,14 +787,16 @@ int choose_projection(int mode, int64_t R, int64_t C, int64_t K, Cut* best) {
 // time of the longer unit (a quarter more with others after it on the device),
 // or of all of them, half a unit of dW, which come last, and 0.15 of the longer
 // (fitted to 18 problems: within 5% of the best cut on average, 27% at most).
+// 0: none fits a launch.
 int choose_gradients(int64_t T, int64_t K, int64_t F, Cut* x, Cut* w) {
   double least = 1e30;
-  int fr_best = 4;
+  int fr_best = 0;
   Candidate cx[std::size(kSplits)], cw[std::size(kSplits)];
   for (int fr = 4; fr >= 1; fr /= 2) {
     const int nx = candidates(kDx, fr, T, K, F, cx), nw = candidates(kDw, fr, F, K, T, cw);
     for (int i = 0; i < nx; ++i)
       for (int j = 0; j < nw; ++j) {
+        if (cx[i].units + cw[j].units > kMaxUnits) continue;
         double t = cx[i].unit > cw[j].unit ? cx[i].unit : cw[j].unit;
         if (cx[i].units + cw[j].units > kUnits) {
           const double all =
@@ -868,7 +872,7 @@ struct Arena {
   }
 };
 
-constexpr int64_t kMaxUnits = UINT32_MAX / kThreads;
+msamp_status too_many_tiles() { return fail(MSAMP_E_INVALID_ARG, "the product has too many tiles"); }
 
 // Plans the tiled projections (taking their partial sums' workspace) and runs
 // them.
@@ -876,7 +880,7 @@ template <int MODE>
 msamp_status tiled_projections(msamp_kernel_kind kind, int dtype, Product p, Arena& ws, bool run, hipStream_t s) {
   Cut c;
   const int fr = choose_projection(MODE, p.R, p.C, p.K, &c);
-  if (tiles_of(MODE, c) * c.splits > kMaxUnits) return fail(MSAMP_E_INVALID_ARG, "the product has too many tiles");
+  if (fr == 0) return too_many_tiles();
   apply(c, (float*)ws.take(c.bytes), &p);
   if (!run) return MSAMP_OK;
   MSAMP_LAUNCH(kind, s, launch_projections<MODE>(dtype, fr, p, false, s));
@@ -888,8 +892,7 @@ msamp_status tiled_projections(msamp_kernel_kind kind, int dtype, Product p, Are
 msamp_status gradients(int dtype, Product x, Product w, Arena& ws, bool run, hipStream_t s) {
   Cut cx, cw;
   const int fr = choose_gradients(x.R, x.C, x.K, &cx, &cw);
-  if (tiles_of(kDx, cx) * cx.splits + tiles_of(kDw, cw) * cw.splits > kMaxUnits)
-    return fail(MSAMP_E_INVALID_ARG, "the product has too many tiles");
+  if (fr == 0) return too_many_tiles();
   apply(cx, (float*)ws.take(cx.bytes), &x);
   apply(cw, (float*)ws.take(cw.bytes), &w);
   if (!run) return MSAMP_OK;
@@ -1319,18 +1322,21 @@ msamp_status ffn_backward_workspace(const msamp_gated_ffn& a, int64_t* bytes) {
   return MSAMP_OK;
 }
 
-void ffn_plan(const msamp_gated_ffn& a, bool backward, int32_t* plan) {
+msamp_status ffn_plan(const msamp_gated_ffn& a, bool backward, int32_t* plan) {
   const int64_t T = a.tokens, K = a.hidden, F = a.ffn;
   for (int i = 0; i < 6; ++i) plan[i] = 0;
-  if (T == 0 || K == 0 || F == 0) return;
+  if (T == 0 || K == 0 || F == 0) return MSAMP_OK;
   Cut x, w;
   if (!few_rows(T, F, K)) {
     plan[0] = 64 * choose_projection(backward ? kRecompute : kForward, T, F, K, &x);
+    if (plan[0] == 0) return too_many_tiles();
     plan[1] = (int32_t)x.splits;
   }
-  if (!backward) return;
+  if (!backward) return MSAMP_OK;
   plan[2] = plan[4] = 64 * choose_gradients(T, K, F, &x, &w);
+  if (plan[2] == 0) return too_many_tiles();
   plan[3] = (int32_t)x.splits, plan[5] = (int32_t)w.splits;
+  return MSAMP_OK;
 }
 
 msamp_status ffn_forward(const msamp_gated_ffn& a, void* ws, hipStream_t s) {

@@ -14,7 +14,7 @@ namespace msamp {
 msamp_status ffn_forward_workspace(const msamp_gated_ffn& a, int64_t* bytes);
 msamp_status ffn_backward_workspace(const msamp_gated_ffn& a, int64_t* bytes);
 // msamp_gated_ffn_plan's numbers.
-void ffn_plan(const msamp_gated_ffn& a, bool backward, int32_t* plan);
+msamp_status ffn_plan(const msamp_gated_ffn& a, bool backward, int32_t* plan);
 msamp_status ffn_forward(const msamp_gated_ffn& a, void* ws, hipStream_t s);
 msamp_status ffn_backward(const msamp_gated_ffn& a, void* ws, hipStream_t s);
 

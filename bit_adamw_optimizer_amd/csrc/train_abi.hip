@@ -364,8 +364,7 @@ msamp_status msamp_gated_ffn_plan(const msamp_gated_ffn* args, int backward, int
     clear_error();
     MSAMP_TRY(check_ffn(args, backward != 0));
     if (plan == nullptr) return invalid("plan is NULL");
-    ffn_plan(*args, backward != 0, plan);
-    return MSAMP_OK;
+    return ffn_plan(*args, backward != 0, plan);
   });
 }
 

@@ -611,7 +611,9 @@ typedef enum { MSAMP_ACT_SILU = 0, MSAMP_ACT_GELU = 1, MSAMP_ACT_GELU_TANH = 2 }
  * call). x [tokens, hidden]; w_gate, w_up [ffn, hidden], as the gate and up
  * projections are stored; h, dh [tokens, ffn]; all of dtype, MSAMP_F16 or
  * MSAMP_BF16. Every size is at most 2^31 - 1; hidden is at most 2^22 - 64 and,
- * in the backward pass, ffn at most 2^21 - 64.
+ * in the backward pass, ffn at most 2^21 - 64. A launch has at most 2^23 - 1
+ * tiles (h: 256 x 128; dx and both weights' gradients together: 256 x 256);
+ * larger products are refused.
  *   forward:   g = x w_gate^T, u = x w_up^T, h = act(g) * u
  *   backward:  from dh: du = dh * act(g), dg = dh * u * act'(g),
  *              dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x

@@ -306,3 +306,27 @@ def test_a_checkpoint_is_taken_as_its_fields_are_at_the_call(call, monkeypatch):
         struct()
     ck.codes = first[0]
     assert same() and (ck.rows, ck.device) == (rows, -1)
+
+
+@pytest.mark.parametrize("tokens,ffn,forward,backward", [
+    (1 << 24, 1, True, True), (1 << 24, 96, True, True), (1 << 30, 1, True, True), (600000000, 96, True, True),
+    # tiles of 256 rows: 2^23 - 1 of them, with those of the weights' gradients in the backward pass
+    (((1 << 23) - 3) * 256, 1, True, True), (((1 << 23) - 3) * 256 + 1, 1, True, False),
+    (((1 << 23) - 1) * 256, 96, True, False), ((1 << 31) - 1, 1, False, False), (1 << 30, 300, False, False)])
+def test_how_many_tokens_are_planned(tokens, ffn, forward, backward):
+    """The largest numbers of tokens are planned up to the limit the header states, and refused beyond it."""
+    for which, fits in (("forward", forward), ("backward", backward)):
+        a = _ffn(tokens=tokens, ffn=ffn, ldh=ffn, lddh=ffn)
+        # far apart: nothing overlaps
+        a.x, a.h, a.dh, a.dx = (i << 44 for i in range(1, 5))
+        n = getattr(M.lib(), "msamp_gated_ffn_%s_workspace" % which)(ctypes.byref(a))
+        plan = (ctypes.c_int32 * 6)()
+        st = M.lib().msamp_gated_ffn_plan(ctypes.byref(a), int(which == "backward"), plan)
+        assert (n >= 0, st == 0) == (fits, fits), (which, n, plan[:], _err())
+        if not fits:
+            assert n == -1 and "too many tiles" in _err()
+        else:
+            # the operands of the gradients' products, 64-column pieces of dg and du in 16 bits, and nothing
+            # like it in the forward pass, whose operands here lie as they are read
+            gates = tokens * 2 * (-(-ffn // 64) * 64) * 2 if which == "backward" else 0
+            assert gates <= n <= gates + (1 << 28), (which, n)
