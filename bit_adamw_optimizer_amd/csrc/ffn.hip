@@ -19,10 +19,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-typedef f16 f16x4 __attribute__((ext_vector_type(4)));
-typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 #define LDS __attribute__((address_space(3)))
 
@@ -247,8 +244,10 @@ struct Acc {
   f32x16 v[FR][2];
 };
 
-// The loads of step 'next' into the stage wr; zeros from step 'end' on (no
-// branch, so that they can be spread between matrix instructions).
+// The loads of step 'next' into the stage wr; zeros from step 'end' on. Those
+// of operands with k along (the projections) have no branch, so that they are
+// spread between matrix instructions. The bounds of one with k across (both
+// gradients) compile to a uniform branch, at which scheduling ends.
 template <typename T, int MODE, int FR>
 __device__ __forceinline__ void load_step(const Product& p, LDS char* wr, const Along<FR>& ra, const Across<FR>& rx,
                                           const Along<4>& ca, const Across<4>& cx, const Across<4>& cy, int64_t row0,
@@ -337,8 +336,10 @@ __device__ __forceinline__ void interleave() {
 // of this stage have arrived; the barrier there lets the waves write over it
 // (the loads of step i + 2, into 'again', the same stage) and, as every wave
 // has waited for its own loads of step i + 1, read the other stage 'nx'. So the
-// loads have a whole step to arrive, and no wave meets the barrier without
-// matrix instructions to go on with.
+// loads have a whole step to arrive. In the projections a wave goes on behind
+// the barrier with matrix instructions between its reads and loads; in the
+// gradients the branch in load_step keeps 8 to 12 LDS reads, the loads and their
+// descriptors before the section's first one.
 template <typename T, int MODE, int FR>
 __device__ __forceinline__ void step(const Product& p, const LDS char* __restrict__ rd,
                                      const LDS char* __restrict__ nx, LDS char* __restrict__ again,

@@ -1,5 +1,7 @@
 // ffn.hpp -- internal interface of the gated feed-forward block's kernels
-// (ffn.hip): what one call needs, planned once from its arguments.
+// (ffn.hip). Each function plans the call from its arguments anew (the cut of
+// the products by a cost model, about a microsecond on the host): an entry
+// point once for the workspace it checks and once for the launches.
 #pragma once
 
 #include <hip/hip_runtime.h>

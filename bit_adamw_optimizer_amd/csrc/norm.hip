@@ -521,7 +521,8 @@ void norm_fwd_any(const NormArgs& a, hipStream_t s) {
 // 8,192 rows of 768 columns took 22 us against 15). At most 256 workgroups of
 // wide rows (one per compute unit, whose partial sums are 3% of the traffic),
 // 512 of narrow ones (32,000 rows of 1,024 columns from a checkpoint: 38 us
-// against 43 with 256, 8,192 x 768: equal, 2,000 x 1,000 binary32: 15 against 12).
+// against 43 with 256, 8,192 x 768: equal; the rule goes by the columns alone and
+// loses where few rows of binary32 meet it: 2,000 x 1,000, 15 against 12).
 int norm_rows(int64_t cols) {
   if (cols <= 512) return cols <= 128 ? 32 : (cols <= 256 ? 16 : 8);
   return cols <= 2048 ? 4 : (cols <= 4096 ? 2 : 1);
