@@ -104,9 +104,12 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 //
 // Bound by the matrix units at the clock that the power limit leaves (about 1.7
 // GHz): at 4096 tokens, hidden 4096, 11008 inner units, bf16, the forward
-// projections take 640 us (1150 TFLOP/s; instructions in the matrix units 62%
-// of the time), those of the backward pass 672 us (56%), both gradients 1256 us
-// (1176 TFLOP/s, 60%); LDS bank conflicts 1% to 3% of the LDS cycles. With
+// projections take 645 us (1145 TFLOP/s; instructions in the matrix units 62%
+// of the time), those of the backward pass 684 us (55%), both gradients 1273 us
+// (1160 TFLOP/s, 61%); LDS bank conflicts 1% to 3% of the LDS cycles. In a row
+// of launches under the profiler the forward projections slow down to 803 us
+// when the power limit acts and end at 710; passes with other work between them
+// took 608 to 645 us. With
 // zeros for operands the same code runs 15% faster. One workgroup of 8 waves a
 // compute unit holds 128 KB of LDS; 128 x 128 tiles on 4 waves, 32 k in four
 // stages, two such workgroups, and two groups of waves half a step apart were
