@@ -848,7 +848,6 @@ class Checkpoint:
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: int = E4M3):
         self.codes, self.scales, self.cols, self.fmt = codes, scales, int(cols), int(fmt)
-        _device_of(scales, "scales")
         self._arg("codes", _device_of(codes, "codes"))
 
     @property
@@ -863,10 +862,12 @@ class Checkpoint:
         """The fields as the library takes them, checked against the call's device and shape."""
         codes, scales, cols = self.codes, self.scales, self.cols
         groups = (cols + GROUP - 1) // GROUP
-        if codes.get_device() != device:
-            raise ValueError("%s is on %s, expected cuda:%d" % (name, codes.device, device))
-        if scales.get_device() != device:
-            raise ValueError("scales is on %s, expected %s" % (scales.device, codes.device))
+        if not isinstance(codes, torch.Tensor) or codes.get_device() != device:
+            if _device_of(codes, "codes") != device:
+                raise ValueError("%s is on %s, expected cuda:%d" % (name, codes.device, device))
+        if not isinstance(scales, torch.Tensor) or scales.get_device() != device:
+            if _device_of(scales, "scales") != device:
+                raise ValueError("scales is on %s, expected %s" % (scales.device, codes.device))
         if codes.element_size() != 1 or scales.element_size() != 1:
             raise TypeError("codes and scales must be bytes, not %s and %s" % (codes.dtype, scales.dtype))
         cshape, sshape = codes.shape, scales.shape

@@ -330,3 +330,13 @@ def test_how_many_tokens_are_planned(tokens, ffn, forward, backward):
             # like it in the forward pass, whose operands here lie as they are read
             gates = tokens * 2 * (-(-ffn // 64) * 64) * 2 if which == "backward" else 0
             assert gates <= n <= gates + (1 << 28), (which, n)
+
+
+@pytest.mark.parametrize("field", ["codes", "scales"])
+def test_a_checkpoint_without_its_tensors_is_refused(field, monkeypatch):
+    with monkeypatch.context() as m:
+        m.setattr(M, "_device_of", lambda t, name: t.get_device())
+        ck = M.Checkpoint(_bytes(4, 64), _bytes(4, 2), 64)
+    setattr(ck, field, None)
+    with pytest.raises(TypeError, match=field):
+        ck._arg("ckpt", -1, (4, 64))
