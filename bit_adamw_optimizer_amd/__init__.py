@@ -11,7 +11,10 @@ memory and streams.
 Around the step it has training operators that keep their activations in 8
 bits: activation checkpoints, layer norm / RMS norm and the gated
 feed-forward block, whose backward passes read a checkpoint and produce the
-binary32 gradients that the step's quantize takes.
+binary32 gradients that the step's quantize takes. At the model's ends and
+between its tokens stand the embedding (lookup and gradient), the gated linear
+recurrence, and two losses over the vocabulary with their gradients:
+distillation from a teacher's top logits and the clipped policy loss.
 
 Layouts (MS-AMP "Optimization Level" page, sections O2/O3 and the table):
   O2: grad FP8 (per-tensor scale), exp_avg FP8 E4M3 (own scale), exp_avg_sq
@@ -47,6 +50,9 @@ __all__ = [
     # training operators with 8-bit activation checkpoints
     "Checkpoint", "new_checkpoint", "checkpoint_save", "checkpoint_load",
     "layernorm_forward", "layernorm_backward", "gated_ffn_forward", "gated_ffn_backward", "ACTIVATIONS",
+    # operators at the ends of a model and between its tokens
+    "embedding_forward", "embedding_backward", "recurrence_forward", "recurrence_backward", "new_recurrence_states",
+    "distill_loss_forward", "distill_loss_backward", "policy_loss_forward", "policy_loss_backward",
     # state helpers
     "new_meta", "allocate_state", "flat_views", "state_bytes_per_param",
     # measurement and test aids
@@ -69,7 +75,8 @@ KERNELS = ["amax", "quantize_fp8", "dequantize_fp8", "step_pass1", "o2_pass2", "
            "o3_pass3", "finalize", "amax_finalize", "o2_delayed", "rmw_probe", "quantize_pass1",
            "read_probe", "copy_probe", "qp1_probe", "checkpoint_save", "checkpoint_load",
            "norm_forward", "norm_backward", "norm_reduce", "ffn_forward", "ffn_recompute", "ffn_gradients",
-           "ffn_layout", "ffn_reduce"]
+           "ffn_layout", "ffn_reduce", "embedding_forward", "embedding_sort", "embedding_backward",
+           "recurrence_forward", "recurrence_backward", "loss_forward", "loss_backward"]
 
 # msamp_activation by name
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
@@ -114,6 +121,33 @@ class _GatedFfn(ctypes.Structure):
                 ("dw_gate", ctypes.c_void_p), ("ld_dw_gate", ctypes.c_int64),
                 ("dw_up", ctypes.c_void_p), ("ld_dw_up", ctypes.c_int64),
                 ("dw_dtype", ctypes.c_int), ("dw_accumulate", ctypes.c_int)]
+
+
+class _Recurrence(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_int64) for k in ("batch", "time", "channels")]
+                + [("dtype", ctypes.c_int), ("length_bytes", ctypes.c_int), ("lengths", ctypes.c_void_p)]
+                + [f for k in ("x", "gate") for f in ((k, ctypes.c_void_p), (k + "_batch", ctypes.c_int64),
+                                                      (k + "_time", ctypes.c_int64))]
+                + [("states", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_batch", ctypes.c_int64),
+                   ("y_time", ctypes.c_int64), ("h0", ctypes.c_void_p), ("ld_h0", ctypes.c_int64),
+                   ("h_last", ctypes.c_void_p), ("ld_h_last", ctypes.c_int64)]
+                + [f for k in ("dy", "dx", "dgate") for f in ((k, ctypes.c_void_p), (k + "_batch", ctypes.c_int64),
+                                                              (k + "_time", ctypes.c_int64))]
+                + [("dh_last", ctypes.c_void_p), ("ld_dh_last", ctypes.c_int64), ("dh0", ctypes.c_void_p),
+                   ("ld_dh0", ctypes.c_int64)])
+
+
+class _VocabLoss(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("id_bytes", ctypes.c_int), ("logits", ctypes.c_void_p), ("ld_logits", ctypes.c_int64),
+                ("ids", ctypes.c_void_p), ("ld_ids", ctypes.c_int64), ("temperature", ctypes.c_double),
+                ("loss", ctypes.c_void_p), ("stats", ctypes.c_void_p), ("dloss", ctypes.c_void_p),
+                ("dlogits", ctypes.c_void_p), ("ld_dlogits", ctypes.c_int64),
+                ("top", ctypes.c_int64), ("teacher", ctypes.c_void_p), ("ld_teacher", ctypes.c_int64),
+                ("teacher_dtype", ctypes.c_int),
+                ("old_logp", ctypes.c_void_p), ("ref_logp", ctypes.c_void_p), ("advantages", ctypes.c_void_p),
+                ("logp", ctypes.c_void_p), ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
+                ("kl", ctypes.c_double)]
 
 
 _lib = None
@@ -239,6 +273,24 @@ def lib():
         L.msamp_gated_ffn_plan.restype = st
         for f in ("msamp_gated_ffn_forward", "msamp_gated_ffn_backward"):
             getattr(L, f).argtypes = [ffn, vp, i64, vp]
+            getattr(L, f).restype = st
+        ib = ctypes.c_int
+        L.msamp_embedding_forward.argtypes = [i64, i64, i64, vp, ib, vp, i64, dt, vp, i64, ctypes.c_double, vp]
+        L.msamp_embedding_forward.restype = st
+        L.msamp_embedding_backward_workspace.argtypes = [i64, i64, i64]
+        L.msamp_embedding_backward_workspace.restype = i64
+        L.msamp_embedding_backward.argtypes = [i64, i64, i64, vp, i64, dt, vp, ib, vp, i64, ctypes.c_double,
+                                               ctypes.c_int, vp, i64, vp]
+        L.msamp_embedding_backward.restype = st
+        rec, loss = ctypes.POINTER(_Recurrence), ctypes.POINTER(_VocabLoss)
+        for f, a in (("recurrence_forward", rec), ("recurrence_backward", rec), ("distill_forward", loss),
+                     ("policy_forward", loss)):
+            getattr(L, "msamp_" + f + "_workspace").argtypes = [a]
+            getattr(L, "msamp_" + f + "_workspace").restype = i64
+            getattr(L, "msamp_" + f).argtypes = [a, vp, i64, vp]
+            getattr(L, "msamp_" + f).restype = st
+        for f in ("msamp_distill_backward", "msamp_policy_backward"):
+            getattr(L, f).argtypes = [loss, vp]
             getattr(L, f).restype = st
         L.msamp_kernel_name.argtypes = [ctypes.c_int]
         L.msamp_kernel_name.restype = ctypes.c_char_p
@@ -1085,6 +1137,286 @@ def gated_ffn_backward(dh: torch.Tensor, x, w_gate: torch.Tensor, w_up: torch.Te
     n = _workspace_bytes(lib().msamp_gated_ffn_backward_workspace(a))
     ws = _workspace(n, dev)
     _run(dev, lib().msamp_gated_ffn_backward, a, None if ws is None else ws.data_ptr(), n)
+
+
+# -------------------- operators at the ends of a model and between its tokens ---
+
+CHUNK = 32  # steps between two saved states of the recurrence (MSAMP_RECURRENCE_CHUNK)
+_INTS = {torch.int32: 4, torch.int64: 8}
+
+
+def _ids(t, name: str, device: int, shape):
+    """(pointer, distance between rows, bytes of an id) of integers, a vector or a matrix."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s is not a tensor" % name)
+    n = _INTS.get(t.dtype)
+    if n is None:
+        raise TypeError("%s has dtype %s, expected int32 or int64" % (name, t.dtype))
+    if len(shape) == 1:
+        return _vector(t, name, device, t.dtype, shape[0]), 0, n
+    p, ld = _matrix(t, name, device, t.dtype, shape)
+    return p, ld, n
+
+
+def embedding_forward(ids: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, *, scale: float = 1.0) -> None:
+    """y[r] <- scale * weight[ids[r]]; zeros for an id outside the vocabulary
+    (-1: padding). ids int32 or int64 [rows], weight [vocab, cols] and y [rows,
+    cols] of one dtype: float32, float16 or bfloat16."""
+    dev, d, shape = _leading(y, "y")
+    rows, cols = shape
+    py, ldy = _matrix(y, "y", dev, y.dtype, shape, True)
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a tensor of two dimensions")
+    vocab = weight.shape[0]
+    pw, ldw = _matrix(weight, "weight", dev, y.dtype, (vocab, cols))
+    pi, _, ib = _ids(ids, "ids", dev, (rows,))
+    _run(dev, lib().msamp_embedding_forward, rows, vocab, cols, pi, ib, pw, ldw, d, py, ldy, scale)
+
+
+def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, dweight: torch.Tensor, *, scale: float = 1.0,
+                       accumulate: bool = False) -> None:
+    """dweight <- the gradient of embedding_forward's weight from dy: for every
+    id scale times the sum of its rows, in their order; float32 [vocab, cols],
+    what amax takes. accumulate adds it to what is there (a tied output
+    projection's gradient) and leaves the rows of absent ids alone."""
+    dev, d, shape = _leading(dy, "dy")
+    rows, cols = shape
+    pdy, lddy = _matrix(dy, "dy", dev, dy.dtype, shape)
+    if not isinstance(dweight, torch.Tensor) or dweight.dim() != 2:
+        raise ValueError("dweight must be a tensor of two dimensions")
+    vocab = dweight.shape[0]
+    pw, ldw = _matrix(dweight, "dweight", dev, torch.float32, (vocab, cols), True)
+    pi, _, ib = _ids(ids, "ids", dev, (rows,))
+    n = _embedding_workspace_bytes(rows, vocab, cols)
+    ws = _workspace(n, dev)
+    _run(dev, lib().msamp_embedding_backward, rows, vocab, cols, pdy, lddy, d, pi, ib, pw, ldw, scale,
+         1 if accumulate else 0, None if ws is None else ws.data_ptr(), n)
+
+
+@functools.lru_cache(maxsize=256)
+def _embedding_workspace_bytes(rows: int, vocab: int, cols: int) -> int:
+    return _workspace_bytes(lib().msamp_embedding_backward_workspace(rows, vocab, cols))
+
+
+def _cube(t, name: str, device: int, dtype, shape, written: bool = False):
+    """(pointer, distance between sequences, distance between steps) of a [batch, time, channels] argument."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        if _device_of(t, name) != device:
+            raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    sb, st, inner = t.stride()
+    batch, time, channels = shape
+    if inner != 1 and channels > 1:
+        raise ValueError("%s: the channels of a step must be consecutive" % name)
+    if batch <= 1:
+        sb = channels
+    if time <= 1:
+        st = channels
+    if written and (st < channels or sb < channels):
+        raise ValueError("%s: its steps overlap" % name)
+    return t.data_ptr(), sb, st
+
+
+def new_recurrence_states(batch: int, time: int, channels: int, device="cuda") -> torch.Tensor:
+    """The states of recurrence_forward that its backward pass starts from:
+    one for every 32 steps, an eighth of a byte for each element."""
+    return torch.empty((batch, -(-int(time) // CHUNK), channels), dtype=torch.float32, device=device)
+
+
+def _recurrence(lead, name: str, x, gate, states, lengths):
+    """The fields both passes share, and the shape; lead is the tensor the others go by."""
+    dev = _device_of(lead, name)
+    if lead.dim() != 3:
+        raise ValueError("%s must have three dimensions" % name)
+    dt = lead.dtype
+    d = _DTYPES.get(dt)
+    if d is None:
+        raise TypeError("%s has dtype %s, expected float32, float16 or bfloat16" % (name, dt))
+    shape = lead.shape
+    batch, time, channels = shape
+    pl, lb = None, 8
+    if lengths is not None:
+        pl, _, lb = _ids(lengths, "lengths", dev, (batch,))
+    ps = None
+    if states is not None:
+        ps = _contiguous(states, "states", dev, (batch, -(-time // CHUNK), channels))
+    return dev, dt, shape, (batch, time, channels, d, lb, pl, *_cube(x, "x", dev, dt, shape),
+                            *_cube(gate, "gate", dev, dt, shape), ps)
+
+
+def _contiguous(t, name: str, device: int, shape):
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        if _device_of(t, name) != device:
+            raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, device))
+    if t.dtype != torch.float32:
+        raise TypeError("%s has dtype %s, expected torch.float32" % (name, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s is not contiguous" % name)
+    return t.data_ptr() if t.numel() else None
+
+
+def _state(t, name: str, device: int, shape, written: bool = False):
+    return (None, 0) if t is None else _matrix(t, name, device, torch.float32, shape, written)
+
+
+def recurrence_forward(x: torch.Tensor, gate: torch.Tensor, y: torch.Tensor, *, h0=None, h_last=None, states=None,
+                       lengths=None) -> None:
+    """y <- the gated linear recurrence over x's steps: with a = sigmoid(gate),
+    h_t = a_t h_{t-1} + (1 - a_t) x_t for every sequence and channel, y = h.
+
+    x, gate and y are [batch, time, channels], float32, float16 or bfloat16,
+    the channels of a step consecutive and sequences and steps any distance
+    apart (time-major tensors transposed, halves of one projection's output);
+    y may be x or gate. h0 and h_last, float32 [batch, channels], are the state
+    before the first and after the last step; h_last may be h0, so that one
+    token a call (time = 1) carries its state along in place. states
+    (new_recurrence_states) receives what the backward pass needs beside x and
+    gate. lengths, int32 or int64 [batch] on the GPU, ends sequences before
+    time: what lies behind is neither read nor written."""
+    dev, dt, shape, a = _recurrence(y, "y", x, gate, states, lengths)
+    state = (shape[0], shape[2])
+    a = _Recurrence(*a, *_cube(y, "y", dev, dt, shape, True), *_state(h0, "h0", dev, state),
+                    *_state(h_last, "h_last", dev, state, True))
+    n = _workspace_bytes(lib().msamp_recurrence_forward_workspace(a))
+    ws = _workspace(n, dev)
+    _run(dev, lib().msamp_recurrence_forward, a, None if ws is None else ws.data_ptr(), n)
+
+
+def recurrence_backward(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, states: torch.Tensor,
+                        dx: torch.Tensor, dgate: torch.Tensor, *, dh_last=None, dh0=None, lengths=None) -> None:
+    """Gradients of recurrence_forward from dy, its x and gate and the states
+    it saved. dh_last is the gradient of h_last (None: 0); dh0, if given,
+    receives h0's, and may be dh_last. dx and dgate may each be one of dy, x
+    and gate. y is not needed: h is formed again from the states."""
+    if states is None:
+        raise TypeError("states is not a tensor")
+    dev, dt, shape, a = _recurrence(dy, "dy", x, gate, states, lengths)
+    state = (shape[0], shape[2])
+    a = _Recurrence(*a, None, 0, 0, None, 0, None, 0, *_cube(dy, "dy", dev, dt, shape),
+                    *_cube(dx, "dx", dev, dt, shape, True), *_cube(dgate, "dgate", dev, dt, shape, True),
+                    *_state(dh_last, "dh_last", dev, state), *_state(dh0, "dh0", dev, state, True))
+    n = _workspace_bytes(lib().msamp_recurrence_backward_workspace(a))
+    ws = _workspace(n, dev)
+    _run(dev, lib().msamp_recurrence_backward, a, None if ws is None else ws.data_ptr(), n)
+
+
+def _rows_f32(t, name: str, device: int, n: int):
+    return None if t is None else _vector(t, name, device, torch.float32, n)
+
+
+def _vocab_loss(logits, ids, temperature, loss, stats, dlogits, dloss, policy: bool):
+    """(device, the fields both losses share, rows)."""
+    dev, d, shape = _leading(logits, "logits")
+    rows, vocab = shape
+    p, ld = _matrix(logits, "logits", dev, logits.dtype, shape)
+    if policy:
+        pi, ldi, ib = _ids(ids, "actions", dev, (rows,))
+    else:
+        if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+            raise ValueError("teacher_ids must be a tensor of two dimensions")
+        pi, ldi, ib = _ids(ids, "teacher_ids", dev, (rows, ids.shape[1]))
+    ps = None if stats is None else _contiguous(stats, "stats", dev, (rows, 2))
+    pg, ldg = (None, 0) if dlogits is None else _matrix(dlogits, "dlogits", dev, logits.dtype, shape, True)
+    if dlogits is None and dloss is not None:
+        raise ValueError("dloss is the gradient that dlogits is formed from: dlogits is not given")
+    return dev, rows, (rows, vocab, d, ib, p, ld, pi, ldi, temperature, _rows_f32(loss, "loss", dev, rows), ps,
+                       _rows_f32(dloss, "dloss", dev, rows), pg, ldg)
+
+
+def _teacher(t, device: int, ids):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("teacher_logits is not a tensor")
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError("teacher_logits has dtype %s, expected float32, float16 or bfloat16" % t.dtype)
+    p, ld = _matrix(t, "teacher_logits", device, t.dtype, ids.shape)
+    return ids.shape[1], p, ld, d
+
+
+def _loss_forward(dev: int, workspace, entry, a: _VocabLoss) -> None:
+    n = _workspace_bytes(workspace(a))
+    ws = _workspace(n, dev)
+    _run(dev, entry, a, None if ws is None else ws.data_ptr(), n)
+
+
+def distill_loss_forward(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                         loss: torch.Tensor, *, temperature: float = 1.0, stats=None, dlogits=None,
+                         dloss=None) -> None:
+    """loss[r] <- temperature^2 KL(p || q), with p the softmax of the teacher's
+    listed logits of the row and q that of all of the student's, both divided
+    by temperature. With one listed class and temperature 1 that is the
+    cross-entropy.
+
+    logits [rows, vocab] float32, float16 or bfloat16; teacher_ids int32 or
+    int64 [rows, top] and teacher_logits [rows, top] of any of the three
+    types, top <= 1024; an id outside the vocabulary (-1) is no entry, and a
+    row without entries has loss and gradient 0. loss is float32 [rows].
+
+    dlogits, if given, receives the gradient in the same pass over the logits,
+    from dloss (float32 [rows], the gradient of each row's loss; None: ones);
+    it may be logits. Or stats, float32 [rows, 2], keeps what
+    distill_loss_backward takes."""
+    if loss is None:
+        raise TypeError("loss is not a tensor")
+    dev, _, a = _vocab_loss(logits, teacher_ids, temperature, loss, stats, dlogits, dloss, False)
+    a = _VocabLoss(*a, *_teacher(teacher_logits, dev, teacher_ids))
+    _loss_forward(dev, lib().msamp_distill_forward_workspace, lib().msamp_distill_forward, a)
+
+
+def distill_loss_backward(dloss, logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                          stats: torch.Tensor, dlogits: torch.Tensor, *, temperature: float = 1.0) -> None:
+    """dlogits <- the gradient of distill_loss_forward from dloss (None: ones)
+    and the stats it kept. dlogits may be logits."""
+    if stats is None or dlogits is None:
+        raise TypeError("stats and dlogits must be tensors")
+    dev, _, a = _vocab_loss(logits, teacher_ids, temperature, None, stats, dlogits, dloss, False)
+    a = _VocabLoss(*a, *_teacher(teacher_logits, dev, teacher_ids))
+    _run(dev, lib().msamp_distill_backward, a)
+
+
+def _policy(dev: int, rows: int, old_logp, ref_logp, advantages, logp, clip_low, clip_high, kl):
+    return (0, None, 0, 0, _vector(old_logp, "old_logp", dev, torch.float32, rows),
+            _rows_f32(ref_logp, "ref_logp", dev, rows), _vector(advantages, "advantages", dev, torch.float32, rows),
+            _rows_f32(logp, "logp", dev, rows), clip_low, clip_high, kl)
+
+
+def policy_loss_forward(logits: torch.Tensor, actions: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
+                        loss: torch.Tensor, *, logp=None, ref_logp=None, kl: float = 0.0, clip_low: float = 0.2,
+                        clip_high: float = 0.2, temperature: float = 1.0, stats=None, dlogits=None,
+                        dloss=None) -> None:
+    """loss[r] <- -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+    + kl (e^d - d - 1), with lp = log softmax(logits / temperature)[action],
+    r = e^(lp - old_logp), A = advantages[r] and d = ref_logp - lp.
+
+    logits [rows, vocab] float32, float16 or bfloat16; actions int32 or int64
+    [rows], one outside the vocabulary (-1) is a row without loss and gradient
+    (a prompt's); old_logp, ref_logp (None with kl = 0), advantages, loss and
+    logp, which receives lp, float32 [rows].
+
+    dlogits, dloss and stats as in distill_loss_forward."""
+    if loss is None:
+        raise TypeError("loss is not a tensor")
+    dev, rows, a = _vocab_loss(logits, actions, temperature, loss, stats, dlogits, dloss, True)
+    a = _VocabLoss(*a, *_policy(dev, rows, old_logp, ref_logp, advantages, logp, clip_low, clip_high, kl))
+    _loss_forward(dev, lib().msamp_policy_forward_workspace, lib().msamp_policy_forward, a)
+
+
+def policy_loss_backward(dloss, logits: torch.Tensor, actions: torch.Tensor, old_logp: torch.Tensor,
+                         advantages: torch.Tensor, stats: torch.Tensor, dlogits: torch.Tensor, *, ref_logp=None,
+                         kl: float = 0.0, clip_low: float = 0.2, clip_high: float = 0.2,
+                         temperature: float = 1.0) -> None:
+    """dlogits <- the gradient of policy_loss_forward from dloss (None: ones)
+    and the stats it kept. dlogits may be logits."""
+    if stats is None or dlogits is None:
+        raise TypeError("stats and dlogits must be tensors")
+    dev, rows, a = _vocab_loss(logits, actions, temperature, None, stats, dlogits, dloss, True)
+    a = _VocabLoss(*a, *_policy(dev, rows, old_logp, ref_logp, advantages, None, clip_low, clip_high, kl))
+    _run(dev, lib().msamp_policy_backward, a)
 
 
 # ----------------------------------------------------------- state helpers ---

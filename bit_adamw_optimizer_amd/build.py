@@ -10,9 +10,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libmsamp.so")
-SOURCES = [os.path.join(CSRC, n) for n in ("kernels.hip", "abi.hip", "norm.hip", "ffn.hip", "train_abi.hip")]
+SOURCES = [os.path.join(CSRC, n) for n in ("kernels.hip", "abi.hip", "norm.hip", "ffn.hip", "train_abi.hip",
+                                           "embedding.hip", "recurrence.hip", "loss.hip", "model_abi.hip")]
 HEADERS = [os.path.join(CSRC, n) for n in ("codec.hpp", "device.hpp", "kernels.hpp", "host.hpp", "train.hpp",
-                                           "checkpoint.hpp", "ffn.hpp")] + [os.path.join(INCLUDE, "msamp.h")]
+                                           "checkpoint.hpp", "ffn.hpp", "lanes.hpp", "args.hpp", "model.hpp")] + [os.path.join(INCLUDE, "msamp.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1092,6 +1092,13 @@ const char* msamp_kernel_name(msamp_kernel_kind kind) {
     case MSAMP_KERNEL_FFN_GRADIENTS: return "ffn_gradients";
     case MSAMP_KERNEL_FFN_LAYOUT: return "ffn_layout";
     case MSAMP_KERNEL_FFN_REDUCE: return "ffn_reduce";
+    case MSAMP_KERNEL_EMBEDDING_FORWARD: return "embedding_forward";
+    case MSAMP_KERNEL_EMBEDDING_SORT: return "embedding_sort";
+    case MSAMP_KERNEL_EMBEDDING_BACKWARD: return "embedding_backward";
+    case MSAMP_KERNEL_RECURRENCE_FORWARD: return "recurrence_forward";
+    case MSAMP_KERNEL_RECURRENCE_BACKWARD: return "recurrence_backward";
+    case MSAMP_KERNEL_LOSS_FORWARD: return "loss_forward";
+    case MSAMP_KERNEL_LOSS_BACKWARD: return "loss_backward";
     default: return "";
   }
 }

@@ -7,109 +7,13 @@
 #include <cmath>
 #include <string>
 
+#include "args.hpp"
 #include "ffn.hpp"
 #include "host.hpp"
 #include "train.hpp"
 
 namespace msamp {
 namespace {
-
-// Elements of a matrix's address range: keeps every offset, in bytes too,
-// within 63 bits.
-constexpr int64_t kMaxSpan = (int64_t)1 << 58;
-constexpr int64_t kMaxCols = INT32_MAX;
-
-msamp_status invalid(const std::string& msg) { return fail(MSAMP_E_INVALID_ARG, msg); }
-
-int64_t elem_size(int dtype) { return dtype == MSAMP_F32 ? 4 : 2; }
-
-msamp_status check_dtype(int dtype, const char* role) {
-  if (dtype != MSAMP_F32 && dtype != MSAMP_F16 && dtype != MSAMP_BF16)
-    return invalid(std::string("unknown ") + role);
-  return MSAMP_OK;
-}
-
-msamp_status check_shape(int64_t rows, int64_t cols) {
-  if (rows < 0 || cols < 0) return invalid("a size is negative");
-  if (cols > kMaxCols) return invalid("cols exceeds 2^31 - 1");
-  if (rows > kMaxSpan) return invalid("rows exceeds 2^58");
-  return MSAMP_OK;
-}
-
-// A matrix of rows x cols elements of 'size' bytes; not NULL unless empty.
-msamp_status check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size, bool written,
-                          const char* role) {
-  if (rows == 0 || cols == 0) return MSAMP_OK;
-  if (p == nullptr) return invalid(std::string(role) + " is NULL");
-  if (((uintptr_t)p & (uintptr_t)(size - 1)) != 0)
-    return fail(MSAMP_E_MISALIGNED, std::string(role) + " is not aligned to its elements");
-  if (ld < 0 || (written && rows > 1 && ld < cols))
-    return invalid(std::string(role) + ": the distance between rows is " + (ld < 0 ? "negative" : "less than a row"));
-  if (ld > 0 && rows - 1 > (kMaxSpan - cols) / ld) return invalid(std::string(role) + " spans too much memory");
-  return MSAMP_OK;
-}
-
-msamp_status check_vector(const void* p, int64_t n, int64_t size, const char* role) {
-  return check_matrix(p, 1, n, n, size, true, role);
-}
-
-msamp_status check_checkpoint(const msamp_checkpoint* c, int64_t rows, int64_t cols, bool written, const char* role) {
-  if (c == nullptr) return invalid(std::string(role) + " is NULL");
-  if (c->fmt != MSAMP_FP8_E4M3 && c->fmt != MSAMP_FP8_E5M2)
-    return invalid(std::string(role) + ": unknown FP8 format");
-  MSAMP_TRY(check_matrix(c->codes, rows, cols, c->ld, 1, written, (std::string(role) + ".codes").c_str()));
-  const int64_t groups = (cols + MSAMP_CHECKPOINT_GROUP - 1) / MSAMP_CHECKPOINT_GROUP;
-  return check_matrix(c->scales, rows, groups, c->ld_scales, 1, written, (std::string(role) + ".scales").c_str());
-}
-
-// The memory of a call's arguments. What is written may share none with
-// anything else (the kernels write some rows while they still read others),
-// but a norm's output may be its input ('in_place': equal matrices, whose rows
-// are read whole before they are written).
-class Regions {
- public:
-  void add(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size, bool written, const char* role,
-           bool in_place = false) {
-    if (p == nullptr || rows == 0 || cols == 0) return;
-    r_[n_++] = {(uintptr_t)p, (uintptr_t)p + (uintptr_t)(((rows - 1) * ld + cols) * size), cols * size,
-                rows == 1 ? cols * size : ld * size, rows == 1, written, in_place, role};
-  }
-  void vector(const void* p, int64_t n, int64_t size, bool written, const char* role) {
-    add(p, 1, n, n, size, written, role);
-  }
-  void checkpoint(const msamp_checkpoint* c, int64_t rows, int64_t cols, bool written, const char* role) {
-    if (c == nullptr) return;
-    add(c->codes, rows, cols, c->ld, 1, written, role);
-    add(c->scales, rows, (cols + MSAMP_CHECKPOINT_GROUP - 1) / MSAMP_CHECKPOINT_GROUP, c->ld_scales, 1, written, role);
-  }
-  msamp_status check() const {
-    for (int i = 1; i < n_; ++i)
-      for (int j = 0; j < i; ++j)
-        if ((r_[i].written || r_[j].written) && overlap(r_[i], r_[j]))
-          return invalid(std::string(r_[j].role) + " and " + r_[i].role + " overlap");
-    return MSAMP_OK;
-  }
-
- private:
-  struct Region {
-    uintptr_t lo, hi;
-    int64_t row, ld;
-    bool one, written, in_place;
-    const char* role;
-  };
-  static bool overlap(const Region& a, const Region& b) {
-    if (a.hi <= b.lo || b.hi <= a.lo) return false;
-    if (a.in_place && b.in_place && a.lo == b.lo && a.row == b.row && (a.ld == b.ld || a.one)) return false;
-    // rows side by side at the same distance (columns of one buffer)
-    const int64_t ld = a.one ? b.ld : a.ld;
-    if ((a.one && b.one) || (!a.one && !b.one && a.ld != b.ld) || ld == 0) return true;
-    const int64_t d = b.lo >= a.lo ? (int64_t)((b.lo - a.lo) % (uintptr_t)ld)
-                                   : (ld - (int64_t)((a.lo - b.lo) % (uintptr_t)ld)) % ld;
-    return d < a.row || d + b.row > ld;
-  }
-  Region r_[16];
-  int n_ = 0;
-};
 
 CkptRef ref(const msamp_checkpoint* c) {
   CkptRef r;
@@ -123,15 +27,6 @@ msamp_status check_input(const void* x, int64_t ldx, const msamp_checkpoint* ck,
   if (ck == nullptr) return check_matrix(x, rows, cols, ldx, elem_size(dtype), false, "x");
   if (x != nullptr) return invalid("both x and x_ckpt are set");
   return check_checkpoint(ck, rows, cols, false, "x_ckpt");
-}
-
-msamp_status check_workspace(const void* ws, int64_t bytes, int64_t need) {
-  if (need == 0) return MSAMP_OK;
-  if (ws == nullptr) return invalid("workspace is NULL");
-  if (((uintptr_t)ws & 15u) != 0) return fail(MSAMP_E_MISALIGNED, "workspace is not 16-byte aligned");
-  if (bytes < need)
-    return invalid("workspace has " + std::to_string(bytes) + " bytes, " + std::to_string(need) + " are needed");
-  return MSAMP_OK;
 }
 
 msamp_status check_norm(int64_t rows, int64_t cols, int dtype, const void* weight, const void* bias,
@@ -191,16 +86,6 @@ msamp_status check_ffn_memory(const msamp_gated_ffn* a, bool backward, const voi
   }
   m.vector(workspace, bytes, 1, true, "workspace");
   return m.check();
-}
-
-template <typename F>
-int64_t workspace_of(F&& f) {
-  int64_t bytes = -1;
-  guarded([&]() -> msamp_status {
-    clear_error();
-    return f(&bytes);
-  });
-  return bytes;
 }
 
 }  // namespace

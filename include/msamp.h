@@ -679,6 +679,218 @@ msamp_status msamp_gated_ffn_backward(const msamp_gated_ffn* args, void* workspa
  */
 msamp_status msamp_gated_ffn_plan(const msamp_gated_ffn* args, int backward, int32_t plan[6]);
 
+/* ----------------------------------------------------------------------
+ * Operators at the ends of a model and between its tokens, under the same
+ * rules as the training operators above: rows into the model (embedding), a
+ * mixer over time (gated linear recurrence), and losses over the vocabulary
+ * that start the backward pass.
+ *
+ * Ids (tokens, actions, a teacher's classes) are device integers of id_bytes
+ * 4 (int32) or 8 (int64). One outside [0, vocab), -1 by custom, names
+ * nothing: it is never used as an address. Rows are at most 2^31 - 1.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * msamp_embedding_forward -- y [rows, cols]: y[r] = scale * weight[ids[r]],
+ * one binary32 product rounded once to dtype; a row of zeros for an id outside
+ * [0, vocab) (padding).
+ *   ids        device [rows]
+ *   weight     device [vocab, cols], dtype
+ *   y          device, dtype, out
+ *   scale      finite in binary32
+ */
+#define MSAMP_EMBEDDING_MAX_VOCAB (1 << 30)
+#define MSAMP_EMBEDDING_MAX_COLS (1 << 22)
+msamp_status msamp_embedding_forward(int64_t rows, int64_t vocab, int64_t cols, const void* ids, int id_bytes,
+                                     const void* weight, int64_t ldw, msamp_dtype dtype, void* y, int64_t ldy,
+                                     double scale, void* stream);
+
+/*
+ * msamp_embedding_backward -- dweight [vocab, cols], binary32 (what msamp_amax
+ * takes): dweight[v] = scale * (sum of dy[r] over the rows r with ids[r] = v,
+ * in binary32, in the rows' order); zeros where there is no such row. With
+ * accumulate the products are added to what is there (the gradient of an
+ * output projection tied to the embedding), and a dweight row without rows of
+ * its id is neither read nor written.
+ *   dy         device [rows, cols], dtype
+ *   ids        device [rows]
+ *   workspace  msamp_embedding_backward_workspace bytes: the rows sorted by
+ *              id, and partial sums of ids with many rows
+ */
+int64_t msamp_embedding_backward_workspace(int64_t rows, int64_t vocab, int64_t cols);
+msamp_status msamp_embedding_backward(int64_t rows, int64_t vocab, int64_t cols, const void* dy, int64_t lddy,
+                                      msamp_dtype dtype, const void* ids, int id_bytes, float* dweight,
+                                      int64_t ld_dweight, double scale, int accumulate, void* workspace,
+                                      int64_t workspace_bytes, void* stream);
+
+/*
+ * Arguments of the gated linear recurrence (host struct, read during the
+ * call): for every sequence and channel, with a_t = 1 / (1 + e^-gate_t),
+ *   forward:   h_t = a_t h_{t-1} + (1 - a_t) x_t,  y_t = h_t
+ *   backward:  from dy: l_t = dy_t + a_{t+1} l_{t+1},
+ *              dx_t = (1 - a_t) l_t,
+ *              dgate_t = l_t (h_{t-1} - x_t) a_t (1 - a_t),
+ *              dh0 = a_0 l_0
+ * where h before the first step is h0 and dh_last takes part as the gradient
+ * of h after the last one. Gates, states and both recurrences are binary32
+ * (1 - a_t is formed as 1 / (1 + e^gate_t), so that it keeps its digits where
+ * the gate is nearly open); y, dx and dgate are rounded once to dtype. Long
+ * sequences are cut into spans that are worked on at the same time and joined,
+ * so the order of the operations depends on the sizes, and on nothing else.
+ *
+ * x, gate, y, dy, dx, dgate are [batch, time, channels] of dtype, a channel's
+ * elements of one step consecutive, *_batch and *_time the distances between
+ * sequences and between steps in elements (any order of the two; x and gate
+ * may be column ranges of one projection's output, and a step that is read
+ * may be repeated by a distance of 0). y may be x or gate, dx and dgate may
+ * each be one of dy, x and gate (the same tensor).
+ *   lengths    NULL, or device [batch] of length_bytes 4 or 8: the steps of
+ *              each sequence, taken as 0 below 0 and as time above it. What
+ *              lies behind them is neither read nor written.
+ *   states     h before the steps 0, 32, 64, ... of every sequence,
+ *              [batch, ceil(time / 32), channels] in binary32 without gaps.
+ *              Forward: out, or NULL. Backward: as the forward pass wrote
+ *              them; nothing else is kept (x and gate are read again).
+ *   h0         [batch, channels] binary32, rows ld_h0 apart; NULL: zeros
+ *   h_last     forward: out, h after the last step (h0 of a sequence of no
+ *              steps), or NULL. It may be h0 (the same matrix): a step of a
+ *              single token with its state in place is time = 1.
+ *   dh_last    backward: [batch, channels] binary32; NULL: zeros
+ *   dh0        backward: out (dh_last of a sequence of no steps), or NULL; it
+ *              may be dh_last
+ * Every size is at most 2^31 - 1, batch * ceil(channels / 64) at most 2^22.
+ * The backward fields are not read by the forward pass; h0 and h_last are not
+ * read by the backward pass.
+ */
+#define MSAMP_RECURRENCE_CHUNK 32
+typedef struct {
+  int64_t batch, time, channels;
+  msamp_dtype dtype;
+  int length_bytes;
+  const void* lengths;
+  const void* x;
+  int64_t x_batch, x_time;
+  const void* gate;
+  int64_t gate_batch, gate_time;
+  float* states;
+  void* y;
+  int64_t y_batch, y_time;
+  const float* h0;
+  int64_t ld_h0;
+  float* h_last;
+  int64_t ld_h_last;
+  const void* dy;
+  int64_t dy_batch, dy_time;
+  void* dx;
+  int64_t dx_batch, dx_time;
+  void* dgate;
+  int64_t dgate_batch, dgate_time;
+  const float* dh_last;
+  int64_t ld_dh_last;
+  float* dh0;
+  int64_t ld_dh0;
+} msamp_recurrence;
+
+/* Bytes of workspace of a call with these arguments; -1 with an error set
+ * when the arguments are not valid. */
+int64_t msamp_recurrence_forward_workspace(const msamp_recurrence* args);
+int64_t msamp_recurrence_backward_workspace(const msamp_recurrence* args);
+msamp_status msamp_recurrence_forward(const msamp_recurrence* args, void* workspace, int64_t workspace_bytes,
+                                      void* stream);
+msamp_status msamp_recurrence_backward(const msamp_recurrence* args, void* workspace, int64_t workspace_bytes,
+                                       void* stream);
+
+/*
+ * Arguments of the losses over a vocabulary (host struct, read during the
+ * call). logits z [rows, vocab] of dtype; with tau = temperature and
+ * q = softmax(z / tau) of a row:
+ *
+ *   distillation from a teacher's top logits (msamp_distill_*): ids and
+ *   teacher [rows, top]; p = softmax(teacher / tau) over a row's entries with
+ *   an id in [0, vocab):
+ *     loss = tau^2 * sum_j p_j (log p_j - log q[id_j])
+ *     dlogits[v] = dloss * tau * (q[v] - sum over {j: id_j = v} of p_j)
+ *   An id may occur more than once. An entry of -Inf has p = 0. With top = 1
+ *   and tau = 1 this is the cross-entropy against ids. top <= 1024.
+ *
+ *   clipped policy loss with a KL term (msamp_policy_*): the action's id,
+ *   old_logp, ref_logp and advantage A of each row; lp = log q[id],
+ *   r = e^(lp - old_logp), d = ref_logp - lp:
+ *     loss = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *            + kl (e^d - d - 1)
+ *     dlogits[v] = dloss / tau * g * ([v = id] - q[v]),
+ *     g = kl (1 - e^d) - (0 where r is beyond the bound that the minimum
+ *         takes: A > 0 and r > 1 + clip_high, or A < 0 and r < 1 - clip_low;
+ *         else r A)
+ *   A row with A = 0 has no first term. lp and the clip's comparison are
+ *   formed in binary64 from binary32 sums, so that a ratio next to a bound
+ *   falls on its side.
+ *
+ * Everything else is binary32; loss and logp are binary32, dlogits is rounded
+ * once to dtype (with MSAMP_F16, values of 2^-25 or less become 0: dloss has
+ * to carry a loss scale that keeps them above).
+ *
+ * A row is left out (loss, logp 0, dlogits 0) when its teacher has no entry of
+ * an id in [0, vocab) and above -Inf, when its action is outside [0, vocab),
+ * or when every logit of it is -Inf. Of rows left out by their ids or action
+ * the logits are not read, and their stats are zeros. Single logits of -Inf
+ * (a masked vocabulary) have q = 0. NaN, +Inf and teacher entries of +Inf make
+ * their row's results NaN.
+ *   stats      [rows][2] without gaps: the largest logit of the row and the
+ *              sum of exp((z - largest) / tau); log q[v] =
+ *              (z[v] - stats[0]) / tau - log(stats[1]). Forward: out, or
+ *              NULL; backward: as the forward pass wrote them
+ *   loss       forward: out [rows]
+ *   logp       policy, forward: out [rows], lp; or NULL
+ *   dlogits    forward: NULL, or out, so that loss and gradient take one pass
+ *              over the logits; backward: out. It may be logits (the same
+ *              matrix)
+ *   dloss      device float[rows], the gradient of each row's loss; NULL: 1.
+ *              Not read without dlogits
+ * vocab, rows <= 2^31 - 1. Fields of the other loss are not read.
+ */
+#define MSAMP_DISTILL_MAX_TOP 1024
+typedef struct {
+  int64_t rows, vocab;
+  msamp_dtype dtype;
+  int id_bytes;
+  const void* logits;
+  int64_t ld_logits;
+  const void* ids; /* distillation: [rows, top], rows ld_ids apart; policy: the actions [rows] */
+  int64_t ld_ids;
+  double temperature; /* > 0; it and its inverse finite in binary32 */
+  float* loss;
+  float* stats;
+  const float* dloss;
+  void* dlogits;
+  int64_t ld_dlogits;
+  /* distillation */
+  int64_t top;
+  const void* teacher; /* of teacher_dtype, any of the three */
+  int64_t ld_teacher;
+  msamp_dtype teacher_dtype;
+  /* policy loss */
+  const float* old_logp;
+  const float* ref_logp; /* may be NULL when kl is 0 */
+  const float* advantages;
+  float* logp;
+  double clip_low;  /* in [0, 1] */
+  double clip_high; /* >= 0, Inf: no upper bound */
+  double kl;        /* finite in binary32 */
+} msamp_vocab_loss;
+
+/* Bytes of workspace of a call with these arguments (either loss, forward or
+ * backward); -1 with an error set when the arguments are not valid. */
+int64_t msamp_distill_forward_workspace(const msamp_vocab_loss* args);
+int64_t msamp_policy_forward_workspace(const msamp_vocab_loss* args);
+msamp_status msamp_distill_forward(const msamp_vocab_loss* args, void* workspace, int64_t workspace_bytes,
+                                   void* stream);
+msamp_status msamp_policy_forward(const msamp_vocab_loss* args, void* workspace, int64_t workspace_bytes,
+                                  void* stream);
+/* The gradient alone, from the forward pass's stats. */
+msamp_status msamp_distill_backward(const msamp_vocab_loss* args, void* stream);
+msamp_status msamp_policy_backward(const msamp_vocab_loss* args, void* stream);
+
 /* Frees every cached device table of the library (all devices) that is not
  * pinned by a graph capture, after waiting for the devices to finish. Safe to
  * call at any time from one thread while no other library call runs. */
@@ -791,7 +1003,14 @@ typedef enum {
   MSAMP_KERNEL_FFN_GRADIENTS = 22, /* dx, dw_gate and dw_up */
   MSAMP_KERNEL_FFN_LAYOUT = 23,    /* operands laid out for the matrix kernels */
   MSAMP_KERNEL_FFN_REDUCE = 24,    /* partial sums of a split product */
-  MSAMP_KERNEL_COUNT = 25
+  MSAMP_KERNEL_EMBEDDING_FORWARD = 25,    /* msamp_embedding_forward */
+  MSAMP_KERNEL_EMBEDDING_SORT = 26,       /* rows sorted by id */
+  MSAMP_KERNEL_EMBEDDING_BACKWARD = 27,   /* the embedding's gradient */
+  MSAMP_KERNEL_RECURRENCE_FORWARD = 28,   /* msamp_recurrence_forward */
+  MSAMP_KERNEL_RECURRENCE_BACKWARD = 29,  /* msamp_recurrence_backward */
+  MSAMP_KERNEL_LOSS_FORWARD = 30,         /* msamp_distill_forward, msamp_policy_forward */
+  MSAMP_KERNEL_LOSS_BACKWARD = 31,        /* msamp_distill_backward, msamp_policy_backward */
+  MSAMP_KERNEL_COUNT = 32
 } msamp_kernel_kind;
 
 /* on != 0 starts recording (and discards earlier records; the events for
