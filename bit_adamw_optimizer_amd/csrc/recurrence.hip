@@ -33,6 +33,19 @@ struct Pair<float> {
     if (n >= 2) *(GLOBAL u32x2_any*)p = u32x2{__float_as_uint(v.x), __float_as_uint(v.y)};
     else *(GLOBAL float*)p = v.x;
   }
+  static __device__ __forceinline__ raw load(__amdgpu_buffer_rsrc_t b, uint32_t at) {
+    return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(b, at, 0, 0));
+  }
+  static __device__ __forceinline__ raw load_each(__amdgpu_buffer_rsrc_t b, uint32_t at, uint32_t second) {
+    return raw{__builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0), __builtin_amdgcn_raw_buffer_load_b32(b, second, 0, 0)};
+  }
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, uint32_t at, float2 v) {
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v.x), __float_as_uint(v.y)}, b, at, 0, 0);
+  }
+  static __device__ __forceinline__ void store_each(__amdgpu_buffer_rsrc_t b, uint32_t at, uint32_t second, float2 v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v.x), b, at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v.y), b, second, 0, 0);
+  }
 };
 typedef uint32_t u32_any __attribute__((aligned(1)));
 template <typename T>
@@ -46,10 +59,28 @@ struct Pair {
     return make_float2(to_f32(__builtin_bit_cast(T, (uint16_t)(r & 0xFFFFu))),
                        to_f32(__builtin_bit_cast(T, (uint16_t)(r >> 16))));
   }
+  static __device__ __forceinline__ raw packed(float2 v) {
+    return (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(v.x)) |
+           (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(v.y)) << 16;
+  }
   static __device__ __forceinline__ void store(T* p, int n, float2 v) {
-    const uint32_t lo = __builtin_bit_cast(uint16_t, from_f32<T>(v.x));
-    if (n >= 2) *(GLOBAL u32_any*)p = lo | (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(v.y)) << 16;
-    else *(GLOBAL uint16_t*)p = (uint16_t)lo;
+    if (n >= 2) *(GLOBAL u32_any*)p = packed(v);
+    else *(GLOBAL T*)p = from_f32<T>(v.x);
+  }
+  static __device__ __forceinline__ raw load(__amdgpu_buffer_rsrc_t b, uint32_t at) {
+    return __builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0);
+  }
+  static __device__ __forceinline__ raw load_each(__amdgpu_buffer_rsrc_t b, uint32_t at, uint32_t second) {
+    return (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, at, 0, 0) |
+           (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, second, 0, 0) << 16;
+  }
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, uint32_t at, float2 v) {
+    __builtin_amdgcn_raw_buffer_store_b32(packed(v), b, at, 0, 0);
+  }
+  static __device__ __forceinline__ void store_each(__amdgpu_buffer_rsrc_t b, uint32_t at, uint32_t second, float2 v) {
+    const uint32_t q = packed(v);
+    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(q & 0xFFFFu), b, at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(q >> 16), b, second, 0, 0);
   }
 };
 
@@ -149,32 +180,446 @@ __global__ __launch_bounds__(kBlock) void k_backward_lane(msamp_recurrence a, in
   if (a.dh0 != nullptr) Pair<float>::store(a.dh0 + b * a.ld_dh0 + c, n, m);
 }
 
+// ------------------------------------------- tiles: waves side by side in time ---
+
+// A workgroup takes a block of 2 * LANES channels through its span of the
+// sequence, 32 * WAVES steps at a time: each wave has a chunk of 32 steps,
+// each of its 64 / LANES groups of lanes R consecutive steps of it in
+// registers. A run of steps maps the state before it to the state behind it
+// by h -> A h + S, so the groups form (A, S) of their steps, join them over
+// the wave's lanes and (through LDS, one barrier) over the waves, and only
+// then go through their steps with the state they start from. The next tile's
+// loads are under way meanwhile.
+//
+// Where batch and channels alone give too few workgroups, sequences are cut
+// into spans: a first launch forms each span's (A, S), and each workgroup of
+// the second joins those before its own.
+struct Spans {
+  int64_t blocks;  // of channels
+  int32_t steps;   // of a span, a multiple of the tile's
+  int32_t count;
+  float4* joined;  // [batch][count][pairs]: (A, S) of each span
+  int64_t pairs;
+};
+
 template <typename T>
-hipError_t forward(const msamp_recurrence& a, void*, hipStream_t s) {
-  const int64_t pairs = (a.channels + 1) / 2;
-  k_forward_lane<T><<<(unsigned)((a.batch * pairs + kBlock - 1) / kBlock), kBlock, 0, s>>>(a, pairs);
+constexpr int lanes_of() {
+  return sizeof(T) == 2 ? 32 : 16;  // 128 bytes of a step
+}
+
+struct Affine {  // v -> a v + s
+  float2 a, s;
+};
+__device__ __forceinline__ float2 apply(const Affine& f, float2 v) { return fma2(f.a, v, f.s); }
+// f after g
+__device__ __forceinline__ Affine after(const Affine& f, const Affine& g) { return {mul2(f.a, g.a), fma2(f.a, g.s, f.s)}; }
+
+__device__ __forceinline__ float2 shuffle2(float2 v, int lane) {
+  return make_float2(__shfl(v.x, lane, 64), __shfl(v.y, lane, 64));
+}
+__device__ __forceinline__ Affine shuffle(const Affine& f, int lane) {
+  return {shuffle2(f.a, lane), shuffle2(f.s, lane)};
+}
+
+// What the groups before (FORWARD: earlier, otherwise later in time) this
+// lane's map a state to, in *before; the whole wave's map in the last group
+// (FORWARD: the highest) of *all.
+template <int LANES, bool FORWARD>
+__device__ __forceinline__ void join_groups(int lane, const Affine& mine, Affine* before, Affine* all) {
+  *all = mine;
+  const Affine same = {make_float2(1.0f, 1.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+  for (int off = LANES; off < 64; off <<= 1) {
+    const int from = FORWARD ? lane - off : lane + off;
+    const Affine f = shuffle(*all, from & 63);
+    if (from >= 0 && from < 64) *all = after(*all, f);
+  }
+  const int from = FORWARD ? lane - LANES : lane + LANES;
+  const Affine f = shuffle(*all, from & 63);
+  *before = from >= 0 && from < 64 ? f : same;
+}
+
+// A tensor's part of one tile, through a buffer whose bounds end behind its
+// last step and channel: what lies outside is read as 0 and not written. The
+// lane's own offset goes through an empty asm once a tile, so that the compiler
+// forms each step's offset with one addition instead of holding all of them in
+// registers over the whole loop.
+constexpr uint32_t kOutside = 0x80000000u;  // beyond every buffer, also with a tile's steps added
+struct Steps {
+  int64_t stride;  // elements
+  uint32_t lane;   // this lane's byte in a tile
+};
+__device__ __forceinline__ Steps steps_of(int64_t stride, int64_t step, int64_t c, int n, int size) {
+  return {stride, n > 0 ? (uint32_t)((step * stride + c) * size) : kOutside};
+}
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const T* p, const Steps& s, int64_t t, int64_t steps,
+                                                            int64_t channels) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)(p + t * s.stride), 0,
+                                           (int)(((steps - 1) * s.stride + channels) * (int64_t)sizeof(T)), 0x00020000);
+}
+__device__ __forceinline__ uint32_t once(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+// odd: the block holds the last of an odd number of channels, whose lane
+// (n = 1) has no second one.
+template <typename T, int R>
+__device__ __forceinline__ void load_steps(__amdgpu_buffer_rsrc_t b, const Steps& s, bool odd, int n,
+                                           typename Pair<T>::raw* v) {
+  const uint32_t at = once(s.lane), row = (uint32_t)(s.stride * (int64_t)sizeof(T));
+  if (odd) {
+    const uint32_t second = n > 1 ? at + (uint32_t)sizeof(T) : kOutside;
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = Pair<T>::load_each(b, at + r * row, second + r * row);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = Pair<T>::load(b, at + r * row);
+  }
+}
+template <typename T, int R>
+__device__ __forceinline__ void store_steps(__amdgpu_buffer_rsrc_t b, const Steps& s, bool odd, int n, const float2* v) {
+  const uint32_t at = once(s.lane), row = (uint32_t)(s.stride * (int64_t)sizeof(T));
+  if (odd) {
+    const uint32_t second = n > 1 ? at + (uint32_t)sizeof(T) : kOutside;
+#pragma unroll
+    for (int r = 0; r < R; ++r) Pair<T>::store_each(b, at + r * row, second + r * row, v[r]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) Pair<T>::store(b, at + r * row, v[r]);
+  }
+}
+
+// Place of a workgroup: block of channels, sequence, span.
+struct Place {
+  int lane, wave, group, n;
+  bool odd;
+  int64_t b, c, span, len, t0, t1;  // steps [t0, t1) of the span
+};
+template <int LANES>
+__device__ __forceinline__ Place place_of(const msamp_recurrence& a, const Spans& sp) {
+  Place p;
+  p.lane = threadIdx.x & 63;
+  p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  p.group = p.lane / LANES;
+  const uint32_t per = (uint32_t)(sp.blocks * sp.count);
+  p.b = blockIdx.x / per;
+  const uint32_t rest = blockIdx.x - (uint32_t)p.b * per;
+  p.span = rest / (uint32_t)sp.blocks;
+  const int64_t block = rest - (uint32_t)p.span * (uint32_t)sp.blocks;
+  p.c = (block * LANES + p.lane % LANES) * 2;
+  const int64_t left = a.channels - p.c;
+  p.n = left <= 0 ? 0 : left == 1 ? 1 : 2;
+  p.odd = (a.channels & 1) && block == sp.blocks - 1;
+  p.len = length_of(a, p.b);
+  p.t0 = p.span * sp.steps;
+  p.t1 = p.t0 + sp.steps < p.len ? p.t0 + sp.steps : p.len;
+  return p;
+}
+
+template <typename T, int WAVES>
+struct Tile {
+  static constexpr int kLanes = lanes_of<T>(), kGroups = 64 / kLanes, kSteps = kChunk / kGroups;
+  static constexpr int kTile = kChunk * WAVES, kThreads = 64 * WAVES;
+  typedef typename Pair<T>::raw raw;
+};
+
+// Maps of the steps' (a, b) in time's order.
+template <int R>
+__device__ __forceinline__ Affine run_of(const float2* av, const float2* bv) {
+  Affine f = {av[0], bv[0]};
+#pragma unroll
+  for (int r = 1; r < R; ++r) f = {mul2(f.a, av[r]), fma2(av[r], f.s, bv[r])};
+  return f;
+}
+
+// PASS 0: y, states and h_last. PASS 1: the spans' maps alone.
+template <typename T, int WAVES, int PASS>
+__global__ __launch_bounds__(64 * WAVES) void k_forward_tile(msamp_recurrence a, Spans sp) {
+  typedef Tile<T, WAVES> K;
+  constexpr int R = K::kSteps;
+  __shared__ float4 wave_map[2][WAVES][K::kLanes];
+  const Place p = place_of<K::kLanes>(a, sp);
+  const T* x = (const T*)a.x + p.b * a.x_batch;
+  const T* g = (const T*)a.gate + p.b * a.gate_batch;
+  T* y = PASS == 0 ? (T*)a.y + p.b * a.y_batch : nullptr;
+  const int mine = p.wave * kChunk + p.group * R;  // this group's steps in a tile
+  const Steps sx = steps_of(a.x_time, mine, p.c, p.n, sizeof(T)), sg = steps_of(a.gate_time, mine, p.c, p.n, sizeof(T));
+  const Steps sy = steps_of(a.y_time, mine, p.c, p.n, sizeof(T));
+  Affine total = {make_float2(1.0f, 1.0f), make_float2(0.0f, 0.0f)};
+  float2 h = make_float2(0.0f, 0.0f);
+  if (PASS == 0 && p.n > 0) {
+    if (a.h0 != nullptr) h = Pair<float>::values(Pair<float>::load(a.h0 + p.b * a.ld_h0 + p.c, p.n));
+    for (int64_t s = 0; s < p.span; ++s) {
+      const float4 f = sp.joined[(p.b * sp.count + s) * sp.pairs + p.c / 2];
+      h = fma2(make_float2(f.x, f.y), h, make_float2(f.z, f.w));
+    }
+  }
+  typename K::raw xr[R], gr[R];
+  auto steps_at = [&](int64_t t) { return t + K::kTile < p.t1 ? (int64_t)K::kTile : p.t1 - t; };
+  auto load = [&](int64_t t) {
+    load_steps<T, R>(buffer_of(g, sg, t, steps_at(t), a.channels), sg, p.odd, p.n, gr);
+    load_steps<T, R>(buffer_of(x, sx, t, steps_at(t), a.channels), sx, p.odd, p.n, xr);
+  };
+  if (p.t0 < p.t1) load(p.t0);
+  int turn = 0;
+  for (int64_t t = p.t0; t < p.t1; t += K::kTile, turn ^= 1) {
+    const int64_t at = t + mine;
+    float2 av[R], bv[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 keep;
+      gate2(Pair<T>::values(gr[r]), &av[r], &keep);
+      bv[r] = mul2(keep, Pair<T>::values(xr[r]));
+    }
+    if (t + K::kTile < p.t1) load(t + K::kTile);
+    if (t + K::kTile > p.t1) {  // steps behind the end keep the state
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (at + r >= p.t1) av[r] = make_float2(1.0f, 1.0f), bv[r] = make_float2(0.0f, 0.0f);
+    }
+    Affine before, all;
+    join_groups<K::kLanes, true>(p.lane, run_of<R>(av, bv), &before, &all);
+    if (WAVES > 1) {
+      if (p.group == K::kGroups - 1)
+        wave_map[turn][p.wave][p.lane % K::kLanes] = make_float4(all.a.x, all.a.y, all.s.x, all.s.y);
+      __syncthreads();
+    } else {
+      all = shuffle(all, 64 - K::kLanes + p.lane % K::kLanes);
+    }
+    float2 start = h;
+    if (PASS == 1) start = total.s;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      if (WAVES > 1) {
+        const float4 f = wave_map[turn][w][p.lane % K::kLanes];
+        all = {make_float2(f.x, f.y), make_float2(f.z, f.w)};
+      }
+      if (PASS == 1) {
+        total = after(all, total);
+      } else {
+        if (w == p.wave) start = h;
+        h = apply(all, h);
+      }
+    }
+    if (PASS == 1) continue;
+    if (a.states != nullptr && p.group == 0 && p.n > 0 && t + p.wave * kChunk < p.t1)
+      Pair<float>::store(a.states + (p.b * ((a.time + kChunk - 1) / kChunk) + t / kChunk + p.wave) * a.channels + p.c, p.n,
+                         start);
+    float2 v = apply(before, start);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      v = fma2(av[r], v, bv[r]);
+      bv[r] = v;
+    }
+    store_steps<T, R>(buffer_of(y, sy, t, steps_at(t), a.channels), sy, p.odd, p.n, bv);
+  }
+  if (p.n == 0 || threadIdx.x >= K::kLanes) return;
+  if (PASS == 1) {
+    sp.joined[(p.b * sp.count + p.span) * sp.pairs + p.c / 2] = make_float4(total.a.x, total.a.y, total.s.x, total.s.y);
+  } else if (a.h_last != nullptr && (p.len == 0 ? p.span == 0 : p.t0 < p.len && p.len <= p.t0 + sp.steps)) {
+    Pair<float>::store(a.h_last + p.b * a.ld_h_last + p.c, p.n, h);
+  }
+}
+
+// Backward in time, m_t = a_t l_t = a_t (dy_t + m_{t+1}); h again from the
+// state before each wave's chunk. PASS 1: the spans' maps of m alone.
+template <typename T, int WAVES, int PASS>
+__global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a, Spans sp) {
+  typedef Tile<T, WAVES> K;
+  constexpr int R = K::kSteps;
+  __shared__ float4 wave_map[2][WAVES][K::kLanes];
+  const Place p = place_of<K::kLanes>(a, sp);
+  const T* x = (const T*)a.x + p.b * a.x_batch;
+  const T* g = (const T*)a.gate + p.b * a.gate_batch;
+  const T* dy = (const T*)a.dy + p.b * a.dy_batch;
+  T* dx = (T*)a.dx + p.b * a.dx_batch;
+  T* dg = (T*)a.dgate + p.b * a.dgate_batch;
+  const float* states = a.states + p.b * ((a.time + kChunk - 1) / kChunk) * a.channels + p.c;
+  const int mine = p.wave * kChunk + p.group * R;
+  const Steps sx = steps_of(a.x_time, mine, p.c, p.n, sizeof(T)), sg = steps_of(a.gate_time, mine, p.c, p.n, sizeof(T));
+  const Steps sd = steps_of(a.dy_time, mine, p.c, p.n, sizeof(T)), ox = steps_of(a.dx_time, mine, p.c, p.n, sizeof(T));
+  const Steps og = steps_of(a.dgate_time, mine, p.c, p.n, sizeof(T));
+  Affine total = {make_float2(1.0f, 1.0f), make_float2(0.0f, 0.0f)};
+  float2 m = make_float2(0.0f, 0.0f);
+  if (PASS == 0 && p.n > 0) {
+    if (a.dh_last != nullptr) m = Pair<float>::values(Pair<float>::load(a.dh_last + p.b * a.ld_dh_last + p.c, p.n));
+    const int64_t last = (p.len + sp.steps - 1) / sp.steps - 1;  // the span with the last step
+    for (int64_t s = last; s > p.span; --s) {
+      const float4 f = sp.joined[(p.b * sp.count + s) * sp.pairs + p.c / 2];
+      m = fma2(make_float2(f.x, f.y), m, make_float2(f.z, f.w));
+    }
+  }
+  typename K::raw xr[R], gr[R], dr[R];
+  float2 state = make_float2(0.0f, 0.0f);
+  auto steps_at = [&](int64_t t) { return t + K::kTile < p.t1 ? (int64_t)K::kTile : p.t1 - t; };
+  auto load = [&](int64_t t) {
+    load_steps<T, R>(buffer_of(g, sg, t, steps_at(t), a.channels), sg, p.odd, p.n, gr);
+    load_steps<T, R>(buffer_of(dy, sd, t, steps_at(t), a.channels), sd, p.odd, p.n, dr);
+    if (PASS == 0) load_steps<T, R>(buffer_of(x, sx, t, steps_at(t), a.channels), sx, p.odd, p.n, xr);
+    if (PASS == 0 && p.n > 0 && t + p.wave * kChunk < p.t1)
+      state = Pair<float>::values(Pair<float>::load(states + (t / kChunk + p.wave) * a.channels, p.n));
+  };
+  const int64_t tiles = p.t0 < p.t1 ? (p.t1 - p.t0 + K::kTile - 1) / K::kTile : 0;
+  if (tiles > 0) load(p.t0 + (tiles - 1) * K::kTile);
+  int turn = 0;
+  for (int64_t i = tiles - 1; i >= 0; --i, turn ^= 1) {
+    const int64_t t = p.t0 + i * K::kTile, at = t + mine;
+    float2 av[R], keep[R], slope[R], d[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      gate2(Pair<T>::values(gr[r]), &av[r], &keep[r]);
+      d[r] = Pair<T>::values(dr[r]);
+      if (PASS == 0) slope[r] = Pair<T>::values(xr[r]);
+    }
+    const float2 first = state;
+    if (i > 0) load(t - K::kTile);
+    if (t + K::kTile > p.t1) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (at + r >= p.t1)
+          av[r] = make_float2(1.0f, 1.0f), keep[r] = d[r] = slope[r] = make_float2(0.0f, 0.0f);
+    }
+    if (PASS == 0) {
+      // h before each step, and dgate's factor (h - x) a (1 - a)
+      Affine f = {av[0], mul2(keep[0], slope[0])}, before, all;
+#pragma unroll
+      for (int r = 1; r < R; ++r) f = {mul2(f.a, av[r]), fma2(av[r], f.s, mul2(keep[r], slope[r]))};
+      join_groups<K::kLanes, true>(p.lane, f, &before, &all);
+      float2 h = apply(before, first);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float2 xv = slope[r];
+        slope[r] = mul2(make_float2(h.x - xv.x, h.y - xv.y), mul2(av[r], keep[r]));
+        h = fma2(av[r], h, mul2(keep[r], xv));
+      }
+    }
+    Affine f = {av[R - 1], mul2(av[R - 1], d[R - 1])}, before, all;
+#pragma unroll
+    for (int r = R - 2; r >= 0; --r)
+      f = {mul2(f.a, av[r]), mul2(av[r], make_float2(d[r].x + f.s.x, d[r].y + f.s.y))};
+    join_groups<K::kLanes, false>(p.lane, f, &before, &all);
+    if (WAVES > 1) {
+      if (p.group == 0) wave_map[turn][p.wave][p.lane] = make_float4(all.a.x, all.a.y, all.s.x, all.s.y);
+      __syncthreads();
+    } else {
+      all = shuffle(all, p.lane % K::kLanes);
+    }
+    float2 start = m;
+#pragma unroll
+    for (int w = WAVES - 1; w >= 0; --w) {
+      if (WAVES > 1) {
+        const float4 q = wave_map[turn][w][p.lane % K::kLanes];
+        all = {make_float2(q.x, q.y), make_float2(q.z, q.w)};
+      }
+      if (PASS == 1) {
+        total = after(all, total);
+      } else {
+        if (w == p.wave) start = m;
+        m = apply(all, m);
+      }
+    }
+    if (PASS == 1) continue;
+    float2 v = apply(before, start);
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+      const float2 l = make_float2(d[r].x + v.x, d[r].y + v.y);
+      keep[r] = mul2(keep[r], l);
+      slope[r] = mul2(slope[r], l);
+      v = mul2(av[r], l);
+    }
+    store_steps<T, R>(buffer_of(dx, ox, t, steps_at(t), a.channels), ox, p.odd, p.n, keep);
+    store_steps<T, R>(buffer_of(dg, og, t, steps_at(t), a.channels), og, p.odd, p.n, slope);
+  }
+  if (p.n == 0 || threadIdx.x >= K::kLanes) return;
+  if (PASS == 1)
+    sp.joined[(p.b * sp.count + p.span) * sp.pairs + p.c / 2] = make_float4(total.a.x, total.a.y, total.s.x, total.s.y);
+  else if (a.dh0 != nullptr && p.span == 0)
+    Pair<float>::store(a.dh0 + p.b * a.ld_dh0 + p.c, p.n, m);
+}
+
+constexpr int64_t kFewSteps = 8;      // up to which a lane goes through them alone
+constexpr int64_t kEnoughGroups = 192;  // workgroups from which sequences are left whole
+constexpr int64_t kMostSpans = 64;
+
+int waves_of(int64_t time) { return time <= kChunk ? 1 : time <= 2 * kChunk ? 2 : time <= 4 * kChunk ? 4 : 8; }
+
+Spans spans_of(const msamp_recurrence& a, void* ws) {
+  Spans s;
+  const int64_t lanes = a.dtype == MSAMP_F32 ? lanes_of<float>() : lanes_of<f16>();
+  s.pairs = (a.channels + 1) / 2;
+  s.blocks = (s.pairs + lanes - 1) / lanes;
+  const int64_t tile = kChunk * waves_of(a.time), tiles = (a.time + tile - 1) / tile;
+  const int64_t groups = s.blocks * a.batch;
+  int64_t count = groups >= kEnoughGroups ? 1 : (256 + groups - 1) / groups;
+  if (count > kMostSpans) count = kMostSpans;
+  if (count > tiles) count = tiles;
+  const int64_t each = (tiles + count - 1) / count;
+  s.count = (int32_t)((tiles + each - 1) / each);
+  s.steps = (int32_t)(each * tile);
+  s.joined = (float4*)ws;
+  return s;
+}
+
+template <typename T, int WAVES, bool BACKWARD>
+hipError_t tiles(const msamp_recurrence& a, const Spans& sp, hipStream_t s) {
+  const unsigned grid = (unsigned)(sp.blocks * sp.count * a.batch);
+  if (sp.count > 1) {
+    if (BACKWARD) k_backward_tile<T, WAVES, 1><<<grid, 64 * WAVES, 0, s>>>(a, sp);
+    else k_forward_tile<T, WAVES, 1><<<grid, 64 * WAVES, 0, s>>>(a, sp);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (BACKWARD) k_backward_tile<T, WAVES, 0><<<grid, 64 * WAVES, 0, s>>>(a, sp);
+  else k_forward_tile<T, WAVES, 0><<<grid, 64 * WAVES, 0, s>>>(a, sp);
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t backward(const msamp_recurrence& a, void*, hipStream_t s) {
-  const int64_t pairs = (a.channels + 1) / 2;
-  k_backward_lane<T><<<(unsigned)((a.batch * pairs + kBlock - 1) / kBlock), kBlock, 0, s>>>(a, pairs);
-  return hipGetLastError();
+// A lane goes through all steps of few, and where a tile's steps do not lie
+// within the 2^31 bytes of a buffer.
+bool lane_alone(const msamp_recurrence& a, bool backward) {
+  if (a.time <= kFewSteps) return true;
+  const int64_t most = ((int64_t)1 << 31) / (a.dtype == MSAMP_F32 ? 4 : 2) - a.channels;
+  const int64_t tile = kChunk * waves_of(a.time);
+  auto far = [&](int64_t stride) { return stride >= most / tile; };
+  if (far(a.x_time) || far(a.gate_time)) return true;
+  return backward ? far(a.dy_time) || far(a.dx_time) || far(a.dgate_time) : far(a.y_time);
+}
+
+template <typename T, bool BACKWARD>
+hipError_t run(const msamp_recurrence& a, void* ws, hipStream_t s) {
+  if (lane_alone(a, BACKWARD)) {
+    const int64_t pairs = (a.channels + 1) / 2;
+    const unsigned grid = (unsigned)((a.batch * pairs + kBlock - 1) / kBlock);
+    if (BACKWARD) k_backward_lane<T><<<grid, kBlock, 0, s>>>(a, pairs);
+    else k_forward_lane<T><<<grid, kBlock, 0, s>>>(a, pairs);
+    return hipGetLastError();
+  }
+  const Spans sp = spans_of(a, ws);
+  switch (waves_of(a.time)) {
+    case 1: return tiles<T, 1, BACKWARD>(a, sp, s);
+    case 2: return tiles<T, 2, BACKWARD>(a, sp, s);
+    case 4: return tiles<T, 4, BACKWARD>(a, sp, s);
+    default: return tiles<T, 8, BACKWARD>(a, sp, s);
+  }
 }
 
 }  // namespace
 
-int64_t recurrence_workspace(const msamp_recurrence&, bool) { return 0; }
+int64_t recurrence_workspace(const msamp_recurrence& a, bool backward) {
+  if (a.batch == 0 || a.channels == 0 || lane_alone(a, backward)) return 0;
+  const Spans s = spans_of(a, nullptr);
+  return s.count > 1 ? a.batch * s.count * s.pairs * (int64_t)sizeof(float4) : 0;
+}
 
 hipError_t launch_recurrence_forward(const msamp_recurrence& a, void* ws, hipStream_t s) {
-  return a.dtype == MSAMP_F32 ? forward<float>(a, ws, s)
-                              : a.dtype == MSAMP_F16 ? forward<f16>(a, ws, s) : forward<bf16>(a, ws, s);
+  return a.dtype == MSAMP_F32 ? run<float, false>(a, ws, s)
+                              : a.dtype == MSAMP_F16 ? run<f16, false>(a, ws, s) : run<bf16, false>(a, ws, s);
 }
 
 hipError_t launch_recurrence_backward(const msamp_recurrence& a, void* ws, hipStream_t s) {
-  return a.dtype == MSAMP_F32 ? backward<float>(a, ws, s)
-                              : a.dtype == MSAMP_F16 ? backward<f16>(a, ws, s) : backward<bf16>(a, ws, s);
+  return a.dtype == MSAMP_F32 ? run<float, true>(a, ws, s)
+                              : a.dtype == MSAMP_F16 ? run<f16, true>(a, ws, s) : run<bf16, true>(a, ws, s);
 }
 
 }  // namespace msamp
