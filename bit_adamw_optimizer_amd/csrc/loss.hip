@@ -18,53 +18,111 @@
 namespace msamp {
 namespace {
 
-constexpr int kBlock = 512, kWaves = kBlock / 64;
-constexpr int kTop = MSAMP_DISTILL_MAX_TOP;
 constexpr float kLog2e = 1.44269504088896341f;
 
 struct LossArgs {
   msamp_vocab_loss a;
-  float inv_tau;                     // 1 / tau
+  float inv_tau;             // 1 / tau
   double inv_tau64;
-  double log_low, log_high;          // logarithms of the clip's bounds
+  double log_low, log_high;  // logarithms of the clip's bounds
   float low, high, kl;
 };
 
-__device__ __forceinline__ float lane_max(float v) {
+__device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, off, 64));
   return v;
 }
 
-// Largest value and sum over the workgroup, given to every thread.
-__device__ __forceinline__ float block_largest(float v) {
-  __shared__ float part[kWaves];
-  v = lane_max(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = part[0];
+// Eight logits as they lie in memory.
+template <typename T>
+struct Raw8 {
+  u32x4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* p) {
+  Raw8<T> r;
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) v = __builtin_fmaxf(v, part[w]);
-  return v;
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = *((const GLOBAL u32x4_any*)p + i);
+  return r;
 }
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float part[kWaves];
-  v = wave_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = part[0];
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* p, int n) {  // -Inf behind the n-th
+  T v[8];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) v += part[w];
-  return v;
+  for (int k = 0; k < 8; ++k) v[k] = k < n ? ((const GLOBAL T*)p)[k] : (T)-INFINITY;
+  return __builtin_bit_cast(Raw8<T>, v);
+}
+// The same through a buffer that starts at a row's or part's first logit and
+// ends behind its last whole piece, so that a piece has one offset and none is
+// beyond the row. The up to 7 logits behind the whole pieces are a thread's
+// each.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(__amdgpu_buffer_rsrc_t b, uint32_t at) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+    r.w[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at + 16 * i, 0, 0));
+  return r;
+}
+constexpr int kPastCaches = 2;             // nt
+constexpr uint32_t kOutside = 0x80000000u;  // beyond every buffer: read as 0, not written
+template <typename T>
+__device__ __forceinline__ void put8(__amdgpu_buffer_rsrc_t b, uint32_t at, const float* f) {
+  struct V {
+    T v[8];
+  } v;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v.v[k] = from_f32<T>(f[k]);
+  const Raw8<T> r = __builtin_bit_cast(Raw8<T>, v);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+    __builtin_amdgcn_raw_buffer_store_b128(r.w[i], b, at + 16 * i, 0, kPastCaches);
+}
+template <typename T>
+__device__ __forceinline__ void values8(const Raw8<T>& r, float* f) {
+  struct V {
+    T v[8];
+  };
+  const V v = __builtin_bit_cast(V, r);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = to_f32(v.v[k]);
 }
 
-// The entries of a row: classes and their p, in LDS.
-struct Entries {
-  int32_t id[kTop];
-  float p[kTop];
+// Nothing to the hardware; to the compiler another value, so that it unpacks a
+// row's logits again in each pass instead of keeping them in twice the
+// registers.
+template <typename T>
+__device__ __forceinline__ void again(Raw8<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) asm volatile("" : "+v"(r.w[i]));
+}
+
+// A row's softmax while it is formed: the largest logit and the sum of
+// exp2((z - largest) scale). Logits of -Inf alone leave the largest at -Inf
+// and the sum at 0; a NaN makes the sum NaN.
+struct Soft {
+  float largest, sum;
 };
+__device__ __forceinline__ Soft join(Soft a, Soft b, float scale) {
+  const float m = __builtin_fmaxf(a.largest, b.largest), base = m == -INFINITY ? 0.0f : m;
+  return {m, a.sum * __builtin_amdgcn_exp2f((a.largest - base) * scale) +
+                 b.sum * __builtin_amdgcn_exp2f((b.largest - base) * scale)};
+}
+__device__ __forceinline__ float sum_exp8(const float* f, float base, float scale) {
+  float e[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) e[k] = __builtin_amdgcn_exp2f((f[k] - base) * scale);
+  return ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+}
+__device__ __forceinline__ float max8(const float* f, float m) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = __builtin_fmaxf(m, f[k]);
+  return m;
+}
 
 __device__ __forceinline__ float teacher_at(const msamp_vocab_loss& a, int64_t row, int j) {
   const int64_t i = row * a.ld_teacher + j;
@@ -73,168 +131,418 @@ __device__ __forceinline__ float teacher_at(const msamp_vocab_loss& a, int64_t r
   return to_f32(((const GLOBAL bf16*)a.teacher)[i]);
 }
 
-// Fills e with the row's entries (class -1: none). Returns whether the row has
-// any; *log_p is what the logarithm of an entry's p is less than its
-// (teacher - largest) / tau, which stays in e.p until p is formed.
-template <bool POLICY>
-__device__ __forceinline__ bool load_entries(const LossArgs& l, int64_t row, Entries& e, float* teacher_max,
-                                             float* teacher_sum) {
-  const msamp_vocab_loss& a = l.a;
-  if constexpr (POLICY) {
-    const int64_t id = load_int(a.ids, a.id_bytes, row);
-    const bool live = id >= 0 && id < a.vocab;
-    if (threadIdx.x == 0) {
-      e.id[0] = live ? (int32_t)id : -1;
-      e.p[0] = 1.0f;
+// The pieces of a row, or of a part of it, that a workgroup holds.
+template <typename T, int BLOCK, int NCH>
+struct Held {
+  Raw8<T> raw[NCH];
+  float last;  // this thread's logit behind the whole pieces; -Inf: none
+  int whole;   // pieces
+  int64_t end;  // the first logit behind them
+
+  __device__ __forceinline__ uint32_t at(int i) const {
+    const int p = i * BLOCK + (int)threadIdx.x;
+    return p < whole ? (uint32_t)(p * 8 * sizeof(T)) : kOutside;
+  }
+  // Logits [v0, vocab) of the row at z, as far as they go in.
+  __device__ __forceinline__ void cut(int64_t v0, int64_t vocab) {
+    const int64_t left = (vocab - v0) / 8;
+    whole = left < BLOCK * NCH ? (int)left : BLOCK * NCH;
+    end = v0 + (int64_t)whole * 8;
+  }
+  __device__ __forceinline__ bool has_last(int64_t vocab) const {
+    return whole < BLOCK * NCH && end + threadIdx.x < vocab;
+  }
+  __device__ __forceinline__ void load(const T* z, int64_t v0, int64_t vocab) {
+    const auto b = row_buffer(z + v0, (int64_t)whole * 8 * sizeof(T));
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) raw[i] = raw8<T>(b, at(i));
+    last = has_last(vocab) ? to_f32(((const GLOBAL T*)z)[end + threadIdx.x]) : -INFINITY;
+  }
+  // What was read beyond the whole pieces is -Inf from here on.
+  __device__ __forceinline__ void mask() {
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      if ((i + 1) * BLOCK <= whole) continue;  // the whole workgroup
+      constexpr uint32_t none = sizeof(T) == 4 ? 0xFF800000u : __is_same(T, f16) ? 0xFC00FC00u : 0xFF80FF80u;
+      if (i * BLOCK + (int)threadIdx.x >= whole) {
+#pragma unroll
+        for (int w = 0; w < (int)(sizeof(T) / 2); ++w) raw[i].w[w] = u32x4{none, none, none, none};
+      }
     }
-    __syncthreads();
+  }
+};
+
+// Largest logit of a thread's pieces over its wave. 16-bit logits that are not
+// negative order as their bits do, two to an instruction, so only where a wave
+// has none of those are the values compared.
+template <typename T, int N>
+__device__ __forceinline__ float largest_of(Raw8<T> (&raw)[N], float last) {
+  if constexpr (sizeof(T) == 2) {
+    typedef short s2 __attribute__((ext_vector_type(2)));
+    s2 m = {INT16_MIN, INT16_MIN};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t two = raw[i].w[0][k];
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(s2, two));
+      }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(s2, __shfl_xor(__builtin_bit_cast(int, m), off, 64)));
+    const short most = m.x > m.y ? m.x : m.y;
+    if (most >= 0) return wave_max(__builtin_fmaxf(last, to_f32(__builtin_bit_cast(T, most))));
+  }
+  float m = last;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float f[8];
+    again(raw[i]);
+    values8(raw[i], f);
+    m = max8(f, m);
+  }
+  return wave_max(m);
+}
+
+template <typename T, int BLOCK, int NCH>
+__device__ __forceinline__ Soft wave_softmax(Held<T, BLOCK, NCH>& held, float scale) {
+  held.mask();
+  const float largest = largest_of<T, NCH>(held.raw, held.last), base = largest == -INFINITY ? 0.0f : largest;
+  float sum = __builtin_amdgcn_exp2f((held.last - base) * scale);
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    float f[8];
+    again(held.raw[i]);
+    values8(held.raw[i], f);
+    sum += sum_exp8(f, base, scale);
+  }
+  return {largest, wave_sum(sum)};
+}
+
+enum { kPolicy = 0, kFewClasses = 1, kManyClasses = 2 };  // up to 64 classes: one to a lane of the first wave
+enum { kOwnSums = 0, kGivenSums = 1, kPartSums = 2 };
+
+// Where rows are cut into parts: what the first launch leaves to the second.
+struct Parts {
+  int count;
+  Soft* soft;  // [rows][count]
+  float* z;    // [rows][top]: the logits at the entries' classes, which the second launch may overwrite
+};
+
+// Whether the row takes part, and (kPolicy, kFewClasses) this lane's class in
+// *id, -1 if it has none. Every wave looks for itself, so that no logit of a
+// row that is left out is read.
+template <int KIND>
+__device__ __forceinline__ bool row_is_live(const msamp_vocab_loss& a, int64_t row, int lane, int64_t* id, float* t) {
+  *id = -1;
+  *t = -INFINITY;
+  if constexpr (KIND == kPolicy) {
+    const int64_t act = load_int(a.ids, a.id_bytes, row);
+    const bool live = act >= 0 && act < a.vocab;
+    if (live) *id = act;
     return live;
+  } else if constexpr (KIND == kFewClasses) {
+    if (lane < a.top) {
+      *id = load_int(a.ids, a.id_bytes, row * a.ld_ids + lane);
+      *t = teacher_at(a, row, lane);
+    }
+    if (*id < 0 || *id >= a.vocab || *t == -INFINITY) *id = -1, *t = -INFINITY;
+    return __ballot(*id >= 0) != 0;
   } else {
-    float most = -INFINITY;
-    bool nan = false;
-    for (int j = threadIdx.x; j < a.top; j += kBlock) {
-      const int64_t id = load_int(a.ids, a.id_bytes, row * a.ld_ids + j);
-      float t = teacher_at(a, row, j);
-      if (id < 0 || id >= a.vocab) t = -INFINITY;
-      e.id[j] = t == -INFINITY ? -1 : (int32_t)id;
-      e.p[j] = t;
-      nan |= t != t;
-      most = __builtin_fmaxf(most, t);
+    bool any = false;
+    for (int j = lane; j < a.top; j += 64) {
+      const int64_t i = load_int(a.ids, a.id_bytes, row * a.ld_ids + j);
+      any |= i >= 0 && i < a.vocab && teacher_at(a, row, j) != -INFINITY;
     }
-    if (nan) most = INFINITY;  // INFINITY - INFINITY: the row's results are NaN
-    most = block_largest(most);
-    float sum = 0.0f;
-    for (int j = threadIdx.x; j < a.top; j += kBlock) {
-      const float t = e.id[j] < 0 ? -INFINITY : (e.p[j] - most) * l.inv_tau;
-      e.p[j] = t;
-      sum += e.id[j] < 0 ? 0.0f : __expf(t);
-    }
-    sum = block_sum(sum);
-    *teacher_max = most;
-    *teacher_sum = sum;
-    return most != -INFINITY;
+    return __ballot(any) != 0;
   }
 }
 
-template <typename T, bool POLICY, bool BACKWARD>
-__global__ __launch_bounds__(kBlock) void k_loss(LossArgs l) {
-  __shared__ Entries e;
+// A row's entries in LDS (kManyClasses): classes (-1: none), the teacher's
+// exponentials, and what the gradient is there.
+struct Entries {
+  int32_t* id;
+  float* e;
+  float* at;
+};
+
+template <typename T, int BLOCK, int NCH>
+constexpr int waves_per_simd() {
+  return 1;
+}
+
+// One workgroup of BLOCK threads to a row, or to a part of one, of which each
+// thread holds NCH pieces of 8 logits in registers from the sums to the
+// gradient, so that the row is read once. NCH 0: rows of any length.
+//
+// Bound by memory where the arithmetic hides behind it: two exponentials and
+// about ten other operations a logit are 60% of the vector units' time at the
+// rate of the memory. The first wave alone has the entries; what it needs of
+// memory is under way before the row is.
+template <typename T, int KIND, int FROM, int BLOCK, int NCH>
+__global__ __launch_bounds__(BLOCK, (waves_per_simd<T, BLOCK, NCH>())) void k_loss(LossArgs l, Parts parts) {
+  constexpr int kWaves = BLOCK / 64;
+  constexpr int64_t kStep = BLOCK * 8;
+  extern __shared__ char lds[];
+  __shared__ Soft soft[kWaves];
+  __shared__ float part_of_loss[kWaves];
+  __shared__ float factor, teacher[2];
   const msamp_vocab_loss& a = l.a;
-  const int top = POLICY ? 1 : (int)a.top;
+  const int top = KIND == kPolicy ? 1 : (int)a.top;
+  const Entries e = {(int32_t*)lds, (float*)lds + top, (float*)lds + 2 * top};
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float scale = l.inv_tau * kLog2e;
+  const int64_t v0 = NCH > 0 ? blockIdx.y * (kStep * NCH) : 0;
+  const int64_t v1 = NCH > 0 && v0 + kStep * NCH < a.vocab ? v0 + kStep * NCH : a.vocab;
+  const bool first = FROM != kGivenSums && blockIdx.y == 0;  // writes the loss
+  Held<T, BLOCK, (NCH > 0 ? NCH : 1)> held;
+  held.cut(v0, a.vocab);
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* z = (const T*)a.logits + row * a.ld_logits;
     T* dz = (T*)a.dlogits + row * a.ld_dlogits;
-    float teacher_max = 0.0f, teacher_sum = 1.0f;
-    __syncthreads();
-    bool live = load_entries<POLICY>(l, row, e, &teacher_max, &teacher_sum);
-    float largest = 0.0f, sum = 0.0f;
+    int64_t id;
+    float t;
+    bool live = row_is_live<KIND>(a, row, lane, &id, &t);
+    Soft s = {0.0f, 0.0f};
+    float zc = 0.0f, old = 0.0f, adv = 0.0f, ref = 0.0f, dloss = 1.0f;
     if (live) {
-      if constexpr (BACKWARD) {
-        largest = a.stats[2 * row];
-        sum = a.stats[2 * row + 1];
-      } else {
-        float most = -INFINITY;
-        for (int64_t v = threadIdx.x * 8; v < a.vocab; v += kBlock * 8) {
-          const int n = (int)(a.vocab - v < 8 ? a.vocab - v : 8);
-          float f[8];
-          load8(z + v, n, f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) most = k < n ? __builtin_fmaxf(most, f[k]) : most;
+      if (wave == 0) {
+        if (KIND != kManyClasses && id >= 0)
+          zc = FROM == kPartSums ? parts.z[row * top + (KIND == kPolicy ? 0 : lane)] : to_f32(((const GLOBAL T*)z)[id]);
+        if (KIND == kPolicy) {
+          old = a.old_logp[row];
+          adv = a.advantages[row];
+          if (l.kl != 0.0f) ref = a.ref_logp[row];
         }
-        largest = block_largest(most);
-        // sums of at most 64 pieces are joined, so that no running sum has many terms
-        for (int64_t v0 = threadIdx.x * 8; v0 < a.vocab; v0 += 64 * kBlock * 8) {
-          float part = 0.0f;
-          for (int64_t v = v0; v < a.vocab && v < v0 + 64 * kBlock * 8; v += kBlock * 8) {
-            const int n = (int)(a.vocab - v < 8 ? a.vocab - v : 8);
-            float f[8];
-            load8(z + v, n, f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              f[k] = k < n ? __builtin_amdgcn_exp2f((f[k] - largest) * (l.inv_tau * kLog2e)) : 0.0f;
-            part += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-          }
-          sum += part;
-        }
-        sum = block_sum(sum);
       }
-      if (largest == -INFINITY) live = false, sum = 0.0f;
+      if (a.dlogits != nullptr && a.dloss != nullptr) dloss = a.dloss[row];
+      if constexpr (FROM == kGivenSums) s = {a.stats[2 * row], a.stats[2 * row + 1]};
+      if constexpr (NCH > 0) {
+        if (FROM == kOwnSums || a.dlogits != nullptr) held.load(z, v0, a.vocab);
+      }
     }
-    if (!BACKWARD && a.stats != nullptr && threadIdx.x == 0) {
-      a.stats[2 * row] = largest;
-      a.stats[2 * row + 1] = sum;
+    // the teacher's softmax: its exponentials, and their sum over the entries of one's own class
+    float teacher_log = 0.0f, teacher_inv = 0.0f, own = 0.0f, mine = 0.0f;
+    if (KIND == kFewClasses && live && wave == 0) {
+      const float most = wave_max(t != t ? INFINITY : t);  // NaN as Inf: Inf - Inf makes the row's results NaN
+      t = (t - most) * l.inv_tau;
+      own = id >= 0 ? __expf(t) : 0.0f;
+      const float sum = wave_sum(own);
+      teacher_log = logf(sum);
+      teacher_inv = 1.0f / sum;
+      for (int k = 0; k < top; ++k) {  // in the entries' order: the same sum for each entry of a class
+        const int other = __builtin_amdgcn_readlane((int)id, k);
+        const float p = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(own), k));
+        mine += (int)id == other ? p : 0.0f;
+      }
     }
-    // the loss and the factor of the gradient
-    float c = 0.0f;
-    if (live) {
-      const float dloss = a.dlogits == nullptr ? 0.0f : a.dloss == nullptr ? 1.0f : a.dloss[row];
-      if constexpr (POLICY) {
-        const double lp = (double)(to_f32(z[e.id[0]]) - largest) * l.inv_tau64 - log((double)sum);
-        const double d = lp - (double)a.old_logp[row];
-        const float adv = a.advantages[row], r = expf((float)d);
+    if (KIND == kManyClasses && live && wave == 0) {
+      float most = -INFINITY, sum = 0.0f;
+      for (int j = lane; j < top; j += 64) {
+        const int64_t i = load_int(a.ids, a.id_bytes, row * a.ld_ids + j);
+        float u = teacher_at(a, row, j);
+        if (i < 0 || i >= a.vocab) u = -INFINITY;
+        e.id[j] = u == -INFINITY ? -1 : (int32_t)i;
+        e.at[j] = u;
+        most = __builtin_fmaxf(most, u != u ? INFINITY : u);
+      }
+      most = wave_max(most);
+      for (int j = lane; j < top; j += 64) {
+        const float u = (e.at[j] - most) * l.inv_tau, x = e.id[j] < 0 ? 0.0f : __expf(u);
+        e.at[j] = u;
+        e.e[j] = x;
+        sum += x;
+      }
+      sum = wave_sum(sum);
+      if (lane == 0) teacher[0] = logf(sum), teacher[1] = 1.0f / sum;
+    }
+    if constexpr (FROM == kOwnSums) {
+      if (live) {
+        if constexpr (NCH > 0) {
+          s = wave_softmax<T, BLOCK, NCH>(held, scale);
+        }
+        if (kWaves > 1) {
+          if (lane == 0) soft[wave] = s;
+          __syncthreads();
+          s = soft[0];
+#pragma unroll
+          for (int w = 1; w < kWaves; ++w) s.largest = __builtin_fmaxf(s.largest, soft[w].largest);
+          const float base = s.largest == -INFINITY ? 0.0f : s.largest;
+          s.sum = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w)
+            s.sum += soft[w].sum * __builtin_amdgcn_exp2f((soft[w].largest - base) * scale);
+        }
+      }
+    }
+    if constexpr (FROM == kPartSums) {
+      if (live) {
+        s = parts.soft[row * parts.count];
+        for (int k = 1; k < parts.count; ++k) s = join(s, parts.soft[row * parts.count + k], scale);
+      }
+    }
+    if (KIND == kManyClasses && (FROM != kOwnSums || kWaves == 1)) __syncthreads();  // the entries are in LDS
+    if (first && a.stats != nullptr && threadIdx.x == 0) {
+      a.stats[2 * row] = s.largest;
+      a.stats[2 * row + 1] = s.sum;
+    }
+    if (live && s.largest == -INFINITY && s.sum == 0.0f) live = false;
+    if (!live) {
+      if (first && threadIdx.x == 0) {
+        a.loss[row] = 0.0f;
+        if (KIND == kPolicy && a.logp != nullptr) a.logp[row] = 0.0f;
+      }
+      if (a.dlogits != nullptr) {
+        const float zero[8] = {};
+        for (int64_t v = v0 + threadIdx.x * 8; v < v1; v += kStep)
+          store8<T, true>(dz + v, (int)(a.vocab - v < 8 ? a.vocab - v : 8), zero);
+      }
+      if (row + gridDim.x < a.rows) __syncthreads();  // what is in LDS is read before the next row's is written
+      continue;
+    }
+    // the loss, the gradient at the entries' classes ('at'), and its factor elsewhere
+    const float inv = 1.0f / s.sum;
+    float c = 0.0f, at = 0.0f;
+    if constexpr (KIND == kPolicy) {
+      if (wave == 0) {
+        const float zv = zc - s.largest;
+        const double lp = (double)zv * l.inv_tau64 - log((double)s.sum);
+        const double d = lp - (double)old;
+        const float r = expf((float)d);
         const bool over = adv > 0.0f && d > l.log_high, under = adv < 0.0f && d < l.log_low;
-        const float away = l.kl != 0.0f ? (float)((double)a.ref_logp[row] - lp) : 0.0f;
+        const float away = l.kl != 0.0f ? (float)((double)ref - lp) : 0.0f;
         const float more = expm1f(away);
-        if (!BACKWARD && threadIdx.x == 0) {
-          const float first = adv == 0.0f ? 0.0f : (over ? l.high : under ? l.low : r) * adv;
-          a.loss[row] = l.kl * (more - away) - first;
+        if (first && lane == 0) {
+          const float won = adv == 0.0f ? 0.0f : (over ? l.high : under ? l.low : r) * adv;
+          a.loss[row] = l.kl * (more - away) - won;
           if (a.logp != nullptr) a.logp[row] = (float)lp;
         }
         const float g = -l.kl * more - (over || under || adv == 0.0f ? 0.0f : r * adv);
         c = -dloss * g * l.inv_tau;
-      } else {
-        const float log_sum = logf(sum), log_teacher = logf(teacher_sum), inv = 1.0f / teacher_sum;
-        float part = 0.0f;
-        for (int j = threadIdx.x; j < top; j += kBlock) {
-          if (e.id[j] < 0) continue;
-          const float t = e.p[j], p = __expf(t) * inv;
-          if (!BACKWARD && p != 0.0f) {
-            const float q = (to_f32(z[e.id[j]]) - largest) * l.inv_tau;
-            part += p * ((t - log_teacher) - (q - log_sum));
-          }
-          e.p[j] = p;
-        }
-        if (!BACKWARD) {
-          const float tau = (float)a.temperature;
-          part = block_sum(part);
-          if (threadIdx.x == 0) a.loss[row] = tau * tau * part;
-        }
-        c = dloss * (float)a.temperature;
+        if (kWaves > 1 && lane == 0) factor = c;
+        at = (__builtin_amdgcn_exp2f(zv * scale) * inv - 1.0f) * c;
+        if (kWaves > 1 && lane == 0) part_of_loss[0] = at;
       }
-    } else if (!BACKWARD && threadIdx.x == 0) {
-      a.loss[row] = 0.0f;
-      if (POLICY && a.logp != nullptr) a.logp[row] = 0.0f;
-    }
-    if (a.dlogits == nullptr) continue;
-    if (!live) {
-      const float zero[8] = {};
-      for (int64_t v = threadIdx.x * 8; v < a.vocab; v += kBlock * 8)
-        store8<T, true>(dz + v, (int)(a.vocab - v < 8 ? a.vocab - v : 8), zero);
-      continue;
-    }
-    const float inv = 1.0f / sum, scale = l.inv_tau * kLog2e;
-    __syncthreads();  // every p is in LDS
-    float at[(kTop + kBlock - 1) / kBlock];
-    for (int j = threadIdx.x, i = 0; j < top; j += kBlock, ++i) {
-      at[i] = 0.0f;
-      if (e.id[j] < 0) continue;
-      float p = 0.0f;  // of every entry of this class, in their order: the same sum from each of them
-      for (int k = 0; k < top; ++k)
-        if (e.id[k] == e.id[j]) p += e.p[k];
-      at[i] = (__builtin_amdgcn_exp2f((to_f32(z[e.id[j]]) - largest) * scale) * inv - p) * c;
-    }
-    __syncthreads();  // the classes' logits are read before dlogits, which may be logits, is written
-    for (int64_t v = threadIdx.x * 8; v < a.vocab; v += kBlock * 8) {
-      const int n = (int)(a.vocab - v < 8 ? a.vocab - v : 8);
-      float f[8];
-      load8(z + v, n, f);
+      if (a.dlogits != nullptr && kWaves > 1) {
+        __syncthreads();
+        c = factor;
+        at = part_of_loss[0];
+      }
+    } else {
+      const float tau = (float)a.temperature, log_sum = logf(s.sum);
+      c = dloss * tau;
+      if constexpr (KIND == kFewClasses) {
+        if (wave == 0) {
+          const float zv = zc - s.largest, p = own * teacher_inv;
+          float loss = p != 0.0f ? p * ((t - teacher_log) - (zv * l.inv_tau - log_sum)) : 0.0f;
+          loss = wave_sum(loss);
+          if (first && lane == 0) a.loss[row] = tau * tau * loss;
+          at = (__builtin_amdgcn_exp2f(zv * scale) * inv - mine * teacher_inv) * c;
+        }
+        if (NCH == 0 && a.dlogits != nullptr) __syncthreads();  // these logits are read before the gradient is written
+      } else {
+        const float log_teacher = teacher[0], inv_teacher = teacher[1];
+        float loss = 0.0f;
+        for (int j = threadIdx.x; j < top; j += BLOCK) {
+          const int32_t i = e.id[j];
+          if (i < 0) continue;
+          const float zv = (FROM == kPartSums ? parts.z[row * top + j] : to_f32(((const GLOBAL T*)z)[i])) - s.largest;
+          const float p = e.e[j] * inv_teacher;
+          if (p != 0.0f) loss += p * ((e.at[j] - log_teacher) - (zv * l.inv_tau - log_sum));
+          float sum = 0.0f;
+          for (int k = 0; k < top; ++k) sum += e.id[k] == i ? e.e[k] : 0.0f;
+          e.at[j] = (__builtin_amdgcn_exp2f(zv * scale) * inv - sum * inv_teacher) * c;
+        }
+        loss = wave_sum(loss);
+        if (lane == 0) part_of_loss[wave] = loss;
+        __syncthreads();  // and the classes' logits are read before the gradient is written
+        if (first && threadIdx.x == 0) {
+          loss = part_of_loss[0];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = __builtin_amdgcn_exp2f((f[k] - largest) * scale) * inv * c;
-      store8(dz + v, n, f);
+          for (int w = 1; w < kWaves; ++w) loss += part_of_loss[w];
+          a.loss[row] = tau * tau * loss;
+        }
+      }
     }
-    __syncthreads();  // the entries' values go over the others'
-    for (int j = threadIdx.x, i = 0; j < top; j += kBlock, ++i)
-      if (e.id[j] >= 0) dz[e.id[j]] = from_f32<T>(at[i]);
+    if (a.dlogits != nullptr) {
+      const float k = c * inv;
+      auto gradient = [&](int64_t v, const Raw8<T>& r, float* f) {
+        values8(r, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __builtin_amdgcn_exp2f((f[j] - s.largest) * scale) * k;
+        if (KIND == kPolicy && v == (id & ~(int64_t)7)) {  // the action is in this piece
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = j == (int)(id & 7) ? at : f[j];
+        }
+      };
+      float f[8];
+      if constexpr (NCH > 0) {
+        const auto db = row_buffer(dz + v0, (int64_t)held.whole * 8 * sizeof(T));
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          again(held.raw[i]);
+          gradient(v0 + i * kStep + threadIdx.x * 8, held.raw[i], f);
+          put8<T>(db, held.at(i), f);
+        }
+        if (held.has_last(a.vocab)) {
+          const int64_t v = held.end + threadIdx.x;
+          const float g = __builtin_amdgcn_exp2f((held.last - s.largest) * scale) * k;
+          dz[v] = from_f32<T>(KIND == kPolicy && v == id ? at : g);
+        }
+      } else {
+        for (int64_t v = threadIdx.x * 8; v < a.vocab; v += kStep) {
+          const int n = (int)(a.vocab - v < 8 ? a.vocab - v : 8);
+          gradient(v, n == 8 ? raw8(z + v) : raw8(z + v, n), f);
+          store8<T, true>(dz + v, n, f);
+        }
+      }
+      if (KIND != kPolicy) {
+        __syncthreads();  // the classes' values go over the others'
+        if (KIND == kFewClasses) {
+          if (wave == 0 && id >= v0 && id < v1) dz[id] = from_f32<T>(at);
+        } else {
+          for (int j = threadIdx.x; j < top; j += BLOCK)
+            if (e.id[j] >= v0 && e.id[j] < v1) dz[e.id[j]] = from_f32<T>(e.at[j]);
+        }
+      }
+    }
+    if (row + gridDim.x < a.rows) __syncthreads();
+  }
+}
+
+// The sums of a row's parts, and the logits at its entries' classes.
+template <typename T, int KIND, int BLOCK, int NCH>
+__global__ __launch_bounds__(BLOCK) void k_parts(LossArgs l, Parts parts) {
+  constexpr int kWaves = BLOCK / 64;
+  constexpr int64_t kStep = BLOCK * 8;
+  __shared__ Soft soft[kWaves];
+  const msamp_vocab_loss& a = l.a;
+  const int top = KIND == kPolicy ? 1 : (int)a.top;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float scale = l.inv_tau * kLog2e;
+  const int64_t v0 = blockIdx.y * (kStep * NCH);
+  Held<T, BLOCK, NCH> held;
+  held.cut(v0, a.vocab);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* z = (const T*)a.logits + row * a.ld_logits;
+    int64_t id;
+    float t;
+    if (!row_is_live<KIND>(a, row, lane, &id, &t)) continue;  // the whole workgroup
+    held.load(z, v0, a.vocab);
+    if (blockIdx.y == 0) {
+      for (int j = threadIdx.x; j < top; j += BLOCK) {
+        const int64_t i = load_int(a.ids, a.id_bytes, KIND == kPolicy ? row : row * a.ld_ids + j);
+        if (i >= 0 && i < a.vocab) parts.z[row * top + j] = to_f32(((const GLOBAL T*)z)[i]);
+      }
+    }
+    Soft s = wave_softmax<T, BLOCK, NCH>(held, scale);
+    if (lane == 0) soft[wave] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kWaves; ++w) s = join(s, soft[w], scale);
+      parts.soft[row * parts.count + blockIdx.y] = s;
+    }
+    __syncthreads();
   }
 }
 
@@ -251,26 +559,92 @@ LossArgs loss_args(const msamp_vocab_loss& a) {
   return l;
 }
 
-template <bool POLICY, bool BACKWARD>
-hipError_t run(const msamp_vocab_loss& a, hipStream_t s) {
-  const LossArgs l = loss_args(a);
-  const unsigned grid = (unsigned)(a.rows < (1 << 20) ? a.rows : 1 << 20);
-  if (a.dtype == MSAMP_F32) k_loss<float, POLICY, BACKWARD><<<grid, kBlock, 0, s>>>(l);
-  else if (a.dtype == MSAMP_F16) k_loss<f16, POLICY, BACKWARD><<<grid, kBlock, 0, s>>>(l);
-  else k_loss<bf16, POLICY, BACKWARD><<<grid, kBlock, 0, s>>>(l);
+unsigned rows_of(const LossArgs& l) { return (unsigned)(l.a.rows < (1 << 20) ? l.a.rows : 1 << 20); }
+
+template <typename T, int KIND, int FROM, int BLOCK, int NCH>
+hipError_t launch(const LossArgs& l, const Parts& parts, int count, hipStream_t s) {
+  const size_t lds = KIND == kManyClasses ? 12 * (size_t)l.a.top : 0;
+  k_loss<T, KIND, FROM, BLOCK, NCH><<<dim3(rows_of(l), (unsigned)count), BLOCK, lds, s>>>(l, parts);
   return hipGetLastError();
+}
+
+// Pieces of 8 logits of a row, and how many of them a part has.
+constexpr int kPartBlock = 512;
+template <typename T>
+constexpr int part_chunks() {
+  return sizeof(T) == 4 ? 4 : 8;
+}
+int64_t pieces_of(const msamp_vocab_loss& a) { return (a.vocab + 7) / 8; }
+int64_t parts_of(const msamp_vocab_loss& a) {
+  const int64_t each = kPartBlock * (a.dtype == MSAMP_F32 ? 4 : 8);
+  return (pieces_of(a) + each - 1) / each;
+}
+// Rows that one workgroup does not hold in registers are cut into parts.
+bool in_parts(const msamp_vocab_loss& a) { return pieces_of(a) > 8192; }
+
+// The smallest workgroup that holds a row in registers.
+template <typename T, int KIND, int FROM>
+hipError_t whole(const LossArgs& l, hipStream_t s) {
+  const int64_t pieces = pieces_of(l.a);
+  const Parts none = {1, nullptr, nullptr};
+  if (pieces <= 64) return launch<T, KIND, FROM, 64, 1>(l, none, 1, s);
+  if (pieces <= 128) return launch<T, KIND, FROM, 64, 2>(l, none, 1, s);
+  if (pieces <= 256) return launch<T, KIND, FROM, 64, 4>(l, none, 1, s);
+  if (pieces <= 512) return launch<T, KIND, FROM, 256, 2>(l, none, 1, s);
+  if (pieces <= 1024) return launch<T, KIND, FROM, 256, 4>(l, none, 1, s);
+  if (pieces <= 2048) return launch<T, KIND, FROM, 512, 4>(l, none, 1, s);
+  if (sizeof(T) == 2 && pieces <= 4096) return launch<T, KIND, FROM, 512, 8>(l, none, 1, s);
+  if (sizeof(T) == 4 && pieces <= 4096) return launch<T, KIND, FROM, 1024, 4>(l, none, 1, s);
+  return launch<T, KIND, FROM, 1024, 8>(l, none, 1, s);
+}
+
+template <typename T, int KIND>
+hipError_t forward(const LossArgs& l, void* ws, hipStream_t s) {
+  if (!in_parts(l.a)) return whole<T, KIND, kOwnSums>(l, s);
+  constexpr int N = part_chunks<T>();
+  const int count = (int)parts_of(l.a);
+  const Parts parts = {count, (Soft*)ws, (float*)ws + 2 * l.a.rows * count};
+  k_parts<T, KIND, kPartBlock, N><<<dim3(rows_of(l), (unsigned)count), kPartBlock, 0, s>>>(l, parts);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch<T, KIND, kPartSums, kPartBlock, N>(l, parts, l.a.dlogits != nullptr ? count : 1, s);
+}
+
+// Parts read the logits at every class, so in place a long row stays with one
+// workgroup, which reads them before it writes.
+template <typename T, int KIND>
+hipError_t backward(const LossArgs& l, hipStream_t s) {
+  if (!in_parts(l.a)) return whole<T, KIND, kGivenSums>(l, s);
+  const Parts none = {1, nullptr, nullptr};
+  if (l.a.dlogits == l.a.logits) return launch<T, KIND, kGivenSums, kPartBlock, 0>(l, none, 1, s);
+  return launch<T, KIND, kGivenSums, kPartBlock, part_chunks<T>()>(l, none, (int)parts_of(l.a), s);
+}
+
+template <typename T>
+hipError_t run(const LossArgs& l, bool policy, bool back, void* ws, hipStream_t s) {
+  if (policy) return back ? backward<T, kPolicy>(l, s) : forward<T, kPolicy>(l, ws, s);
+  if (l.a.top <= 64) return back ? backward<T, kFewClasses>(l, s) : forward<T, kFewClasses>(l, ws, s);
+  return back ? backward<T, kManyClasses>(l, s) : forward<T, kManyClasses>(l, ws, s);
+}
+
+hipError_t run(const msamp_vocab_loss& a, bool policy, bool back, void* ws, hipStream_t s) {
+  const LossArgs l = loss_args(a);
+  return a.dtype == MSAMP_F32 ? run<float>(l, policy, back, ws, s)
+                              : a.dtype == MSAMP_F16 ? run<f16>(l, policy, back, ws, s) : run<bf16>(l, policy, back, ws, s);
 }
 
 }  // namespace
 
-int64_t loss_workspace(const msamp_vocab_loss&) { return 0; }
+int64_t loss_workspace(bool policy, const msamp_vocab_loss& a) {
+  return in_parts(a) ? a.rows * (8 * parts_of(a) + 4 * (policy ? 1 : a.top)) : 0;
+}
 
-hipError_t launch_loss_forward(bool policy, const msamp_vocab_loss& a, void*, hipStream_t s) {
-  return policy ? run<true, false>(a, s) : run<false, false>(a, s);
+hipError_t launch_loss_forward(bool policy, const msamp_vocab_loss& a, void* ws, hipStream_t s) {
+  return run(a, policy, false, ws, s);
 }
 
 hipError_t launch_loss_backward(bool policy, const msamp_vocab_loss& a, hipStream_t s) {
-  return policy ? run<true, true>(a, s) : run<false, true>(a, s);
+  return run(a, policy, true, nullptr, s);
 }
 
 }  // namespace msamp

@@ -42,7 +42,7 @@ int64_t recurrence_workspace(const msamp_recurrence& a, bool backward);
 hipError_t launch_recurrence_forward(const msamp_recurrence& a, void* ws, hipStream_t s);
 hipError_t launch_recurrence_backward(const msamp_recurrence& a, void* ws, hipStream_t s);
 
-int64_t loss_workspace(const msamp_vocab_loss& a);
+int64_t loss_workspace(bool policy, const msamp_vocab_loss& a);
 hipError_t launch_loss_forward(bool policy, const msamp_vocab_loss& a, void* ws, hipStream_t s);
 hipError_t launch_loss_backward(bool policy, const msamp_vocab_loss& a, hipStream_t s);
 

@@ -179,7 +179,7 @@ msamp_status run_loss_forward(const msamp_vocab_loss* args, bool policy, void* w
                               hipStream_t s) {
   MSAMP_TRY(check_loss(args, policy, false));
   if (args->rows == 0) return MSAMP_OK;
-  const int64_t need = loss_workspace(*args);
+  const int64_t need = loss_workspace(policy, *args);
   MSAMP_TRY(check_workspace(workspace, workspace_bytes, need));
   MSAMP_TRY(check_loss_memory(args, policy, false, workspace, need));
   MSAMP_LAUNCH(MSAMP_KERNEL_LOSS_FORWARD, s, launch_loss_forward(policy, *args, workspace, s));
@@ -307,7 +307,7 @@ msamp_status msamp_recurrence_backward(const msamp_recurrence* args, void* works
 int64_t msamp_distill_forward_workspace(const msamp_vocab_loss* args) {
   return workspace_of([&](int64_t* bytes) -> msamp_status {
     MSAMP_TRY(check_loss(args, false, false));
-    *bytes = loss_workspace(*args);
+    *bytes = loss_workspace(false, *args);
     return MSAMP_OK;
   });
 }
@@ -315,7 +315,7 @@ int64_t msamp_distill_forward_workspace(const msamp_vocab_loss* args) {
 int64_t msamp_policy_forward_workspace(const msamp_vocab_loss* args) {
   return workspace_of([&](int64_t* bytes) -> msamp_status {
     MSAMP_TRY(check_loss(args, true, false));
-    *bytes = loss_workspace(*args);
+    *bytes = loss_workspace(true, *args);
     return MSAMP_OK;
   });
 }
