@@ -22,6 +22,7 @@ constexpr float kLog2e = 1.44269504088896341f;
 
 struct LossArgs {
   msamp_vocab_loss a;
+  int64_t row0;              // of the launch's first workgroup
   float inv_tau;             // 1 / tau
   double inv_tau64;
   double log_low, log_high;  // logarithms of the clip's bounds
@@ -34,72 +35,44 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-// Eight logits as they lie in memory.
+// A piece of a row: the 16 bytes of 8 logits, or of 4 in binary32, as they lie
+// in memory.
 template <typename T>
-struct Raw8 {
-  u32x4 w[sizeof(T) / 2];
-};
+constexpr int kPer = 16 / (int)sizeof(T);
+
 template <typename T>
-__device__ __forceinline__ Raw8<T> raw8(const T* p) {
-  Raw8<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = *((const GLOBAL u32x4_any*)p + i);
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ Raw8<T> raw8(const T* p, int n) {  // -Inf behind the n-th
-  T v[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = k < n ? ((const GLOBAL T*)p)[k] : (T)-INFINITY;
-  return __builtin_bit_cast(Raw8<T>, v);
-}
-// The same through a buffer that starts at a row's or part's first logit and
-// ends behind its last whole piece, so that a piece has one offset and none is
-// beyond the row. The up to 7 logits behind the whole pieces are a thread's
-// each.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
-}
-template <typename T>
-__device__ __forceinline__ Raw8<T> raw8(__amdgpu_buffer_rsrc_t b, uint32_t at) {
-  Raw8<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-    r.w[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at + 16 * i, 0, 0));
-  return r;
-}
-constexpr int kPastCaches = 2;             // nt
-constexpr uint32_t kOutside = 0x80000000u;  // beyond every buffer: read as 0, not written
-template <typename T>
-__device__ __forceinline__ void put8(__amdgpu_buffer_rsrc_t b, uint32_t at, const float* f) {
+__device__ __forceinline__ void values(u32x4 r, float* f) {
   struct V {
-    T v[8];
-  } v;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v.v[k] = from_f32<T>(f[k]);
-  const Raw8<T> r = __builtin_bit_cast(Raw8<T>, v);
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-    __builtin_amdgcn_raw_buffer_store_b128(r.w[i], b, at + 16 * i, 0, kPastCaches);
-}
-template <typename T>
-__device__ __forceinline__ void values8(const Raw8<T>& r, float* f) {
-  struct V {
-    T v[8];
+    T v[kPer<T>];
   };
   const V v = __builtin_bit_cast(V, r);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = to_f32(v.v[k]);
+  for (int k = 0; k < kPer<T>; ++k) f[k] = to_f32(v.v[k]);
 }
+template <typename T>
+__device__ __forceinline__ u32x4 rounded(const float* f) {
+  struct V {
+    T v[kPer<T>];
+  } v;
+#pragma unroll
+  for (int k = 0; k < kPer<T>; ++k) v.v[k] = from_f32<T>(f[k]);
+  return __builtin_bit_cast(u32x4, v);
+}
+
+// Pieces are read and written through a buffer that starts at a row's or
+// part's first logit and ends behind its last whole piece, so that a piece has
+// one offset and none is beyond the row. The few logits behind the whole pieces
+// are a thread's each.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+constexpr int kPastCaches = 2;             // nt
+constexpr uint32_t kOutside = 0x80000000u;  // beyond every buffer: read as 0, not written
 
 // Nothing to the hardware; to the compiler another value, so that it unpacks a
 // row's logits again in each pass instead of keeping them in twice the
 // registers.
-template <typename T>
-__device__ __forceinline__ void again(Raw8<T>& r) {
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) asm volatile("" : "+v"(r.w[i]));
-}
+__device__ __forceinline__ void again(u32x4& r) { asm volatile("" : "+v"(r)); }
 
 // A row's softmax while it is formed: the largest logit and the sum of
 // exp2((z - largest) scale). Logits of -Inf alone leave the largest at -Inf
@@ -112,16 +85,16 @@ __device__ __forceinline__ Soft join(Soft a, Soft b, float scale) {
   return {m, a.sum * __builtin_amdgcn_exp2f((a.largest - base) * scale) +
                  b.sum * __builtin_amdgcn_exp2f((b.largest - base) * scale)};
 }
-__device__ __forceinline__ float sum_exp8(const float* f, float base, float scale) {
-  float e[8];
+template <int N>
+__device__ __forceinline__ float sum_exp(const float* f, float base, float scale) {
+  float e[N];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) e[k] = __builtin_amdgcn_exp2f((f[k] - base) * scale);
-  return ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-}
-__device__ __forceinline__ float max8(const float* f, float m) {
+  for (int k = 0; k < N; ++k) e[k] = __builtin_amdgcn_exp2f((f[k] - base) * scale);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = __builtin_fmaxf(m, f[k]);
-  return m;
+  for (int n = N / 2; n > 0; n /= 2)
+#pragma unroll
+    for (int k = 0; k < n; ++k) e[k] += e[k + n];
+  return e[0];
 }
 
 __device__ __forceinline__ float teacher_at(const msamp_vocab_loss& a, int64_t row, int j) {
@@ -134,28 +107,29 @@ __device__ __forceinline__ float teacher_at(const msamp_vocab_loss& a, int64_t r
 // The pieces of a row, or of a part of it, that a workgroup holds.
 template <typename T, int BLOCK, int NCH>
 struct Held {
-  Raw8<T> raw[NCH];
-  float last;  // this thread's logit behind the whole pieces; -Inf: none
-  int whole;   // pieces
+  u32x4 raw[NCH];
+  float last;   // this thread's logit behind the whole pieces; -Inf: none
+  int whole;    // pieces
   int64_t end;  // the first logit behind them
 
   __device__ __forceinline__ uint32_t at(int i) const {
     const int p = i * BLOCK + (int)threadIdx.x;
-    return p < whole ? (uint32_t)(p * 8 * sizeof(T)) : kOutside;
+    return p < whole ? (uint32_t)p * 16 : kOutside;
   }
-  // Logits [v0, vocab) of the row at z, as far as they go in.
+  // Logits [v0, vocab) of a row, as far as they go in.
   __device__ __forceinline__ void cut(int64_t v0, int64_t vocab) {
-    const int64_t left = (vocab - v0) / 8;
+    const int64_t left = (vocab - v0) / kPer<T>;
     whole = left < BLOCK * NCH ? (int)left : BLOCK * NCH;
-    end = v0 + (int64_t)whole * 8;
+    end = v0 + (int64_t)whole * kPer<T>;
   }
   __device__ __forceinline__ bool has_last(int64_t vocab) const {
     return whole < BLOCK * NCH && end + threadIdx.x < vocab;
   }
   __device__ __forceinline__ void load(const T* z, int64_t v0, int64_t vocab) {
-    const auto b = row_buffer(z + v0, (int64_t)whole * 8 * sizeof(T));
+    const auto b = row_buffer(z + v0, (int64_t)whole * 16);
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) raw[i] = raw8<T>(b, at(i));
+    for (int i = 0; i < NCH; ++i)
+      raw[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at(i), 0, 0));
     last = has_last(vocab) ? to_f32(((const GLOBAL T*)z)[end + threadIdx.x]) : -INFINITY;
   }
   // What was read beyond the whole pieces is -Inf from here on.
@@ -164,10 +138,7 @@ struct Held {
     for (int i = 0; i < NCH; ++i) {
       if ((i + 1) * BLOCK <= whole) continue;  // the whole workgroup
       constexpr uint32_t none = sizeof(T) == 4 ? 0xFF800000u : __is_same(T, f16) ? 0xFC00FC00u : 0xFF80FF80u;
-      if (i * BLOCK + (int)threadIdx.x >= whole) {
-#pragma unroll
-        for (int w = 0; w < (int)(sizeof(T) / 2); ++w) raw[i].w[w] = u32x4{none, none, none, none};
-      }
+      if (i * BLOCK + (int)threadIdx.x >= whole) raw[i] = u32x4{none, none, none, none};
     }
   }
 };
@@ -176,7 +147,7 @@ struct Held {
 // negative order as their bits do, two to an instruction, so only where a wave
 // has none of those are the values compared.
 template <typename T, int N>
-__device__ __forceinline__ float largest_of(Raw8<T> (&raw)[N], float last) {
+__device__ __forceinline__ float largest_of(u32x4 (&raw)[N], float last) {
   if constexpr (sizeof(T) == 2) {
     typedef short s2 __attribute__((ext_vector_type(2)));
     s2 m = {INT16_MIN, INT16_MIN};
@@ -184,7 +155,7 @@ __device__ __forceinline__ float largest_of(Raw8<T> (&raw)[N], float last) {
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t two = raw[i].w[0][k];
+        const uint32_t two = raw[i][k];
         m = __builtin_elementwise_max(m, __builtin_bit_cast(s2, two));
       }
 #pragma unroll
@@ -196,10 +167,11 @@ __device__ __forceinline__ float largest_of(Raw8<T> (&raw)[N], float last) {
   float m = last;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float f[8];
+    float f[kPer<T>];
     again(raw[i]);
-    values8(raw[i], f);
-    m = max8(f, m);
+    values<T>(raw[i], f);
+#pragma unroll
+    for (int k = 0; k < kPer<T>; ++k) m = __builtin_fmaxf(m, f[k]);
   }
   return wave_max(m);
 }
@@ -211,10 +183,10 @@ __device__ __forceinline__ Soft wave_softmax(Held<T, BLOCK, NCH>& held, float sc
   float sum = __builtin_amdgcn_exp2f((held.last - base) * scale);
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    float f[8];
+    float f[kPer<T>];
     again(held.raw[i]);
-    values8(held.raw[i], f);
-    sum += sum_exp8(f, base, scale);
+    values<T>(held.raw[i], f);
+    sum += sum_exp<kPer<T>>(f, base, scale);
   }
   return {largest, wave_sum(sum)};
 }
@@ -266,11 +238,6 @@ struct Entries {
   float* at;
 };
 
-template <typename T, int BLOCK, int NCH>
-constexpr int waves_per_simd() {
-  return 1;
-}
-
 // One workgroup of BLOCK threads to a row, or to a part of one, of which each
 // thread holds NCH pieces of 8 logits in registers from the sums to the
 // gradient, so that the row is read once. NCH 0: rows of any length.
@@ -280,9 +247,9 @@ constexpr int waves_per_simd() {
 // rate of the memory. The first wave alone has the entries; what it needs of
 // memory is under way before the row is.
 template <typename T, int KIND, int FROM, int BLOCK, int NCH>
-__global__ __launch_bounds__(BLOCK, (waves_per_simd<T, BLOCK, NCH>())) void k_loss(LossArgs l, Parts parts) {
+__global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
   constexpr int kWaves = BLOCK / 64;
-  constexpr int64_t kStep = BLOCK * 8;
+  constexpr int64_t kStep = BLOCK * kPer<T>;
   extern __shared__ char lds[];
   __shared__ Soft soft[kWaves];
   __shared__ float part_of_loss[kWaves];
@@ -297,216 +264,214 @@ __global__ __launch_bounds__(BLOCK, (waves_per_simd<T, BLOCK, NCH>())) void k_lo
   const bool first = FROM != kGivenSums && blockIdx.y == 0;  // writes the loss
   Held<T, BLOCK, (NCH > 0 ? NCH : 1)> held;
   held.cut(v0, a.vocab);
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const T* z = (const T*)a.logits + row * a.ld_logits;
-    T* dz = (T*)a.dlogits + row * a.ld_dlogits;
-    int64_t id;
-    float t;
-    bool live = row_is_live<KIND>(a, row, lane, &id, &t);
-    Soft s = {0.0f, 0.0f};
-    float zc = 0.0f, old = 0.0f, adv = 0.0f, ref = 0.0f, dloss = 1.0f;
+  const int64_t row = l.row0 + blockIdx.x;
+  const T* z = (const T*)a.logits + row * a.ld_logits;
+  T* dz = (T*)a.dlogits + row * a.ld_dlogits;
+  int64_t id;
+  float t;
+  bool live = row_is_live<KIND>(a, row, lane, &id, &t);
+  Soft s = {0.0f, 0.0f};
+  float zc = 0.0f, old = 0.0f, adv = 0.0f, ref = 0.0f, dloss = 1.0f;
+  if (live) {
+    if (wave == 0) {
+      if (KIND != kManyClasses && id >= 0)
+        zc = FROM == kPartSums ? parts.z[row * top + (KIND == kPolicy ? 0 : lane)] : to_f32(((const GLOBAL T*)z)[id]);
+      if (KIND == kPolicy) {
+        old = a.old_logp[row];
+        adv = a.advantages[row];
+        if (l.kl != 0.0f) ref = a.ref_logp[row];
+      }
+    }
+    if (a.dlogits != nullptr && a.dloss != nullptr) dloss = a.dloss[row];
+    if constexpr (FROM == kGivenSums) s = {a.stats[2 * row], a.stats[2 * row + 1]};
+    if constexpr (NCH > 0) {
+      if (FROM == kOwnSums || a.dlogits != nullptr) held.load(z, v0, a.vocab);
+    }
+  }
+  // the teacher's softmax: its exponentials, and their sum over the entries of one's own class
+  float teacher_log = 0.0f, teacher_inv = 0.0f, own = 0.0f, mine = 0.0f;
+  if (KIND == kFewClasses && live && wave == 0) {
+    const float most = wave_max(t != t ? INFINITY : t);  // NaN as Inf: Inf - Inf makes the row's results NaN
+    t = (t - most) * l.inv_tau;
+    own = id >= 0 ? __expf(t) : 0.0f;
+    const float sum = wave_sum(own);
+    teacher_log = logf(sum);
+    teacher_inv = 1.0f / sum;
+    for (int k = 0; k < top; ++k) {  // in the entries' order: the same sum for each entry of a class
+      const int other = __builtin_amdgcn_readlane((int)id, k);
+      const float p = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(own), k));
+      mine += (int)id == other ? p : 0.0f;
+    }
+  }
+  if (KIND == kManyClasses && live && wave == 0) {
+    float most = -INFINITY, sum = 0.0f;
+    for (int j = lane; j < top; j += 64) {
+      const int64_t i = load_int(a.ids, a.id_bytes, row * a.ld_ids + j);
+      float u = teacher_at(a, row, j);
+      if (i < 0 || i >= a.vocab) u = -INFINITY;
+      e.id[j] = u == -INFINITY ? -1 : (int32_t)i;
+      e.at[j] = u;
+      most = __builtin_fmaxf(most, u != u ? INFINITY : u);
+    }
+    most = wave_max(most);
+    for (int j = lane; j < top; j += 64) {
+      const float u = (e.at[j] - most) * l.inv_tau, x = e.id[j] < 0 ? 0.0f : __expf(u);
+      e.at[j] = u;
+      e.e[j] = x;
+      sum += x;
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) teacher[0] = logf(sum), teacher[1] = 1.0f / sum;
+  }
+  if constexpr (FROM == kOwnSums) {
     if (live) {
-      if (wave == 0) {
-        if (KIND != kManyClasses && id >= 0)
-          zc = FROM == kPartSums ? parts.z[row * top + (KIND == kPolicy ? 0 : lane)] : to_f32(((const GLOBAL T*)z)[id]);
-        if (KIND == kPolicy) {
-          old = a.old_logp[row];
-          adv = a.advantages[row];
-          if (l.kl != 0.0f) ref = a.ref_logp[row];
-        }
-      }
-      if (a.dlogits != nullptr && a.dloss != nullptr) dloss = a.dloss[row];
-      if constexpr (FROM == kGivenSums) s = {a.stats[2 * row], a.stats[2 * row + 1]};
       if constexpr (NCH > 0) {
-        if (FROM == kOwnSums || a.dlogits != nullptr) held.load(z, v0, a.vocab);
+        s = wave_softmax<T, BLOCK, NCH>(held, scale);
       }
-    }
-    // the teacher's softmax: its exponentials, and their sum over the entries of one's own class
-    float teacher_log = 0.0f, teacher_inv = 0.0f, own = 0.0f, mine = 0.0f;
-    if (KIND == kFewClasses && live && wave == 0) {
-      const float most = wave_max(t != t ? INFINITY : t);  // NaN as Inf: Inf - Inf makes the row's results NaN
-      t = (t - most) * l.inv_tau;
-      own = id >= 0 ? __expf(t) : 0.0f;
-      const float sum = wave_sum(own);
-      teacher_log = logf(sum);
-      teacher_inv = 1.0f / sum;
-      for (int k = 0; k < top; ++k) {  // in the entries' order: the same sum for each entry of a class
-        const int other = __builtin_amdgcn_readlane((int)id, k);
-        const float p = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(own), k));
-        mine += (int)id == other ? p : 0.0f;
-      }
-    }
-    if (KIND == kManyClasses && live && wave == 0) {
-      float most = -INFINITY, sum = 0.0f;
-      for (int j = lane; j < top; j += 64) {
-        const int64_t i = load_int(a.ids, a.id_bytes, row * a.ld_ids + j);
-        float u = teacher_at(a, row, j);
-        if (i < 0 || i >= a.vocab) u = -INFINITY;
-        e.id[j] = u == -INFINITY ? -1 : (int32_t)i;
-        e.at[j] = u;
-        most = __builtin_fmaxf(most, u != u ? INFINITY : u);
-      }
-      most = wave_max(most);
-      for (int j = lane; j < top; j += 64) {
-        const float u = (e.at[j] - most) * l.inv_tau, x = e.id[j] < 0 ? 0.0f : __expf(u);
-        e.at[j] = u;
-        e.e[j] = x;
-        sum += x;
-      }
-      sum = wave_sum(sum);
-      if (lane == 0) teacher[0] = logf(sum), teacher[1] = 1.0f / sum;
-    }
-    if constexpr (FROM == kOwnSums) {
-      if (live) {
-        if constexpr (NCH > 0) {
-          s = wave_softmax<T, BLOCK, NCH>(held, scale);
-        }
-        if (kWaves > 1) {
-          if (lane == 0) soft[wave] = s;
-          __syncthreads();
-          s = soft[0];
-#pragma unroll
-          for (int w = 1; w < kWaves; ++w) s.largest = __builtin_fmaxf(s.largest, soft[w].largest);
-          const float base = s.largest == -INFINITY ? 0.0f : s.largest;
-          s.sum = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w)
-            s.sum += soft[w].sum * __builtin_amdgcn_exp2f((soft[w].largest - base) * scale);
-        }
-      }
-    }
-    if constexpr (FROM == kPartSums) {
-      if (live) {
-        s = parts.soft[row * parts.count];
-        for (int k = 1; k < parts.count; ++k) s = join(s, parts.soft[row * parts.count + k], scale);
-      }
-    }
-    if (KIND == kManyClasses && (FROM != kOwnSums || kWaves == 1)) __syncthreads();  // the entries are in LDS
-    if (first && a.stats != nullptr && threadIdx.x == 0) {
-      a.stats[2 * row] = s.largest;
-      a.stats[2 * row + 1] = s.sum;
-    }
-    if (live && s.largest == -INFINITY && s.sum == 0.0f) live = false;
-    if (!live) {
-      if (first && threadIdx.x == 0) {
-        a.loss[row] = 0.0f;
-        if (KIND == kPolicy && a.logp != nullptr) a.logp[row] = 0.0f;
-      }
-      if (a.dlogits != nullptr) {
-        const float zero[8] = {};
-        for (int64_t v = v0 + threadIdx.x * 8; v < v1; v += kStep)
-          store8<T, true>(dz + v, (int)(a.vocab - v < 8 ? a.vocab - v : 8), zero);
-      }
-      if (row + gridDim.x < a.rows) __syncthreads();  // what is in LDS is read before the next row's is written
-      continue;
-    }
-    // the loss, the gradient at the entries' classes ('at'), and its factor elsewhere
-    const float inv = 1.0f / s.sum;
-    float c = 0.0f, at = 0.0f;
-    if constexpr (KIND == kPolicy) {
-      if (wave == 0) {
-        const float zv = zc - s.largest;
-        const double lp = (double)zv * l.inv_tau64 - log((double)s.sum);
-        const double d = lp - (double)old;
-        const float r = expf((float)d);
-        const bool over = adv > 0.0f && d > l.log_high, under = adv < 0.0f && d < l.log_low;
-        const float away = l.kl != 0.0f ? (float)((double)ref - lp) : 0.0f;
-        const float more = expm1f(away);
-        if (first && lane == 0) {
-          const float won = adv == 0.0f ? 0.0f : (over ? l.high : under ? l.low : r) * adv;
-          a.loss[row] = l.kl * (more - away) - won;
-          if (a.logp != nullptr) a.logp[row] = (float)lp;
-        }
-        const float g = -l.kl * more - (over || under || adv == 0.0f ? 0.0f : r * adv);
-        c = -dloss * g * l.inv_tau;
-        if (kWaves > 1 && lane == 0) factor = c;
-        at = (__builtin_amdgcn_exp2f(zv * scale) * inv - 1.0f) * c;
-        if (kWaves > 1 && lane == 0) part_of_loss[0] = at;
-      }
-      if (a.dlogits != nullptr && kWaves > 1) {
+      if (kWaves > 1) {
+        if (lane == 0) soft[wave] = s;
         __syncthreads();
-        c = factor;
-        at = part_of_loss[0];
-      }
-    } else {
-      const float tau = (float)a.temperature, log_sum = logf(s.sum);
-      c = dloss * tau;
-      if constexpr (KIND == kFewClasses) {
-        if (wave == 0) {
-          const float zv = zc - s.largest, p = own * teacher_inv;
-          float loss = p != 0.0f ? p * ((t - teacher_log) - (zv * l.inv_tau - log_sum)) : 0.0f;
-          loss = wave_sum(loss);
-          if (first && lane == 0) a.loss[row] = tau * tau * loss;
-          at = (__builtin_amdgcn_exp2f(zv * scale) * inv - mine * teacher_inv) * c;
-        }
-        if (NCH == 0 && a.dlogits != nullptr) __syncthreads();  // these logits are read before the gradient is written
-      } else {
-        const float log_teacher = teacher[0], inv_teacher = teacher[1];
-        float loss = 0.0f;
-        for (int j = threadIdx.x; j < top; j += BLOCK) {
-          const int32_t i = e.id[j];
-          if (i < 0) continue;
-          const float zv = (FROM == kPartSums ? parts.z[row * top + j] : to_f32(((const GLOBAL T*)z)[i])) - s.largest;
-          const float p = e.e[j] * inv_teacher;
-          if (p != 0.0f) loss += p * ((e.at[j] - log_teacher) - (zv * l.inv_tau - log_sum));
-          float sum = 0.0f;
-          for (int k = 0; k < top; ++k) sum += e.id[k] == i ? e.e[k] : 0.0f;
-          e.at[j] = (__builtin_amdgcn_exp2f(zv * scale) * inv - sum * inv_teacher) * c;
-        }
-        loss = wave_sum(loss);
-        if (lane == 0) part_of_loss[wave] = loss;
-        __syncthreads();  // and the classes' logits are read before the gradient is written
-        if (first && threadIdx.x == 0) {
-          loss = part_of_loss[0];
+        s = soft[0];
 #pragma unroll
-          for (int w = 1; w < kWaves; ++w) loss += part_of_loss[w];
-          a.loss[row] = tau * tau * loss;
-        }
+        for (int w = 1; w < kWaves; ++w) s.largest = __builtin_fmaxf(s.largest, soft[w].largest);
+        const float base = s.largest == -INFINITY ? 0.0f : s.largest;
+        s.sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+          s.sum += soft[w].sum * __builtin_amdgcn_exp2f((soft[w].largest - base) * scale);
       }
+    }
+  }
+  if constexpr (FROM == kPartSums) {
+    if (live) {
+      s = parts.soft[row * parts.count];
+      for (int k = 1; k < parts.count; ++k) s = join(s, parts.soft[row * parts.count + k], scale);
+    }
+  }
+  if (KIND == kManyClasses && (FROM != kOwnSums || kWaves == 1)) __syncthreads();  // the entries are in LDS
+  if (first && a.stats != nullptr && threadIdx.x == 0) {
+    a.stats[2 * row] = s.largest;
+    a.stats[2 * row + 1] = s.sum;
+  }
+  if (live && s.largest == -INFINITY && s.sum == 0.0f) live = false;
+  if (!live) {
+    if (first && threadIdx.x == 0) {
+      a.loss[row] = 0.0f;
+      if (KIND == kPolicy && a.logp != nullptr) a.logp[row] = 0.0f;
     }
     if (a.dlogits != nullptr) {
-      const float k = c * inv;
-      auto gradient = [&](int64_t v, const Raw8<T>& r, float* f) {
-        values8(r, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __builtin_amdgcn_exp2f((f[j] - s.largest) * scale) * k;
-        if (KIND == kPolicy && v == (id & ~(int64_t)7)) {  // the action is in this piece
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = j == (int)(id & 7) ? at : f[j];
-        }
-      };
-      float f[8];
-      if constexpr (NCH > 0) {
-        const auto db = row_buffer(dz + v0, (int64_t)held.whole * 8 * sizeof(T));
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-          again(held.raw[i]);
-          gradient(v0 + i * kStep + threadIdx.x * 8, held.raw[i], f);
-          put8<T>(db, held.at(i), f);
-        }
-        if (held.has_last(a.vocab)) {
-          const int64_t v = held.end + threadIdx.x;
-          const float g = __builtin_amdgcn_exp2f((held.last - s.largest) * scale) * k;
-          dz[v] = from_f32<T>(KIND == kPolicy && v == id ? at : g);
-        }
-      } else {
-        for (int64_t v = threadIdx.x * 8; v < a.vocab; v += kStep) {
-          const int n = (int)(a.vocab - v < 8 ? a.vocab - v : 8);
-          gradient(v, n == 8 ? raw8(z + v) : raw8(z + v, n), f);
-          store8<T, true>(dz + v, n, f);
-        }
+      const float zero[8] = {};
+      for (int64_t v = v0 + threadIdx.x * 8; v < v1; v += BLOCK * 8)
+        store8<T, true>(dz + v, (int)(v1 - v < 8 ? v1 - v : 8), zero);
+    }
+    return;
+  }
+  // the loss, the gradient at the entries' classes ('at'), and its factor elsewhere
+  const float inv = 1.0f / s.sum;
+  float c = 0.0f, at = 0.0f;
+  if constexpr (KIND == kPolicy) {
+    if (wave == 0) {
+      const float zv = zc - s.largest;
+      const double lp = (double)zv * l.inv_tau64 - log((double)s.sum);
+      const double d = lp - (double)old;
+      const float r = expf((float)d);
+      const bool over = adv > 0.0f && d > l.log_high, under = adv < 0.0f && d < l.log_low;
+      const float away = l.kl != 0.0f ? (float)((double)ref - lp) : 0.0f;
+      const float more = expm1f(away);
+      if (first && lane == 0) {
+        const float won = adv == 0.0f ? 0.0f : (over ? l.high : under ? l.low : r) * adv;
+        a.loss[row] = l.kl * (more - away) - won;
+        if (a.logp != nullptr) a.logp[row] = (float)lp;
       }
-      if (KIND != kPolicy) {
-        __syncthreads();  // the classes' values go over the others'
-        if (KIND == kFewClasses) {
-          if (wave == 0 && id >= v0 && id < v1) dz[id] = from_f32<T>(at);
-        } else {
-          for (int j = threadIdx.x; j < top; j += BLOCK)
-            if (e.id[j] >= v0 && e.id[j] < v1) dz[e.id[j]] = from_f32<T>(e.at[j]);
-        }
+      const float g = -l.kl * more - (over || under || adv == 0.0f ? 0.0f : r * adv);
+      c = -dloss * g * l.inv_tau;
+      if (kWaves > 1 && lane == 0) factor = c;
+      at = (__builtin_amdgcn_exp2f(zv * scale) * inv - 1.0f) * c;
+      if (kWaves > 1 && lane == 0) part_of_loss[0] = at;
+    }
+    if (a.dlogits != nullptr && kWaves > 1) {
+      __syncthreads();
+      c = factor;
+      at = part_of_loss[0];
+    }
+  } else {
+    const float tau = (float)a.temperature, log_sum = logf(s.sum);
+    c = dloss * tau;
+    if constexpr (KIND == kFewClasses) {
+      if (wave == 0) {
+        const float zv = zc - s.largest, p = own * teacher_inv;
+        float loss = p != 0.0f ? p * ((t - teacher_log) - (zv * l.inv_tau - log_sum)) : 0.0f;
+        loss = wave_sum(loss);
+        if (first && lane == 0) a.loss[row] = tau * tau * loss;
+        at = (__builtin_amdgcn_exp2f(zv * scale) * inv - mine * teacher_inv) * c;
+      }
+      if (NCH == 0 && a.dlogits != nullptr) __syncthreads();  // these logits are read before the gradient is written
+    } else {
+      const float log_teacher = teacher[0], inv_teacher = teacher[1];
+      float loss = 0.0f;
+      for (int j = threadIdx.x; j < top; j += BLOCK) {
+        const int32_t i = e.id[j];
+        if (i < 0) continue;
+        const float zv = (FROM == kPartSums ? parts.z[row * top + j] : to_f32(((const GLOBAL T*)z)[i])) - s.largest;
+        const float p = e.e[j] * inv_teacher;
+        if (p != 0.0f) loss += p * ((e.at[j] - log_teacher) - (zv * l.inv_tau - log_sum));
+        float sum = 0.0f;
+        for (int k = 0; k < top; ++k) sum += e.id[k] == i ? e.e[k] : 0.0f;
+        e.at[j] = (__builtin_amdgcn_exp2f(zv * scale) * inv - sum * inv_teacher) * c;
+      }
+      loss = wave_sum(loss);
+      if (lane == 0) part_of_loss[wave] = loss;
+      __syncthreads();  // and the classes' logits are read before the gradient is written
+      if (first && threadIdx.x == 0) {
+        loss = part_of_loss[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) loss += part_of_loss[w];
+        a.loss[row] = tau * tau * loss;
       }
     }
-    if (row + gridDim.x < a.rows) __syncthreads();
+  }
+  if (a.dlogits != nullptr) {
+    const float k = c * inv;
+    constexpr int N = kPer<T>;
+    auto gradient = [&](int64_t v, u32x4 r) {
+      float f[N];
+      values<T>(r, f);
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[j] = __builtin_amdgcn_exp2f((f[j] - s.largest) * scale) * k;
+      if (KIND == kPolicy && v == (id & ~(int64_t)(N - 1))) {  // the action is in this piece
+#pragma unroll
+        for (int j = 0; j < N; ++j) f[j] = j == (int)(id & (N - 1)) ? at : f[j];
+      }
+      return rounded<T>(f);
+    };
+    auto single = [&](int64_t v, float zv) {
+      const float g = __builtin_amdgcn_exp2f((zv - s.largest) * scale) * k;
+      dz[v] = from_f32<T>(KIND == kPolicy && v == id ? at : g);
+    };
+    if constexpr (NCH > 0) {
+      const auto db = row_buffer(dz + v0, (int64_t)held.whole * 16);
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        again(held.raw[i]);
+        __builtin_amdgcn_raw_buffer_store_b128(gradient(v0 + i * kStep + threadIdx.x * N, held.raw[i]), db, held.at(i), 0,
+                                               kPastCaches);
+      }
+      if (held.has_last(a.vocab)) single(held.end + threadIdx.x, held.last);
+    } else {
+      const int64_t whole = a.vocab / N * N;
+      for (int64_t v = threadIdx.x * N; v < whole; v += kStep)
+        *(GLOBAL u32x4_any*)(dz + v) = gradient(v, *(const GLOBAL u32x4_any*)(z + v));
+      if (whole + threadIdx.x < a.vocab) single(whole + threadIdx.x, to_f32(((const GLOBAL T*)z)[whole + threadIdx.x]));
+    }
+    if (KIND != kPolicy) {
+      __syncthreads();  // the classes' values go over the others'
+      if (KIND == kFewClasses) {
+        if (wave == 0 && id >= v0 && id < v1) dz[id] = from_f32<T>(at);
+      } else {
+        for (int j = threadIdx.x; j < top; j += BLOCK)
+          if (e.id[j] >= v0 && e.id[j] < v1) dz[e.id[j]] = from_f32<T>(e.at[j]);
+      }
+    }
   }
 }
 
@@ -514,7 +479,7 @@ __global__ __launch_bounds__(BLOCK, (waves_per_simd<T, BLOCK, NCH>())) void k_lo
 template <typename T, int KIND, int BLOCK, int NCH>
 __global__ __launch_bounds__(BLOCK) void k_parts(LossArgs l, Parts parts) {
   constexpr int kWaves = BLOCK / 64;
-  constexpr int64_t kStep = BLOCK * 8;
+  constexpr int64_t kStep = BLOCK * kPer<T>;
   __shared__ Soft soft[kWaves];
   const msamp_vocab_loss& a = l.a;
   const int top = KIND == kPolicy ? 1 : (int)a.top;
@@ -523,32 +488,31 @@ __global__ __launch_bounds__(BLOCK) void k_parts(LossArgs l, Parts parts) {
   const int64_t v0 = blockIdx.y * (kStep * NCH);
   Held<T, BLOCK, NCH> held;
   held.cut(v0, a.vocab);
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const T* z = (const T*)a.logits + row * a.ld_logits;
-    int64_t id;
-    float t;
-    if (!row_is_live<KIND>(a, row, lane, &id, &t)) continue;  // the whole workgroup
-    held.load(z, v0, a.vocab);
-    if (blockIdx.y == 0) {
-      for (int j = threadIdx.x; j < top; j += BLOCK) {
-        const int64_t i = load_int(a.ids, a.id_bytes, KIND == kPolicy ? row : row * a.ld_ids + j);
-        if (i >= 0 && i < a.vocab) parts.z[row * top + j] = to_f32(((const GLOBAL T*)z)[i]);
-      }
+  const int64_t row = l.row0 + blockIdx.x;
+  const T* z = (const T*)a.logits + row * a.ld_logits;
+  int64_t id;
+  float t;
+  if (!row_is_live<KIND>(a, row, lane, &id, &t)) return;  // the whole workgroup
+  held.load(z, v0, a.vocab);
+  if (blockIdx.y == 0) {
+    for (int j = threadIdx.x; j < top; j += BLOCK) {
+      const int64_t i = load_int(a.ids, a.id_bytes, KIND == kPolicy ? row : row * a.ld_ids + j);
+      if (i >= 0 && i < a.vocab) parts.z[row * top + j] = to_f32(((const GLOBAL T*)z)[i]);
     }
-    Soft s = wave_softmax<T, BLOCK, NCH>(held, scale);
-    if (lane == 0) soft[wave] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kWaves; ++w) s = join(s, soft[w], scale);
-      parts.soft[row * parts.count + blockIdx.y] = s;
-    }
-    __syncthreads();
+  }
+  Soft s = wave_softmax<T, BLOCK, NCH>(held, scale);
+  if (lane == 0) soft[wave] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kWaves; ++w) s = join(s, soft[w], scale);
+    parts.soft[row * parts.count + blockIdx.y] = s;
   }
 }
 
 LossArgs loss_args(const msamp_vocab_loss& a) {
   LossArgs l;
   l.a = a;
+  l.row0 = 0;
   l.inv_tau = (float)(1.0 / a.temperature);
   l.inv_tau64 = 1.0 / a.temperature;
   l.log_low = std::log(1.0 - a.clip_low);
@@ -559,33 +523,43 @@ LossArgs loss_args(const msamp_vocab_loss& a) {
   return l;
 }
 
-unsigned rows_of(const LossArgs& l) { return (unsigned)(l.a.rows < (1 << 20) ? l.a.rows : 1 << 20); }
+// One workgroup to a row (a loop over rows would keep its constants in
+// registers), at most 2^20 rows a launch.
+template <typename F>
+hipError_t each_rows(const LossArgs& l, F&& f) {
+  LossArgs part = l;
+  for (part.row0 = 0; part.row0 < l.a.rows; part.row0 += 1 << 20) {
+    const int64_t left = l.a.rows - part.row0;
+    f(part, (unsigned)(left < (1 << 20) ? left : 1 << 20));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 template <typename T, int KIND, int FROM, int BLOCK, int NCH>
 hipError_t launch(const LossArgs& l, const Parts& parts, int count, hipStream_t s) {
   const size_t lds = KIND == kManyClasses ? 12 * (size_t)l.a.top : 0;
-  k_loss<T, KIND, FROM, BLOCK, NCH><<<dim3(rows_of(l), (unsigned)count), BLOCK, lds, s>>>(l, parts);
-  return hipGetLastError();
+  return each_rows(l, [&](const LossArgs& p, unsigned rows) {
+    k_loss<T, KIND, FROM, BLOCK, NCH><<<dim3(rows, (unsigned)count), BLOCK, lds, s>>>(p, parts);
+  });
 }
 
-// Pieces of 8 logits of a row, and how many of them a part has.
-constexpr int kPartBlock = 512;
-template <typename T>
-constexpr int part_chunks() {
-  return sizeof(T) == 4 ? 4 : 8;
-}
-int64_t pieces_of(const msamp_vocab_loss& a) { return (a.vocab + 7) / 8; }
+// Rows that one workgroup does not hold in registers are cut into parts of
+// 32,768 16-bit or 16,384 binary32 logits.
+constexpr int kPartBlock = 512, kPartPieces = 8;
+int64_t bytes_of(const msamp_vocab_loss& a) { return a.vocab * (a.dtype == MSAMP_F32 ? 4 : 2); }
 int64_t parts_of(const msamp_vocab_loss& a) {
-  const int64_t each = kPartBlock * (a.dtype == MSAMP_F32 ? 4 : 8);
-  return (pieces_of(a) + each - 1) / each;
+  return (bytes_of(a) + kPartBlock * kPartPieces * 16 - 1) / (kPartBlock * kPartPieces * 16);
 }
-// Rows that one workgroup does not hold in registers are cut into parts.
-bool in_parts(const msamp_vocab_loss& a) { return pieces_of(a) > 8192; }
+bool in_parts(const msamp_vocab_loss& a) { return bytes_of(a) > 512 * 16 * 16; }
 
-// The smallest workgroup that holds a row in registers.
+// The smallest workgroup that holds a row in registers. Rows fit where their
+// pieces do: those logits behind the last whole piece have a register of their
+// own.
 template <typename T, int KIND, int FROM>
 hipError_t whole(const LossArgs& l, hipStream_t s) {
-  const int64_t pieces = pieces_of(l.a);
+  const int64_t pieces = (bytes_of(l.a) + 15) / 16;
   const Parts none = {1, nullptr, nullptr};
   if (pieces <= 64) return launch<T, KIND, FROM, 64, 1>(l, none, 1, s);
   if (pieces <= 128) return launch<T, KIND, FROM, 64, 2>(l, none, 1, s);
@@ -593,21 +567,21 @@ hipError_t whole(const LossArgs& l, hipStream_t s) {
   if (pieces <= 512) return launch<T, KIND, FROM, 256, 2>(l, none, 1, s);
   if (pieces <= 1024) return launch<T, KIND, FROM, 256, 4>(l, none, 1, s);
   if (pieces <= 2048) return launch<T, KIND, FROM, 512, 4>(l, none, 1, s);
-  if (sizeof(T) == 2 && pieces <= 4096) return launch<T, KIND, FROM, 512, 8>(l, none, 1, s);
-  if (sizeof(T) == 4 && pieces <= 4096) return launch<T, KIND, FROM, 1024, 4>(l, none, 1, s);
-  return launch<T, KIND, FROM, 1024, 8>(l, none, 1, s);
+  if (pieces <= 4096) return launch<T, KIND, FROM, 512, 8>(l, none, 1, s);
+  if (pieces <= 6656) return launch<T, KIND, FROM, 512, 13>(l, none, 1, s);
+  return launch<T, KIND, FROM, 512, 16>(l, none, 1, s);
 }
 
 template <typename T, int KIND>
 hipError_t forward(const LossArgs& l, void* ws, hipStream_t s) {
   if (!in_parts(l.a)) return whole<T, KIND, kOwnSums>(l, s);
-  constexpr int N = part_chunks<T>();
   const int count = (int)parts_of(l.a);
   const Parts parts = {count, (Soft*)ws, (float*)ws + 2 * l.a.rows * count};
-  k_parts<T, KIND, kPartBlock, N><<<dim3(rows_of(l), (unsigned)count), kPartBlock, 0, s>>>(l, parts);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = each_rows(l, [&](const LossArgs& p, unsigned rows) {
+    k_parts<T, KIND, kPartBlock, kPartPieces><<<dim3(rows, (unsigned)count), kPartBlock, 0, s>>>(p, parts);
+  });
   if (e != hipSuccess) return e;
-  return launch<T, KIND, kPartSums, kPartBlock, N>(l, parts, l.a.dlogits != nullptr ? count : 1, s);
+  return launch<T, KIND, kPartSums, kPartBlock, kPartPieces>(l, parts, l.a.dlogits != nullptr ? count : 1, s);
 }
 
 // Parts read the logits at every class, so in place a long row stays with one
@@ -617,7 +591,7 @@ hipError_t backward(const LossArgs& l, hipStream_t s) {
   if (!in_parts(l.a)) return whole<T, KIND, kGivenSums>(l, s);
   const Parts none = {1, nullptr, nullptr};
   if (l.a.dlogits == l.a.logits) return launch<T, KIND, kGivenSums, kPartBlock, 0>(l, none, 1, s);
-  return launch<T, KIND, kGivenSums, kPartBlock, part_chunks<T>()>(l, none, (int)parts_of(l.a), s);
+  return launch<T, KIND, kGivenSums, kPartBlock, kPartPieces>(l, none, (int)parts_of(l.a), s);
 }
 
 template <typename T>
