@@ -59,10 +59,10 @@ __device__ __forceinline__ u32x4 rounded(const float* f) {
   return __builtin_bit_cast(u32x4, v);
 }
 
-// Pieces are read and written through a buffer that starts at a row's or
-// part's first logit and ends behind its last whole piece, so that a piece has
-// one offset and none is beyond the row. The few logits behind the whole pieces
-// are a thread's each.
+// The pieces of a row start at its first logit on 16 bytes. They are read and
+// written through a buffer that ends behind the last whole one, so that a piece
+// has one offset and none is beyond the row. The few logits before and behind
+// the pieces are a thread's each.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
 }
@@ -108,29 +108,36 @@ __device__ __forceinline__ float teacher_at(const msamp_vocab_loss& a, int64_t r
 template <typename T, int BLOCK, int NCH>
 struct Held {
   u32x4 raw[NCH];
-  float last;   // this thread's logit behind the whole pieces; -Inf: none
-  int whole;    // pieces
-  int64_t end;  // the first logit behind them
+  float single;      // this thread's logit outside the pieces; -Inf: none
+  int whole;         // pieces
+  int64_t start;     // of the pieces
+  int64_t lo, hi;    // of the part, with the logits outside the pieces
+  int64_t single_v;  // where this thread's is; -1: none
 
   __device__ __forceinline__ uint32_t at(int i) const {
     const int p = i * BLOCK + (int)threadIdx.x;
     return p < whole ? (uint32_t)p * 16 : kOutside;
   }
-  // Logits [v0, vocab) of a row, as far as they go in.
-  __device__ __forceinline__ void cut(int64_t v0, int64_t vocab) {
-    const int64_t left = (vocab - v0) / kPer<T>;
-    whole = left < BLOCK * NCH ? (int)left : BLOCK * NCH;
-    end = v0 + (int64_t)whole * kPer<T>;
+  __device__ __forceinline__ void cut(const T* z, int part, int64_t vocab) {
+    constexpr int N = kPer<T>, kMost = BLOCK * NCH;
+    int64_t head = (-(int64_t)(uintptr_t)z & 15) / (int)sizeof(T);
+    if (head > vocab) head = vocab;
+    start = head + (int64_t)part * (kMost * N);
+    const int64_t left = vocab > start ? (vocab - start) / N : 0;
+    whole = left < kMost ? (int)left : kMost;
+    const int64_t end = start + (int64_t)whole * N;
+    const bool last = whole < kMost;
+    lo = part == 0 ? 0 : start;
+    hi = last ? vocab : end;
+    const int i = threadIdx.x;
+    single_v = part == 0 && i < head ? i : last && i >= 16 && end + i - 16 < vocab ? end + i - 16 : -1;
   }
-  __device__ __forceinline__ bool has_last(int64_t vocab) const {
-    return whole < BLOCK * NCH && end + threadIdx.x < vocab;
-  }
-  __device__ __forceinline__ void load(const T* z, int64_t v0, int64_t vocab) {
-    const auto b = row_buffer(z + v0, (int64_t)whole * 16);
+  __device__ __forceinline__ void load(const T* z) {
+    const auto b = row_buffer(z + start, (int64_t)whole * 16);
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
       raw[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at(i), 0, 0));
-    last = has_last(vocab) ? to_f32(((const GLOBAL T*)z)[end + threadIdx.x]) : -INFINITY;
+    single = single_v >= 0 ? to_f32(((const GLOBAL T*)z)[single_v]) : -INFINITY;
   }
   // What was read beyond the whole pieces is -Inf from here on.
   __device__ __forceinline__ void mask() {
@@ -147,7 +154,7 @@ struct Held {
 // negative order as their bits do, two to an instruction, so only where a wave
 // has none of those are the values compared.
 template <typename T, int N>
-__device__ __forceinline__ float largest_of(u32x4 (&raw)[N], float last) {
+__device__ __forceinline__ float largest_of(u32x4 (&raw)[N], float single) {
   if constexpr (sizeof(T) == 2) {
     typedef short s2 __attribute__((ext_vector_type(2)));
     s2 m = {INT16_MIN, INT16_MIN};
@@ -162,9 +169,9 @@ __device__ __forceinline__ float largest_of(u32x4 (&raw)[N], float last) {
     for (int off = 32; off > 0; off >>= 1)
       m = __builtin_elementwise_max(m, __builtin_bit_cast(s2, __shfl_xor(__builtin_bit_cast(int, m), off, 64)));
     const short most = m.x > m.y ? m.x : m.y;
-    if (most >= 0) return wave_max(__builtin_fmaxf(last, to_f32(__builtin_bit_cast(T, most))));
+    if (most >= 0) return wave_max(__builtin_fmaxf(single, to_f32(__builtin_bit_cast(T, most))));
   }
-  float m = last;
+  float m = single;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     float f[kPer<T>];
@@ -179,8 +186,8 @@ __device__ __forceinline__ float largest_of(u32x4 (&raw)[N], float last) {
 template <typename T, int BLOCK, int NCH>
 __device__ __forceinline__ Soft wave_softmax(Held<T, BLOCK, NCH>& held, float scale) {
   held.mask();
-  const float largest = largest_of<T, NCH>(held.raw, held.last), base = largest == -INFINITY ? 0.0f : largest;
-  float sum = __builtin_amdgcn_exp2f((held.last - base) * scale);
+  const float largest = largest_of<T, NCH>(held.raw, held.single), base = largest == -INFINITY ? 0.0f : largest;
+  float sum = __builtin_amdgcn_exp2f((held.single - base) * scale);
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     float f[kPer<T>];
@@ -259,14 +266,13 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
   const Entries e = {(int32_t*)lds, (float*)lds + top, (float*)lds + 2 * top};
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float scale = l.inv_tau * kLog2e;
-  const int64_t v0 = NCH > 0 ? blockIdx.y * (kStep * NCH) : 0;
-  const int64_t v1 = NCH > 0 && v0 + kStep * NCH < a.vocab ? v0 + kStep * NCH : a.vocab;
   const bool first = FROM != kGivenSums && blockIdx.y == 0;  // writes the loss
-  Held<T, BLOCK, (NCH > 0 ? NCH : 1)> held;
-  held.cut(v0, a.vocab);
   const int64_t row = l.row0 + blockIdx.x;
   const T* z = (const T*)a.logits + row * a.ld_logits;
   T* dz = (T*)a.dlogits + row * a.ld_dlogits;
+  Held<T, BLOCK, (NCH > 0 ? NCH : 1)> held;
+  held.cut(z, NCH > 0 ? blockIdx.y : 0, a.vocab);
+  if (NCH == 0) held.lo = 0, held.hi = a.vocab;
   int64_t id;
   float t;
   bool live = row_is_live<KIND>(a, row, lane, &id, &t);
@@ -285,7 +291,7 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
     if (a.dlogits != nullptr && a.dloss != nullptr) dloss = a.dloss[row];
     if constexpr (FROM == kGivenSums) s = {a.stats[2 * row], a.stats[2 * row + 1]};
     if constexpr (NCH > 0) {
-      if (FROM == kOwnSums || a.dlogits != nullptr) held.load(z, v0, a.vocab);
+      if (FROM == kOwnSums || a.dlogits != nullptr) held.load(z);
     }
   }
   // the teacher's softmax: its exponentials, and their sum over the entries of one's own class
@@ -361,8 +367,8 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
     }
     if (a.dlogits != nullptr) {
       const float zero[8] = {};
-      for (int64_t v = v0 + threadIdx.x * 8; v < v1; v += BLOCK * 8)
-        store8<T, true>(dz + v, (int)(v1 - v < 8 ? v1 - v : 8), zero);
+      for (int64_t v = held.lo + threadIdx.x * 8; v < held.hi; v += BLOCK * 8)
+        store8<T, true>(dz + v, (int)(held.hi - v < 8 ? held.hi - v : 8), zero);
     }
     return;
   }
@@ -438,9 +444,9 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
       values<T>(r, f);
 #pragma unroll
       for (int j = 0; j < N; ++j) f[j] = __builtin_amdgcn_exp2f((f[j] - s.largest) * scale) * k;
-      if (KIND == kPolicy && v == (id & ~(int64_t)(N - 1))) {  // the action is in this piece
+      if (KIND == kPolicy && id >= v && id < v + N) {  // the action is in this piece
 #pragma unroll
-        for (int j = 0; j < N; ++j) f[j] = j == (int)(id & (N - 1)) ? at : f[j];
+        for (int j = 0; j < N; ++j) f[j] = id == v + j ? at : f[j];
       }
       return rounded<T>(f);
     };
@@ -449,14 +455,14 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
       dz[v] = from_f32<T>(KIND == kPolicy && v == id ? at : g);
     };
     if constexpr (NCH > 0) {
-      const auto db = row_buffer(dz + v0, (int64_t)held.whole * 16);
+      const auto db = row_buffer(dz + held.start, (int64_t)held.whole * 16);
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
         again(held.raw[i]);
-        __builtin_amdgcn_raw_buffer_store_b128(gradient(v0 + i * kStep + threadIdx.x * N, held.raw[i]), db, held.at(i), 0,
+        __builtin_amdgcn_raw_buffer_store_b128(gradient(held.start + i * kStep + threadIdx.x * N, held.raw[i]), db, held.at(i), 0,
                                                kPastCaches);
       }
-      if (held.has_last(a.vocab)) single(held.end + threadIdx.x, held.last);
+      if (held.single_v >= 0) single(held.single_v, held.single);
     } else {
       const int64_t whole = a.vocab / N * N;
       for (int64_t v = threadIdx.x * N; v < whole; v += kStep)
@@ -466,10 +472,10 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
     if (KIND != kPolicy) {
       __syncthreads();  // the classes' values go over the others'
       if (KIND == kFewClasses) {
-        if (wave == 0 && id >= v0 && id < v1) dz[id] = from_f32<T>(at);
+        if (wave == 0 && id >= held.lo && id < held.hi) dz[id] = from_f32<T>(at);
       } else {
         for (int j = threadIdx.x; j < top; j += BLOCK)
-          if (e.id[j] >= v0 && e.id[j] < v1) dz[e.id[j]] = from_f32<T>(e.at[j]);
+          if (e.id[j] >= held.lo && e.id[j] < held.hi) dz[e.id[j]] = from_f32<T>(e.at[j]);
       }
     }
   }
@@ -485,15 +491,14 @@ __global__ __launch_bounds__(BLOCK) void k_parts(LossArgs l, Parts parts) {
   const int top = KIND == kPolicy ? 1 : (int)a.top;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float scale = l.inv_tau * kLog2e;
-  const int64_t v0 = blockIdx.y * (kStep * NCH);
-  Held<T, BLOCK, NCH> held;
-  held.cut(v0, a.vocab);
   const int64_t row = l.row0 + blockIdx.x;
   const T* z = (const T*)a.logits + row * a.ld_logits;
+  Held<T, BLOCK, NCH> held;
+  held.cut(z, blockIdx.y, a.vocab);
   int64_t id;
   float t;
   if (!row_is_live<KIND>(a, row, lane, &id, &t)) return;  // the whole workgroup
-  held.load(z, v0, a.vocab);
+  held.load(z);
   if (blockIdx.y == 0) {
     for (int j = threadIdx.x; j < top; j += BLOCK) {
       const int64_t i = load_int(a.ids, a.id_bytes, KIND == kPolicy ? row : row * a.ld_ids + j);
