@@ -132,11 +132,12 @@ struct Held {
     const int i = threadIdx.x;
     single_v = part == 0 && i < head ? i : last && i >= 16 && end + i - 16 < vocab ? end + i - 16 : -1;
   }
+  template <int CACHES>
   __device__ __forceinline__ void load(const T* z) {
     const auto b = row_buffer(z + start, (int64_t)whole * 16);
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
-      raw[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at(i), 0, 0));
+      raw[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at(i), 0, CACHES));
     single = single_v >= 0 ? to_f32(((const GLOBAL T*)z)[single_v]) : -INFINITY;
   }
   // What was read beyond the whole pieces is -Inf from here on.
@@ -291,7 +292,7 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
     if (a.dlogits != nullptr && a.dloss != nullptr) dloss = a.dloss[row];
     if constexpr (FROM == kGivenSums) s = {a.stats[2 * row], a.stats[2 * row + 1]};
     if constexpr (NCH > 0) {
-      if (FROM == kOwnSums || a.dlogits != nullptr) held.load(z);
+      if (FROM == kOwnSums || a.dlogits != nullptr) held.template load<kPastCaches>(z);
     }
   }
   // the teacher's softmax: its exponentials, and their sum over the entries of one's own class
@@ -485,7 +486,6 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
 template <typename T, int KIND, int BLOCK, int NCH>
 __global__ __launch_bounds__(BLOCK) void k_parts(LossArgs l, Parts parts) {
   constexpr int kWaves = BLOCK / 64;
-  constexpr int64_t kStep = BLOCK * kPer<T>;
   __shared__ Soft soft[kWaves];
   const msamp_vocab_loss& a = l.a;
   const int top = KIND == kPolicy ? 1 : (int)a.top;
@@ -498,7 +498,7 @@ __global__ __launch_bounds__(BLOCK) void k_parts(LossArgs l, Parts parts) {
   int64_t id;
   float t;
   if (!row_is_live<KIND>(a, row, lane, &id, &t)) return;  // the whole workgroup
-  held.load(z);
+  held.template load<0>(z);  // read again by the second launch
   if (blockIdx.y == 0) {
     for (int j = threadIdx.x; j < top; j += BLOCK) {
       const int64_t i = load_int(a.ids, a.id_bytes, KIND == kPolicy ? row : row * a.ld_ids + j);
