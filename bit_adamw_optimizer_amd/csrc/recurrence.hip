@@ -14,6 +14,10 @@ namespace msamp {
 namespace {
 
 constexpr int kChunk = MSAMP_RECURRENCE_CHUNK;
+#ifndef KL16
+#define KL16 32
+#endif
+constexpr int kLanes16 = KL16;
 
 // Two consecutive channels as they lie in memory; n (1 or 2) of them are the
 // tensor's.
@@ -60,8 +64,9 @@ struct Pair {
                        to_f32(__builtin_bit_cast(T, (uint16_t)(r >> 16))));
   }
   static __device__ __forceinline__ raw packed(float2 v) {
-    return (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(v.x)) |
-           (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(v.y)) << 16;
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef T t2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(raw, __builtin_convertvector((f2{v.x, v.y}), t2));
   }
   static __device__ __forceinline__ void store(T* p, int n, float2 v) {
     if (n >= 2) *(GLOBAL u32_any*)p = packed(v);
@@ -204,7 +209,7 @@ struct Spans {
 
 template <typename T>
 constexpr int lanes_of() {
-  return sizeof(T) == 2 ? 32 : 16;  // 128 bytes of a step
+  return sizeof(T) == 2 ? kLanes16 : 16;
 }
 
 struct Affine {  // v -> a v + s
@@ -262,6 +267,14 @@ __device__ __forceinline__ uint32_t once(uint32_t v) {
   asm volatile("" : "+v"(v));
   return v;
 }
+// Nothing to the hardware; to the compiler another value, which it unpacks
+// again where it is used instead of keeping it in twice the registers.
+__device__ __forceinline__ uint32_t again(uint32_t v) { return once(v); }
+__device__ __forceinline__ u32x2 again(u32x2 v) { return v; }  // binary32: nothing is unpacked
+
+// Formed here and not where it is used next, behind what it is formed from.
+__device__ __forceinline__ void formed(float2& v) { asm volatile("" : "+v"(v.x), "+v"(v.y)); }
+
 // odd: the block holds the last of an odd number of channels, whose lane
 // (n = 1) has no second one.
 template <typename T, int R>
@@ -293,7 +306,7 @@ __device__ __forceinline__ void store_steps(__amdgpu_buffer_rsrc_t b, const Step
 // Place of a workgroup: block of channels, sequence, span.
 struct Place {
   int lane, wave, group, n;
-  bool odd;
+  bool odd, none;
   int64_t b, c, span, len, t0, t1;  // steps [t0, t1) of the span
 };
 template <int LANES>
@@ -302,11 +315,16 @@ __device__ __forceinline__ Place place_of(const msamp_recurrence& a, const Spans
   p.lane = threadIdx.x & 63;
   p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   p.group = p.lane / LANES;
-  const uint32_t per = (uint32_t)(sp.blocks * sp.count);
-  p.b = blockIdx.x / per;
-  const uint32_t rest = blockIdx.x - (uint32_t)p.b * per;
-  p.span = rest / (uint32_t)sp.blocks;
-  const int64_t block = rest - (uint32_t)p.span * (uint32_t)sp.blocks;
+  // neighbouring blocks of channels, which share lines of memory where a block has half of one, to the same of
+  // the 8 dies (workgroups go to them in turn), 8 pairs at a time
+  const uint32_t pairs = (uint32_t)((sp.blocks + 1) / 2), per = pairs * (uint32_t)sp.count;
+  const uint32_t q = blockIdx.x / 16 * 8 + blockIdx.x % 8;
+  p.b = q / per;
+  const uint32_t rest = q - (uint32_t)p.b * per;
+  p.span = rest / pairs;
+  const int64_t block = (rest - (uint32_t)p.span * pairs) * 2 + blockIdx.x / 8 % 2;
+  p.none = p.b >= a.batch || block >= sp.blocks;
+  if (p.none) return p;
   p.c = (block * LANES + p.lane % LANES) * 2;
   const int64_t left = a.channels - p.c;
   p.n = left <= 0 ? 0 : left == 1 ? 1 : 2;
@@ -340,6 +358,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_forward_tile(msamp_recurrence a,
   constexpr int R = K::kSteps;
   __shared__ float4 wave_map[2][WAVES][K::kLanes];
   const Place p = place_of<K::kLanes>(a, sp);
+  if (p.none) return;
   const T* x = (const T*)a.x + p.b * a.x_batch;
   const T* g = (const T*)a.gate + p.b * a.gate_batch;
   T* y = PASS == 0 ? (T*)a.y + p.b * a.y_batch : nullptr;
@@ -430,6 +449,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a
   constexpr int R = K::kSteps;
   __shared__ float4 wave_map[2][WAVES][K::kLanes];
   const Place p = place_of<K::kLanes>(a, sp);
+  if (p.none) return;
   const T* x = (const T*)a.x + p.b * a.x_batch;
   const T* g = (const T*)a.gate + p.b * a.gate_batch;
   const T* dy = (const T*)a.dy + p.b * a.dy_batch;
@@ -453,51 +473,58 @@ __global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a
   typename K::raw xr[R], gr[R], dr[R];
   float2 state = make_float2(0.0f, 0.0f);
   auto steps_at = [&](int64_t t) { return t + K::kTile < p.t1 ? (int64_t)K::kTile : p.t1 - t; };
-  auto load = [&](int64_t t) {
-    load_steps<T, R>(buffer_of(g, sg, t, steps_at(t), a.channels), sg, p.odd, p.n, gr);
-    load_steps<T, R>(buffer_of(dy, sd, t, steps_at(t), a.channels), sd, p.odd, p.n, dr);
-    if (PASS == 0) load_steps<T, R>(buffer_of(x, sx, t, steps_at(t), a.channels), sx, p.odd, p.n, xr);
-    if (PASS == 0 && p.n > 0 && t + p.wave * kChunk < p.t1)
+  auto load_state = [&](int64_t t) {
+    if (p.n > 0 && t + p.wave * kChunk < p.t1)
       state = Pair<float>::values(Pair<float>::load(states + (t / kChunk + p.wave) * a.channels, p.n));
   };
   const int64_t tiles = p.t0 < p.t1 ? (p.t1 - p.t0 + K::kTile - 1) / K::kTile : 0;
-  if (tiles > 0) load(p.t0 + (tiles - 1) * K::kTile);
+  if (tiles > 0) {
+    const int64_t t = p.t0 + (tiles - 1) * K::kTile;
+    load_steps<T, R>(buffer_of(g, sg, t, steps_at(t), a.channels), sg, p.odd, p.n, gr);
+    if (PASS == 0) {
+      load_steps<T, R>(buffer_of(x, sx, t, steps_at(t), a.channels), sx, p.odd, p.n, xr);
+      load_state(t);
+    }
+    load_steps<T, R>(buffer_of(dy, sd, t, steps_at(t), a.channels), sd, p.odd, p.n, dr);
+  }
   int turn = 0;
   for (int64_t i = tiles - 1; i >= 0; --i, turn ^= 1) {
     const int64_t t = p.t0 + i * K::kTile, at = t + mine;
-    float2 av[R], keep[R], slope[R], d[R];
+    const bool cut = t + K::kTile > p.t1, more = i > 0;  // steps behind the end leave m and h as they are
+    float2 av[R], keep[R], slope[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      gate2(Pair<T>::values(gr[r]), &av[r], &keep[r]);
-      d[r] = Pair<T>::values(dr[r]);
-      if (PASS == 0) slope[r] = Pair<T>::values(xr[r]);
-    }
-    const float2 first = state;
-    if (i > 0) load(t - K::kTile);
-    if (t + K::kTile > p.t1) {
+    for (int r = 0; r < R; ++r) gate2(Pair<T>::values(gr[r]), &av[r], &keep[r]);
+    if (cut) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if (at + r >= p.t1)
-          av[r] = make_float2(1.0f, 1.0f), keep[r] = d[r] = slope[r] = make_float2(0.0f, 0.0f);
+        if (at + r >= p.t1) av[r] = make_float2(1.0f, 1.0f), keep[r] = make_float2(0.0f, 0.0f);
     }
+    if (more) load_steps<T, R>(buffer_of(g, sg, t - K::kTile, K::kTile, a.channels), sg, p.odd, p.n, gr);
     if (PASS == 0) {
       // h before each step, and dgate's factor (h - x) a (1 - a)
-      Affine f = {av[0], mul2(keep[0], slope[0])}, before, all;
+      Affine f = {av[0], mul2(keep[0], Pair<T>::values(xr[0]))}, before, all;
 #pragma unroll
-      for (int r = 1; r < R; ++r) f = {mul2(f.a, av[r]), fma2(av[r], f.s, mul2(keep[r], slope[r]))};
+      for (int r = 1; r < R; ++r) f = {mul2(f.a, av[r]), fma2(av[r], f.s, mul2(keep[r], Pair<T>::values(xr[r])))};
       join_groups<K::kLanes, true>(p.lane, f, &before, &all);
-      float2 h = apply(before, first);
+      float2 h = apply(before, state);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float2 xv = slope[r];
+        const float2 xv = Pair<T>::values(again(xr[r]));
         slope[r] = mul2(make_float2(h.x - xv.x, h.y - xv.y), mul2(av[r], keep[r]));
+        formed(slope[r]);
         h = fma2(av[r], h, mul2(keep[r], xv));
       }
+      if (more) {
+        load_steps<T, R>(buffer_of(x, sx, t - K::kTile, K::kTile, a.channels), sx, p.odd, p.n, xr);
+        load_state(t - K::kTile);
+      }
     }
-    Affine f = {av[R - 1], mul2(av[R - 1], d[R - 1])}, before, all;
+    Affine f = {av[R - 1], mul2(av[R - 1], Pair<T>::values(again(dr[R - 1])))}, before, all;
 #pragma unroll
-    for (int r = R - 2; r >= 0; --r)
-      f = {mul2(f.a, av[r]), mul2(av[r], make_float2(d[r].x + f.s.x, d[r].y + f.s.y))};
+    for (int r = R - 2; r >= 0; --r) {
+      const float2 d = Pair<T>::values(again(dr[r]));
+      f = {mul2(f.a, av[r]), mul2(av[r], make_float2(d.x + f.s.x, d.y + f.s.y))};
+    }
     join_groups<K::kLanes, false>(p.lane, f, &before, &all);
     if (WAVES > 1) {
       if (p.group == 0) wave_map[turn][p.wave][p.lane] = make_float4(all.a.x, all.a.y, all.s.x, all.s.y);
@@ -519,17 +546,21 @@ __global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a
         m = apply(all, m);
       }
     }
-    if (PASS == 1) continue;
-    float2 v = apply(before, start);
+    if (PASS == 0) {
+      float2 v = apply(before, start);
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-      const float2 l = make_float2(d[r].x + v.x, d[r].y + v.y);
-      keep[r] = mul2(keep[r], l);
-      slope[r] = mul2(slope[r], l);
-      v = mul2(av[r], l);
+      for (int r = R - 1; r >= 0; --r) {
+        const float2 d = Pair<T>::values(again(dr[r])), l = make_float2(d.x + v.x, d.y + v.y);
+        keep[r] = mul2(keep[r], l);
+        slope[r] = mul2(slope[r], l);
+        v = mul2(av[r], l);
+      }
     }
-    store_steps<T, R>(buffer_of(dx, ox, t, steps_at(t), a.channels), ox, p.odd, p.n, keep);
-    store_steps<T, R>(buffer_of(dg, og, t, steps_at(t), a.channels), og, p.odd, p.n, slope);
+    if (more) load_steps<T, R>(buffer_of(dy, sd, t - K::kTile, K::kTile, a.channels), sd, p.odd, p.n, dr);
+    if (PASS == 0) {
+      store_steps<T, R>(buffer_of(dx, ox, t, steps_at(t), a.channels), ox, p.odd, p.n, keep);
+      store_steps<T, R>(buffer_of(dg, og, t, steps_at(t), a.channels), og, p.odd, p.n, slope);
+    }
   }
   if (p.n == 0 || threadIdx.x >= K::kLanes) return;
   if (PASS == 1)
@@ -563,7 +594,8 @@ Spans spans_of(const msamp_recurrence& a, void* ws) {
 
 template <typename T, int WAVES, bool BACKWARD>
 hipError_t tiles(const msamp_recurrence& a, const Spans& sp, hipStream_t s) {
-  const unsigned grid = (unsigned)(sp.blocks * sp.count * a.batch);
+  const int64_t pairs = (sp.blocks + 1) / 2 * sp.count * a.batch;
+  const unsigned grid = (unsigned)((pairs + 7) / 8 * 16);
   if (sp.count > 1) {
     if (BACKWARD) k_backward_tile<T, WAVES, 1><<<grid, 64 * WAVES, 0, s>>>(a, sp);
     else k_forward_tile<T, WAVES, 1><<<grid, 64 * WAVES, 0, s>>>(a, sp);
