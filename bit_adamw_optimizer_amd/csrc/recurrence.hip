@@ -226,22 +226,28 @@ __device__ __forceinline__ Affine shuffle(const Affine& f, int lane) {
   return {shuffle2(f.a, lane), shuffle2(f.s, lane)};
 }
 
+__device__ __forceinline__ float2 pick(bool c, float2 a, float2 b) { return make_float2(c ? a.x : b.x, c ? a.y : b.y); }
+
 // What the groups before (FORWARD: earlier, otherwise later in time) this
 // lane's map a state to, in *before; the whole wave's map in the last group
 // (FORWARD: the highest) of *all.
 template <int LANES, bool FORWARD>
 __device__ __forceinline__ void join_groups(int lane, const Affine& mine, Affine* before, Affine* all) {
-  *all = mine;
-  const Affine same = {make_float2(1.0f, 1.0f), make_float2(0.0f, 0.0f)};
+  Affine sum = mine;
 #pragma unroll
   for (int off = LANES; off < 64; off <<= 1) {
     const int from = FORWARD ? lane - off : lane + off;
-    const Affine f = shuffle(*all, from & 63);
-    if (from >= 0 && from < 64) *all = after(*all, f);
+    const Affine f = shuffle(sum, from & 63), both = after(sum, f);
+    const bool in = from >= 0 && from < 64;
+    sum.a = pick(in, both.a, sum.a);
+    sum.s = pick(in, both.s, sum.s);
   }
   const int from = FORWARD ? lane - LANES : lane + LANES;
-  const Affine f = shuffle(*all, from & 63);
-  *before = from >= 0 && from < 64 ? f : same;
+  const Affine f = shuffle(sum, from & 63);
+  const bool in = from >= 0 && from < 64;
+  before->a = pick(in, f.a, make_float2(1.0f, 1.0f));
+  before->s = pick(in, f.s, make_float2(0.0f, 0.0f));
+  *all = sum;
 }
 
 // A tensor's part of one tile, through a buffer whose bounds end behind its
