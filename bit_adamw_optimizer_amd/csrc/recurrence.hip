@@ -281,13 +281,12 @@ __device__ __forceinline__ u32x2 again(u32x2 v) { return v; }  // binary32: noth
 // Formed here and not where it is used next, behind what it is formed from.
 __device__ __forceinline__ void formed(float2& v) { asm volatile("" : "+v"(v.x), "+v"(v.y)); }
 
-// odd: the block holds the last of an odd number of channels, whose lane
+// ODD: the block holds the last of an odd number of channels, whose lane
 // (n = 1) has no second one.
-template <typename T, int R>
-__device__ __forceinline__ void load_steps(__amdgpu_buffer_rsrc_t b, const Steps& s, bool odd, int n,
-                                           typename Pair<T>::raw* v) {
+template <typename T, int R, bool ODD>
+__device__ __forceinline__ void load_steps(__amdgpu_buffer_rsrc_t b, const Steps& s, int n, typename Pair<T>::raw* v) {
   const uint32_t at = once(s.lane), row = (uint32_t)(s.stride * (int64_t)sizeof(T));
-  if (odd) {
+  if (ODD) {
     const uint32_t second = n > 1 ? at + (uint32_t)sizeof(T) : kOutside;
 #pragma unroll
     for (int r = 0; r < R; ++r) v[r] = Pair<T>::load_each(b, at + r * row, second + r * row);
@@ -296,10 +295,10 @@ __device__ __forceinline__ void load_steps(__amdgpu_buffer_rsrc_t b, const Steps
     for (int r = 0; r < R; ++r) v[r] = Pair<T>::load(b, at + r * row);
   }
 }
-template <typename T, int R>
-__device__ __forceinline__ void store_steps(__amdgpu_buffer_rsrc_t b, const Steps& s, bool odd, int n, const float2* v) {
+template <typename T, int R, bool ODD>
+__device__ __forceinline__ void store_steps(__amdgpu_buffer_rsrc_t b, const Steps& s, int n, const float2* v) {
   const uint32_t at = once(s.lane), row = (uint32_t)(s.stride * (int64_t)sizeof(T));
-  if (odd) {
+  if (ODD) {
     const uint32_t second = n > 1 ? at + (uint32_t)sizeof(T) : kOutside;
 #pragma unroll
     for (int r = 0; r < R; ++r) Pair<T>::store_each(b, at + r * row, second + r * row, v[r]);
@@ -335,7 +334,7 @@ __device__ __forceinline__ Place place_of(const msamp_recurrence& a, const Spans
   const int64_t left = a.channels - p.c;
   p.n = left <= 0 ? 0 : left == 1 ? 1 : 2;
   p.odd = (a.channels & 1) && block == sp.blocks - 1;
-  p.len = length_of(a, p.b);
+  p.len = __builtin_amdgcn_readfirstlane((int)length_of(a, p.b));
   p.t0 = p.span * sp.steps;
   p.t1 = p.t0 + sp.steps < p.len ? p.t0 + sp.steps : p.len;
   return p;
@@ -358,13 +357,11 @@ __device__ __forceinline__ Affine run_of(const float2* av, const float2* bv) {
 }
 
 // PASS 0: y, states and h_last. PASS 1: the spans' maps alone.
-template <typename T, int WAVES, int PASS>
-__global__ __launch_bounds__(64 * WAVES) void k_forward_tile(msamp_recurrence a, Spans sp) {
+template <typename T, int WAVES, int PASS, bool ODD>
+__device__ __forceinline__ void forward_tiles(const msamp_recurrence& a, const Spans& sp, const Place& p,
+                                         float4 (&wave_map)[2][WAVES][lanes_of<T>()]) {
   typedef Tile<T, WAVES> K;
   constexpr int R = K::kSteps;
-  __shared__ float4 wave_map[2][WAVES][K::kLanes];
-  const Place p = place_of<K::kLanes>(a, sp);
-  if (p.none) return;
   const T* x = (const T*)a.x + p.b * a.x_batch;
   const T* g = (const T*)a.gate + p.b * a.gate_batch;
   T* y = PASS == 0 ? (T*)a.y + p.b * a.y_batch : nullptr;
@@ -383,21 +380,24 @@ __global__ __launch_bounds__(64 * WAVES) void k_forward_tile(msamp_recurrence a,
   typename K::raw xr[R], gr[R];
   auto steps_at = [&](int64_t t) { return t + K::kTile < p.t1 ? (int64_t)K::kTile : p.t1 - t; };
   auto load = [&](int64_t t) {
-    load_steps<T, R>(buffer_of(g, sg, t, steps_at(t), a.channels), sg, p.odd, p.n, gr);
-    load_steps<T, R>(buffer_of(x, sx, t, steps_at(t), a.channels), sx, p.odd, p.n, xr);
+    load_steps<T, R, ODD>(buffer_of(g, sg, t, steps_at(t), a.channels), sg, p.n, gr);
+    load_steps<T, R, ODD>(buffer_of(x, sx, t, steps_at(t), a.channels), sx, p.n, xr);
   };
   if (p.t0 < p.t1) load(p.t0);
   int turn = 0;
   for (int64_t t = p.t0; t < p.t1; t += K::kTile, turn ^= 1) {
     const int64_t at = t + mine;
+    typename K::raw xc[R], gc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) xc[r] = xr[r], gc[r] = gr[r];
+    if (t + K::kTile < p.t1) load(t + K::kTile);
     float2 av[R], bv[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 keep;
-      gate2(Pair<T>::values(gr[r]), &av[r], &keep);
-      bv[r] = mul2(keep, Pair<T>::values(xr[r]));
+      gate2(Pair<T>::values(gc[r]), &av[r], &keep);
+      bv[r] = mul2(keep, Pair<T>::values(xc[r]));
     }
-    if (t + K::kTile < p.t1) load(t + K::kTile);
     if (t + K::kTile > p.t1) {  // steps behind the end keep the state
 #pragma unroll
       for (int r = 0; r < R; ++r)
@@ -437,7 +437,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_forward_tile(msamp_recurrence a,
       v = fma2(av[r], v, bv[r]);
       bv[r] = v;
     }
-    store_steps<T, R>(buffer_of(y, sy, t, steps_at(t), a.channels), sy, p.odd, p.n, bv);
+    store_steps<T, R, ODD>(buffer_of(y, sy, t, steps_at(t), a.channels), sy, p.n, bv);
   }
   if (p.n == 0 || threadIdx.x >= K::kLanes) return;
   if (PASS == 1) {
@@ -447,15 +447,22 @@ __global__ __launch_bounds__(64 * WAVES) void k_forward_tile(msamp_recurrence a,
   }
 }
 
+template <typename T, int WAVES, int PASS>
+__global__ __launch_bounds__(64 * WAVES) void k_forward_tile(msamp_recurrence a, Spans sp) {
+  __shared__ float4 wave_map[2][WAVES][lanes_of<T>()];
+  const Place p = place_of<lanes_of<T>()>(a, sp);
+  if (p.none) return;
+  if (p.odd) forward_tiles<T, WAVES, PASS, true>(a, sp, p, wave_map);
+  else forward_tiles<T, WAVES, PASS, false>(a, sp, p, wave_map);
+}
+
 // Backward in time, m_t = a_t l_t = a_t (dy_t + m_{t+1}); h again from the
 // state before each wave's chunk. PASS 1: the spans' maps of m alone.
-template <typename T, int WAVES, int PASS>
-__global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a, Spans sp) {
+template <typename T, int WAVES, int PASS, bool ODD>
+__device__ __forceinline__ void backward_tiles(const msamp_recurrence& a, const Spans& sp, const Place& p,
+                                         float4 (&wave_map)[2][WAVES][lanes_of<T>()]) {
   typedef Tile<T, WAVES> K;
   constexpr int R = K::kSteps;
-  __shared__ float4 wave_map[2][WAVES][K::kLanes];
-  const Place p = place_of<K::kLanes>(a, sp);
-  if (p.none) return;
   const T* x = (const T*)a.x + p.b * a.x_batch;
   const T* g = (const T*)a.gate + p.b * a.gate_batch;
   const T* dy = (const T*)a.dy + p.b * a.dy_batch;
@@ -486,26 +493,29 @@ __global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a
   const int64_t tiles = p.t0 < p.t1 ? (p.t1 - p.t0 + K::kTile - 1) / K::kTile : 0;
   if (tiles > 0) {
     const int64_t t = p.t0 + (tiles - 1) * K::kTile;
-    load_steps<T, R>(buffer_of(g, sg, t, steps_at(t), a.channels), sg, p.odd, p.n, gr);
+    load_steps<T, R, ODD>(buffer_of(g, sg, t, steps_at(t), a.channels), sg, p.n, gr);
     if (PASS == 0) {
-      load_steps<T, R>(buffer_of(x, sx, t, steps_at(t), a.channels), sx, p.odd, p.n, xr);
+      load_steps<T, R, ODD>(buffer_of(x, sx, t, steps_at(t), a.channels), sx, p.n, xr);
       load_state(t);
     }
-    load_steps<T, R>(buffer_of(dy, sd, t, steps_at(t), a.channels), sd, p.odd, p.n, dr);
+    load_steps<T, R, ODD>(buffer_of(dy, sd, t, steps_at(t), a.channels), sd, p.n, dr);
   }
   int turn = 0;
   for (int64_t i = tiles - 1; i >= 0; --i, turn ^= 1) {
     const int64_t t = p.t0 + i * K::kTile, at = t + mine;
     const bool cut = t + K::kTile > p.t1, more = i > 0;  // steps behind the end leave m and h as they are
     float2 av[R], keep[R], slope[R];
+    typename K::raw gc[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) gate2(Pair<T>::values(gr[r]), &av[r], &keep[r]);
+    for (int r = 0; r < R; ++r) gc[r] = gr[r];
+    if (more) load_steps<T, R, ODD>(buffer_of(g, sg, t - K::kTile, K::kTile, a.channels), sg, p.n, gr);
+#pragma unroll
+    for (int r = 0; r < R; ++r) gate2(Pair<T>::values(gc[r]), &av[r], &keep[r]);
     if (cut) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
         if (at + r >= p.t1) av[r] = make_float2(1.0f, 1.0f), keep[r] = make_float2(0.0f, 0.0f);
     }
-    if (more) load_steps<T, R>(buffer_of(g, sg, t - K::kTile, K::kTile, a.channels), sg, p.odd, p.n, gr);
     if (PASS == 0) {
       // h before each step, and dgate's factor (h - x) a (1 - a)
       Affine f = {av[0], mul2(keep[0], Pair<T>::values(xr[0]))}, before, all;
@@ -521,7 +531,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a
         h = fma2(av[r], h, mul2(keep[r], xv));
       }
       if (more) {
-        load_steps<T, R>(buffer_of(x, sx, t - K::kTile, K::kTile, a.channels), sx, p.odd, p.n, xr);
+        load_steps<T, R, ODD>(buffer_of(x, sx, t - K::kTile, K::kTile, a.channels), sx, p.n, xr);
         load_state(t - K::kTile);
       }
     }
@@ -562,10 +572,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a
         v = mul2(av[r], l);
       }
     }
-    if (more) load_steps<T, R>(buffer_of(dy, sd, t - K::kTile, K::kTile, a.channels), sd, p.odd, p.n, dr);
+    if (more) load_steps<T, R, ODD>(buffer_of(dy, sd, t - K::kTile, K::kTile, a.channels), sd, p.n, dr);
     if (PASS == 0) {
-      store_steps<T, R>(buffer_of(dx, ox, t, steps_at(t), a.channels), ox, p.odd, p.n, keep);
-      store_steps<T, R>(buffer_of(dg, og, t, steps_at(t), a.channels), og, p.odd, p.n, slope);
+      store_steps<T, R, ODD>(buffer_of(dx, ox, t, steps_at(t), a.channels), ox, p.n, keep);
+      store_steps<T, R, ODD>(buffer_of(dg, og, t, steps_at(t), a.channels), og, p.n, slope);
     }
   }
   if (p.n == 0 || threadIdx.x >= K::kLanes) return;
@@ -573,6 +583,15 @@ __global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a
     sp.joined[(p.b * sp.count + p.span) * sp.pairs + p.c / 2] = make_float4(total.a.x, total.a.y, total.s.x, total.s.y);
   else if (a.dh0 != nullptr && p.span == 0)
     Pair<float>::store(a.dh0 + p.b * a.ld_dh0 + p.c, p.n, m);
+}
+
+template <typename T, int WAVES, int PASS>
+__global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a, Spans sp) {
+  __shared__ float4 wave_map[2][WAVES][lanes_of<T>()];
+  const Place p = place_of<lanes_of<T>()>(a, sp);
+  if (p.none) return;
+  if (p.odd) backward_tiles<T, WAVES, PASS, true>(a, sp, p, wave_map);
+  else backward_tiles<T, WAVES, PASS, false>(a, sp, p, wave_map);
 }
 
 constexpr int64_t kFewSteps = 8;      // up to which a lane goes through them alone
