@@ -377,6 +377,7 @@ __device__ __forceinline__ void forward_tiles(const msamp_recurrence& a, const S
       h = fma2(make_float2(f.x, f.y), h, make_float2(f.z, f.w));
     }
   }
+  formed(h);  // waited for here: in the loop that would wait for the next tile's loads too
   typename K::raw xr[R], gr[R];
   auto steps_at = [&](int64_t t) { return t + K::kTile < p.t1 ? (int64_t)K::kTile : p.t1 - t; };
   auto load = [&](int64_t t) {
@@ -483,6 +484,7 @@ __device__ __forceinline__ void backward_tiles(const msamp_recurrence& a, const 
       m = fma2(make_float2(f.x, f.y), m, make_float2(f.z, f.w));
     }
   }
+  formed(m);
   typename K::raw xr[R], gr[R], dr[R];
   float2 state = make_float2(0.0f, 0.0f);
   auto steps_at = [&](int64_t t) { return t + K::kTile < p.t1 ? (int64_t)K::kTile : p.t1 - t; };
