@@ -14,10 +14,7 @@ namespace msamp {
 namespace {
 
 constexpr int kChunk = MSAMP_RECURRENCE_CHUNK;
-#ifndef KL16
-#define KL16 32
-#endif
-constexpr int kLanes16 = KL16;
+constexpr int kPastCaches = 2;  // nt
 
 // Two consecutive channels as they lie in memory; n (1 or 2) of them are the
 // tensor's.
@@ -44,7 +41,7 @@ struct Pair<float> {
     return raw{__builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0), __builtin_amdgcn_raw_buffer_load_b32(b, second, 0, 0)};
   }
   static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, uint32_t at, float2 v) {
-    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v.x), __float_as_uint(v.y)}, b, at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v.x), __float_as_uint(v.y)}, b, at, 0, kPastCaches);
   }
   static __device__ __forceinline__ void store_each(__amdgpu_buffer_rsrc_t b, uint32_t at, uint32_t second, float2 v) {
     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v.x), b, at, 0, 0);
@@ -80,7 +77,7 @@ struct Pair {
            (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, second, 0, 0) << 16;
   }
   static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, uint32_t at, float2 v) {
-    __builtin_amdgcn_raw_buffer_store_b32(packed(v), b, at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(packed(v), b, at, 0, kPastCaches);
   }
   static __device__ __forceinline__ void store_each(__amdgpu_buffer_rsrc_t b, uint32_t at, uint32_t second, float2 v) {
     const uint32_t q = packed(v);
@@ -209,7 +206,7 @@ struct Spans {
 
 template <typename T>
 constexpr int lanes_of() {
-  return sizeof(T) == 2 ? kLanes16 : 16;
+  return sizeof(T) == 2 ? 32 : 16;  // 128 bytes of a step
 }
 
 struct Affine {  // v -> a v + s
@@ -311,7 +308,7 @@ __device__ __forceinline__ void store_steps(__amdgpu_buffer_rsrc_t b, const Step
 // Place of a workgroup: block of channels, sequence, span.
 struct Place {
   int lane, wave, group, n;
-  bool odd, none;
+  bool odd;
   int64_t b, c, span, len, t0, t1;  // steps [t0, t1) of the span
 };
 template <int LANES>
@@ -320,16 +317,11 @@ __device__ __forceinline__ Place place_of(const msamp_recurrence& a, const Spans
   p.lane = threadIdx.x & 63;
   p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   p.group = p.lane / LANES;
-  // neighbouring blocks of channels, which share lines of memory where a block has half of one, to the same of
-  // the 8 dies (workgroups go to them in turn), 8 pairs at a time
-  const uint32_t pairs = (uint32_t)((sp.blocks + 1) / 2), per = pairs * (uint32_t)sp.count;
-  const uint32_t q = blockIdx.x / 16 * 8 + blockIdx.x % 8;
-  p.b = q / per;
-  const uint32_t rest = q - (uint32_t)p.b * per;
-  p.span = rest / pairs;
-  const int64_t block = (rest - (uint32_t)p.span * pairs) * 2 + blockIdx.x / 8 % 2;
-  p.none = p.b >= a.batch || block >= sp.blocks;
-  if (p.none) return p;
+  const uint32_t per = (uint32_t)(sp.blocks * sp.count);
+  p.b = blockIdx.x / per;
+  const uint32_t rest = blockIdx.x - (uint32_t)p.b * per;
+  p.span = rest / (uint32_t)sp.blocks;
+  const int64_t block = rest - (uint32_t)p.span * (uint32_t)sp.blocks;
   p.c = (block * LANES + p.lane % LANES) * 2;
   const int64_t left = a.channels - p.c;
   p.n = left <= 0 ? 0 : left == 1 ? 1 : 2;
@@ -452,7 +444,6 @@ template <typename T, int WAVES, int PASS>
 __global__ __launch_bounds__(64 * WAVES) void k_forward_tile(msamp_recurrence a, Spans sp) {
   __shared__ float4 wave_map[2][WAVES][lanes_of<T>()];
   const Place p = place_of<lanes_of<T>()>(a, sp);
-  if (p.none) return;
   if (p.odd) forward_tiles<T, WAVES, PASS, true>(a, sp, p, wave_map);
   else forward_tiles<T, WAVES, PASS, false>(a, sp, p, wave_map);
 }
@@ -591,13 +582,13 @@ template <typename T, int WAVES, int PASS>
 __global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a, Spans sp) {
   __shared__ float4 wave_map[2][WAVES][lanes_of<T>()];
   const Place p = place_of<lanes_of<T>()>(a, sp);
-  if (p.none) return;
   if (p.odd) backward_tiles<T, WAVES, PASS, true>(a, sp, p, wave_map);
   else backward_tiles<T, WAVES, PASS, false>(a, sp, p, wave_map);
 }
 
 constexpr int64_t kFewSteps = 8;      // up to which a lane goes through them alone
 constexpr int64_t kEnoughGroups = 192;  // workgroups from which sequences are left whole
+constexpr int64_t kSpanGroups = 256;    // of sequences that are cut
 constexpr int64_t kMostSpans = 64;
 
 int waves_of(int64_t time) { return time <= kChunk ? 1 : time <= 2 * kChunk ? 2 : time <= 4 * kChunk ? 4 : 8; }
@@ -609,7 +600,7 @@ Spans spans_of(const msamp_recurrence& a, void* ws) {
   s.blocks = (s.pairs + lanes - 1) / lanes;
   const int64_t tile = kChunk * waves_of(a.time), tiles = (a.time + tile - 1) / tile;
   const int64_t groups = s.blocks * a.batch;
-  int64_t count = groups >= kEnoughGroups ? 1 : (256 + groups - 1) / groups;
+  int64_t count = groups >= kEnoughGroups ? 1 : (kSpanGroups + groups - 1) / groups;
   if (count > kMostSpans) count = kMostSpans;
   if (count > tiles) count = tiles;
   const int64_t each = (tiles + count - 1) / count;
@@ -621,8 +612,7 @@ Spans spans_of(const msamp_recurrence& a, void* ws) {
 
 template <typename T, int WAVES, bool BACKWARD>
 hipError_t tiles(const msamp_recurrence& a, const Spans& sp, hipStream_t s) {
-  const int64_t pairs = (sp.blocks + 1) / 2 * sp.count * a.batch;
-  const unsigned grid = (unsigned)((pairs + 7) / 8 * 16);
+  const unsigned grid = (unsigned)(sp.blocks * sp.count * a.batch);
   if (sp.count > 1) {
     if (BACKWARD) k_backward_tile<T, WAVES, 1><<<grid, 64 * WAVES, 0, s>>>(a, sp);
     else k_forward_tile<T, WAVES, 1><<<grid, 64 * WAVES, 0, s>>>(a, sp);
