@@ -308,7 +308,7 @@ __device__ __forceinline__ void store_steps(__amdgpu_buffer_rsrc_t b, const Step
 // Place of a workgroup: block of channels, sequence, span.
 struct Place {
   int lane, wave, group, n;
-  bool odd;
+  bool odd, none;
   int64_t b, c, span, len, t0, t1;  // steps [t0, t1) of the span
 };
 template <int LANES>
@@ -317,9 +317,13 @@ __device__ __forceinline__ Place place_of(const msamp_recurrence& a, const Spans
   p.lane = threadIdx.x & 63;
   p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   p.group = p.lane / LANES;
-  const uint32_t per = (uint32_t)(sp.blocks * sp.count);
-  p.b = blockIdx.x / per;
-  const uint32_t rest = blockIdx.x - (uint32_t)p.b * per;
+  // workgroups go to the 8 dies in turn: neighbouring blocks to one of them, whose cache then has both halves of a
+  // line that they share (rows that do not start on 128 bytes)
+  const uint32_t i = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8, per = (uint32_t)(sp.blocks * sp.count);
+  p.b = i / per;
+  p.none = p.b >= a.batch;
+  if (p.none) return p;
+  const uint32_t rest = i - (uint32_t)p.b * per;
   p.span = rest / (uint32_t)sp.blocks;
   const int64_t block = rest - (uint32_t)p.span * (uint32_t)sp.blocks;
   p.c = (block * LANES + p.lane % LANES) * 2;
@@ -444,6 +448,7 @@ template <typename T, int WAVES, int PASS>
 __global__ __launch_bounds__(64 * WAVES) void k_forward_tile(msamp_recurrence a, Spans sp) {
   __shared__ float4 wave_map[2][WAVES][lanes_of<T>()];
   const Place p = place_of<lanes_of<T>()>(a, sp);
+  if (p.none) return;
   if (p.odd) forward_tiles<T, WAVES, PASS, true>(a, sp, p, wave_map);
   else forward_tiles<T, WAVES, PASS, false>(a, sp, p, wave_map);
 }
@@ -582,6 +587,7 @@ template <typename T, int WAVES, int PASS>
 __global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a, Spans sp) {
   __shared__ float4 wave_map[2][WAVES][lanes_of<T>()];
   const Place p = place_of<lanes_of<T>()>(a, sp);
+  if (p.none) return;
   if (p.odd) backward_tiles<T, WAVES, PASS, true>(a, sp, p, wave_map);
   else backward_tiles<T, WAVES, PASS, false>(a, sp, p, wave_map);
 }
@@ -612,7 +618,7 @@ Spans spans_of(const msamp_recurrence& a, void* ws) {
 
 template <typename T, int WAVES, bool BACKWARD>
 hipError_t tiles(const msamp_recurrence& a, const Spans& sp, hipStream_t s) {
-  const unsigned grid = (unsigned)(sp.blocks * sp.count * a.batch);
+  const unsigned grid = (unsigned)((sp.blocks * sp.count * a.batch + 7) / 8 * 8);
   if (sp.count > 1) {
     if (BACKWARD) k_backward_tile<T, WAVES, 1><<<grid, 64 * WAVES, 0, s>>>(a, sp);
     else k_forward_tile<T, WAVES, 1><<<grid, 64 * WAVES, 0, s>>>(a, sp);
