@@ -10,7 +10,7 @@ namespace msamp {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int64_t kMaxGroups = 1 << 20;  // workgroups of a launch; they walk over the rest
+constexpr int64_t kMaxGroups = 1 << 20;  // workgroups of a launch
 
 // --------------------------------------------------------------- lookup ---
 
@@ -334,11 +334,11 @@ __global__ __launch_bounds__(kBlock) void k_pieces(EmbeddingArgs a, Sorted s, in
 // are found from sorted rows that are the first of their id, so that ids of no
 // row (which accumulating leaves alone) are not looked at.
 template <typename T, int LANES, int CH, bool BY_ROW>
-__global__ __launch_bounds__(kBlock) void k_embedding_backward(EmbeddingArgs a, Sorted s, int64_t piece) {
+__global__ __launch_bounds__(kBlock) void k_embedding_backward(EmbeddingArgs a, Sorted s, int64_t piece, int64_t group0) {
   constexpr int kRows = kBlock / LANES, kStep = LANES * 4;
   constexpr bool kWave = LANES >= 64;
   const int lane = threadIdx.x % LANES;
-  int64_t v = (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
+  int64_t v = (group0 + blockIdx.x) * kRows + threadIdx.x / LANES;
   if (BY_ROW) {
     if (v >= a.rows) return;
     const int64_t total = s.first[a.vocab];
@@ -420,12 +420,15 @@ hipError_t backward(const EmbeddingArgs& a, void* ws, hipStream_t s) {
   }
   auto run = [&](auto lanes, auto chunks) -> hipError_t {
     constexpr int L = decltype(lanes)::value, CH = decltype(chunks)::value, R = kBlock / L;
-    if (a.accumulate) {
-      if (a.rows > 0) k_embedding_backward<T, L, CH, true><<<(unsigned)((a.rows + R - 1) / R), kBlock, 0, s>>>(a, st, piece);
-    } else {
-      k_embedding_backward<T, L, CH, false><<<(unsigned)((a.vocab + R - 1) / R), kBlock, 0, s>>>(a, st, piece);
+    const int64_t groups = ((a.accumulate ? a.rows : a.vocab) + R - 1) / R;
+    for (int64_t g = 0; g < groups; g += kMaxGroups) {
+      const unsigned n = (unsigned)(groups - g < kMaxGroups ? groups - g : kMaxGroups);
+      if (a.accumulate) k_embedding_backward<T, L, CH, true><<<n, kBlock, 0, s>>>(a, st, piece, g);
+      else k_embedding_backward<T, L, CH, false><<<n, kBlock, 0, s>>>(a, st, piece, g);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
   };
   const int64_t units = (a.cols + 3) / 4;
   using std::integral_constant;

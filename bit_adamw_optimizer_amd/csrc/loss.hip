@@ -412,7 +412,9 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
         if (first && lane == 0) a.loss[row] = tau * tau * loss;
         at = (__builtin_amdgcn_exp2f(zv * scale) * inv - mine * teacher_inv) * c;
       }
-      if (NCH == 0 && a.dlogits != nullptr) __syncthreads();  // these logits are read before the gradient is written
+      // these logits are read before the gradient, which may go over them, is written (the barrier of the sums does
+      // where they are formed here, and parts have them from the first launch)
+      if (FROM == kGivenSums && kWaves > 1) __syncthreads();
     } else {
       const float log_teacher = teacher[0], inv_teacher = teacher[1];
       float loss = 0.0f;

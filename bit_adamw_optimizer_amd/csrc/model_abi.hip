@@ -119,7 +119,8 @@ msamp_status check_loss(const msamp_vocab_loss* a, bool policy, bool backward) {
   if (a == nullptr) return invalid("args is NULL");
   const int64_t R = a->rows, V = a->vocab;
   if (R < 0 || V < 0) return invalid("a size is negative");
-  if (R > kMaxInt || V > kMaxInt) return invalid("a size exceeds 2^31 - 1");
+  if (R > kMaxInt) return invalid("rows exceeds 2^31 - 1");
+  if (V > MSAMP_LOSS_MAX_VOCAB) return invalid("vocab exceeds 2^29");
   MSAMP_TRY(check_dtype(a->dtype, "dtype"));
   MSAMP_TRY(check_int_bytes(a->id_bytes, "id_bytes"));
   const float tau = (float)a->temperature, inv = (float)(1.0 / a->temperature);

@@ -200,6 +200,7 @@ struct Spans {
   int32_t count;
   int32_t run;     // neighbouring blocks on a die
   float4* joined;  // [batch][count][pairs]: (A, S) of each span
+  float2* first;   // [batch][pairs]: the state before all spans, which the last state may go over
   int64_t pairs;
 };
 
@@ -375,7 +376,10 @@ __device__ __forceinline__ void forward_tiles(const msamp_recurrence& a, const S
   Affine total = {make_float2(1.0f, 1.0f), make_float2(0.0f, 0.0f)};
   float2 h = make_float2(0.0f, 0.0f);
   if (PASS == 0 && p.n > 0) {
-    if (a.h0 != nullptr) h = Pair<float>::values(Pair<float>::load(a.h0 + p.b * a.ld_h0 + p.c, p.n));
+    if (a.h0 != nullptr) {
+      if (sp.count > 1) h = sp.first[p.b * sp.pairs + p.c / 2];
+      else h = Pair<float>::values(Pair<float>::load(a.h0 + p.b * a.ld_h0 + p.c, p.n));
+    }
     for (int64_t s = 0; s < p.span; ++s) {
       const float4 f = sp.joined[(p.b * sp.count + s) * sp.pairs + p.c / 2];
       h = fma2(make_float2(f.x, f.y), h, make_float2(f.z, f.w));
@@ -447,6 +451,8 @@ __device__ __forceinline__ void forward_tiles(const msamp_recurrence& a, const S
   if (p.n == 0 || threadIdx.x >= K::kLanes) return;
   if (PASS == 1) {
     sp.joined[(p.b * sp.count + p.span) * sp.pairs + p.c / 2] = make_float4(total.a.x, total.a.y, total.s.x, total.s.y);
+    if (p.span == 0 && a.h0 != nullptr)
+      sp.first[p.b * sp.pairs + p.c / 2] = Pair<float>::values(Pair<float>::load(a.h0 + p.b * a.ld_h0 + p.c, p.n));
   } else if (a.h_last != nullptr && (p.len == 0 ? p.span == 0 : p.t0 < p.len && p.len <= p.t0 + sp.steps)) {
     Pair<float>::store(a.h_last + p.b * a.ld_h_last + p.c, p.n, h);
   }
@@ -481,7 +487,10 @@ __device__ __forceinline__ void backward_tiles(const msamp_recurrence& a, const 
   Affine total = {make_float2(1.0f, 1.0f), make_float2(0.0f, 0.0f)};
   float2 m = make_float2(0.0f, 0.0f);
   if (PASS == 0 && p.n > 0) {
-    if (a.dh_last != nullptr) m = Pair<float>::values(Pair<float>::load(a.dh_last + p.b * a.ld_dh_last + p.c, p.n));
+    if (a.dh_last != nullptr) {
+      if (sp.count > 1) m = sp.first[p.b * sp.pairs + p.c / 2];
+      else m = Pair<float>::values(Pair<float>::load(a.dh_last + p.b * a.ld_dh_last + p.c, p.n));
+    }
     const int64_t last = (p.len + sp.steps - 1) / sp.steps - 1;  // the span with the last step
     for (int64_t s = last; s > p.span; --s) {
       const float4 f = sp.joined[(p.b * sp.count + s) * sp.pairs + p.c / 2];
@@ -585,9 +594,12 @@ __device__ __forceinline__ void backward_tiles(const msamp_recurrence& a, const 
     }
   }
   if (p.n == 0 || threadIdx.x >= K::kLanes) return;
-  if (PASS == 1)
+  if (PASS == 1) {
     sp.joined[(p.b * sp.count + p.span) * sp.pairs + p.c / 2] = make_float4(total.a.x, total.a.y, total.s.x, total.s.y);
-  else if (a.dh0 != nullptr && p.span == 0)
+    if (p.span == 0 && a.dh_last != nullptr)
+      sp.first[p.b * sp.pairs + p.c / 2] =
+          Pair<float>::values(Pair<float>::load(a.dh_last + p.b * a.ld_dh_last + p.c, p.n));
+  } else if (a.dh0 != nullptr && p.span == 0)
     Pair<float>::store(a.dh0 + p.b * a.ld_dh0 + p.c, p.n, m);
 }
 
@@ -637,6 +649,7 @@ Spans spans_of(const msamp_recurrence& a, void* ws, bool backward) {
   const int64_t all = s.blocks * s.count * a.batch;
   s.run = whole_lines(a, backward) ? 4 : (int32_t)((all + 7) / 8);
   s.joined = (float4*)ws;
+  s.first = (float2*)(s.joined + a.batch * s.count * s.pairs);
   return s;
 }
 
@@ -689,7 +702,7 @@ hipError_t run(const msamp_recurrence& a, void* ws, hipStream_t s) {
 int64_t recurrence_workspace(const msamp_recurrence& a, bool backward) {
   if (a.batch == 0 || a.channels == 0 || lane_alone(a, backward)) return 0;
   const Spans s = spans_of(a, nullptr, backward);
-  return s.count > 1 ? a.batch * s.count * s.pairs * (int64_t)sizeof(float4) : 0;
+  return s.count > 1 ? a.batch * s.pairs * (s.count * (int64_t)sizeof(float4) + (int64_t)sizeof(float2)) : 0;
 }
 
 hipError_t launch_recurrence_forward(const msamp_recurrence& a, void* ws, hipStream_t s) {

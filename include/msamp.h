@@ -736,7 +736,8 @@ msamp_status msamp_embedding_backward(int64_t rows, int64_t vocab, int64_t cols,
  * (1 - a_t is formed as 1 / (1 + e^gate_t), so that it keeps its digits where
  * the gate is nearly open); y, dx and dgate are rounded once to dtype. Long
  * sequences are cut into spans that are worked on at the same time and joined,
- * so the order of the operations depends on the sizes, and on nothing else.
+ * so the order of the operations depends on the sizes, and on nothing else (an
+ * infinite state may become NaN where spans are joined: 0 times Inf).
  *
  * x, gate, y, dy, dx, dgate are [batch, time, channels] of dtype, a channel's
  * elements of one step consecutive, *_batch and *_time the distances between
@@ -847,9 +848,10 @@ msamp_status msamp_recurrence_backward(const msamp_recurrence* args, void* works
  *              matrix)
  *   dloss      device float[rows], the gradient of each row's loss; NULL: 1.
  *              Not read without dlogits
- * vocab, rows <= 2^31 - 1. Fields of the other loss are not read.
+ * vocab <= 2^29. Fields of the other loss are not read.
  */
 #define MSAMP_DISTILL_MAX_TOP 1024
+#define MSAMP_LOSS_MAX_VOCAB (1 << 29)
 typedef struct {
   int64_t rows, vocab;
   msamp_dtype dtype;

@@ -57,6 +57,9 @@ def check_distill(z, ids, t, tau, dloss=None):
     inplace = z.clone()
     M.distill_loss_forward(inplace, ids, t, both, temperature=tau, dlogits=inplace, dloss=dloss)
     near(val, err, {"loss": both, "dlogits": inplace})
+    inplace = z.clone()
+    M.distill_loss_backward(dloss, inplace, ids, t, stats, inplace, temperature=tau)
+    near(val, err, {"dlogits": inplace})
     return loss, stats, dz
 
 
@@ -179,6 +182,9 @@ def check_policy(z, act, old, adv, tau, ref=None, kl=0.0, low=0.2, high=0.2, dlo
     inplace = z.clone()
     M.policy_loss_forward(inplace, act, old, adv, both, dlogits=inplace, dloss=dloss, **kw)
     near(val, err, {"loss": both, "dlogits": inplace})
+    inplace = z.clone()
+    M.policy_loss_backward(dloss, inplace, act, old, adv, stats, inplace, **kw)
+    near(val, err, {"dlogits": inplace})
     return loss, logp, stats, dz
 
 

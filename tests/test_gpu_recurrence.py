@@ -229,6 +229,36 @@ def test_sequences_in_two_calls():
         R.assert_near(got, val[name], err[name], name)
 
 
+@pytest.mark.parametrize("shape", [(2, 5000, 70), (1, 9001, 600)])
+def test_states_in_place_of_sequences_in_spans(shape):
+    """The last state over the first one while other spans still start from it."""
+    b, t, c = shape
+    x, g, dy = (cube(shape, torch.float16, i, offset=i % 2) for i in (1, 2, 3))
+    h0 = torch.linspace(-3, 3, b * c).view(b, c).cuda()
+    y, y2, st = torch.empty_like(x), torch.empty_like(x), M.new_recurrence_states(*shape)
+    last, h = torch.empty_like(h0), h0.clone()
+    M.recurrence_forward(x, g, y, h0=h0, h_last=last, states=st)
+    M.recurrence_forward(x, g, y2, h0=h, h_last=h)
+    assert torch.equal(h, last) and torch.equal(y, y2)
+    outs = [torch.empty_like(x) for _ in range(4)]
+    dh0, d = torch.empty_like(h0), h0.clone()
+    M.recurrence_backward(dy, x, g, st, outs[0], outs[1], dh_last=h0, dh0=dh0)
+    M.recurrence_backward(dy, x, g, st, outs[2], outs[3], dh_last=d, dh0=d)
+    assert torch.equal(d, dh0) and torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("channels", [1, 3, 63, 65, 127, 129])
+def test_odd_channels_in_place(channels, dtype):
+    """The last channel's lane reads its neighbour's too, and writes its own alone."""
+    shape = (2, 300, channels)
+    x, g = cube(shape, DT[dtype], 1, pad=1), cube(shape, DT[dtype], 2)
+    y = torch.empty(shape, dtype=DT[dtype], device="cuda")
+    M.recurrence_forward(x, g, y)
+    M.recurrence_forward(x, g, x)
+    assert torch.equal(x, y)
+
+
 def test_empty_sizes():
     h0 = torch.ones(2, 3, device="cuda")
     h = torch.zeros(2, 3, device="cuda")

@@ -151,7 +151,7 @@ def test_losses_refuse(which):
     assert getattr(M.lib(), "msamp_%s_backward" % which)(None, None) == 1
     W = getattr(M.lib(), "msamp_%s_forward_workspace" % which)
     assert W(None) == -1 and W(ctypes.byref(_loss())) >= 0
-    for bad in (dict(rows=-1), dict(vocab=-1), dict(rows=1 << 31), dict(vocab=1 << 31), dict(dtype=3), dict(id_bytes=1),
+    for bad in (dict(rows=-1), dict(vocab=-1), dict(rows=1 << 31), dict(vocab=(1 << 29) + 1), dict(dtype=3), dict(id_bytes=1),
                 dict(temperature=0.0), dict(temperature=-1.0), dict(temperature=float("nan")), dict(temperature=1e39),
                 dict(temperature=1e-39), dict(logits=0), dict(ids=0), dict(ld_logits=-1), dict(ld_dlogits=99)):
         for back in (False, True):
