@@ -247,13 +247,22 @@ struct Entries {
 };
 
 // One workgroup of BLOCK threads to a row, or to a part of one, of which each
-// thread holds NCH pieces of 8 logits in registers from the sums to the
-// gradient, so that the row is read once. NCH 0: rows of any length.
+// thread holds NCH pieces in registers from the sums to the gradient, so that
+// the row is read once. NCH 0: rows of any length.
 //
-// Bound by memory where the arithmetic hides behind it: two exponentials and
-// about ten other operations a logit are 60% of the vector units' time at the
-// rate of the memory. The first wave alone has the entries; what it needs of
-// memory is under way before the row is.
+// Bound by memory: 8,192 x 32,000 bfloat16 logits with their gradient, 1.05 GB,
+// take 185 us (5.7 TB/s), 4,096 x 50,257 147 us, the gradient alone of 500 x
+// 131,072 binary32 97 us (5.4 TB/s); three passes over the row in memory took
+// 366 us for the first. The arithmetic, two exponentials and about ten other
+// operations a logit, is 60% of the vector units' time at that rate, so several
+// rows have to be in different stages on a compute unit: that takes few
+// registers (64 for 32,000 16-bit logits, four workgroups a compute unit), for
+// which there is no loop over rows (its constants would stay in registers: 112)
+// and the logits are unpacked again in each pass (145). Rows that start
+// anywhere are cut at their first 16 bytes (4,096 x 50,257: 178 us from the
+// row's start). Logits and gradient bypass the caches (without that on the
+// loads 200 us). The first wave alone has the entries; what it needs of memory
+// is under way before the row is.
 template <typename T, int KIND, int FROM, int BLOCK, int NCH>
 __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
   constexpr int kWaves = BLOCK / 64;

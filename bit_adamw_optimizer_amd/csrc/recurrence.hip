@@ -191,9 +191,20 @@ __global__ __launch_bounds__(kBlock) void k_backward_lane(msamp_recurrence a, in
 // then go through their steps with the state they start from. The next tile's
 // loads are under way meanwhile.
 //
+// Bound by memory: 4 x 4,096 steps of 4,096 bfloat16 channels take 72 us
+// forward (411 MB, 5.7 TB/s) and 135 us backward (679 MB, 5.0 TB/s; x, gate and
+// dy are read once, h comes from the saved states); a lane that goes through
+// all steps alone takes 2,627 and 5,664 us. A tile's loads have to be under way
+// for the whole of the tile before it: nothing in the loop may wait for memory
+// (a state loaded before the loop is waited for there, no value goes through
+// scratch, the odd channel's block has a loop of its own), and the two channels
+// of a 16-bit step share a register until they are used. 16 waves, or 32
+// channels to a workgroup and twice the workgroups, were slower (99 us forward).
+//
 // Where batch and channels alone give too few workgroups, sequences are cut
 // into spans: a first launch forms each span's (A, S), and each workgroup of
-// the second joins those before its own.
+// the second joins those before its own. 1 x 16,384 x 2,048: 25 + 35 us forward
+// and 25 + 56 backward; 256 workgroups, twice as many take 28 + 38 and 25 + 60.
 struct Spans {
   int64_t blocks;  // of channels
   int32_t steps;   // of a span, a multiple of the tile's
@@ -612,7 +623,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_backward_tile(msamp_recurrence a
   else backward_tiles<T, WAVES, PASS, false>(a, sp, p, wave_map);
 }
 
-constexpr int64_t kFewSteps = 8;      // up to which a lane goes through them alone
+// Steps up to which a lane goes through them alone (channels 4,096, bfloat16). Forward, 64 sequences of 8 steps: 5.6 us,
+// the tiles with 9 8.5; 256 sequences 10 and 27. Backward, 64 of 4 steps 11, of 8 16 as the tiles with 9; 256 of 8 steps
+// 70 and 48.
+constexpr int64_t kFewForward = 16, kFewBackward = 4;
 constexpr int64_t kEnoughGroups = 192;  // workgroups from which sequences are left whole
 constexpr int64_t kSpanGroups = 256;    // of sequences that are cut
 constexpr int64_t kMostSpans = 64;
@@ -671,7 +685,7 @@ hipError_t tiles(const msamp_recurrence& a, const Spans& sp, hipStream_t s) {
 // A lane goes through all steps of few, and where a tile's steps do not lie
 // within the 2^31 bytes of a buffer.
 bool lane_alone(const msamp_recurrence& a, bool backward) {
-  if (a.time <= kFewSteps) return true;
+  if (a.time <= (backward ? kFewBackward : kFewForward)) return true;
   const int64_t most = ((int64_t)1 << 31) / (a.dtype == MSAMP_F32 ? 4 : 2) - a.channels;
   const int64_t tile = kChunk * waves_of(a.time);
   auto far = [&](int64_t stride) { return stride >= most / tile; };
