@@ -191,10 +191,10 @@ __global__ __launch_bounds__(kBlock) void k_backward_lane(msamp_recurrence a, in
 // then go through their steps with the state they start from. The next tile's
 // loads are under way meanwhile.
 //
-// Bound by memory: 4 x 4,096 steps of 4,096 bfloat16 channels take 72 us
-// forward (411 MB, 5.7 TB/s) and 135 us backward (679 MB, 5.0 TB/s; x, gate and
-// dy are read once, h comes from the saved states); a lane that goes through
-// all steps alone takes 2,627 and 5,664 us. A tile's loads have to be under way
+// Bound by memory: 4 x 4,096 steps of 4,096 bfloat16 channels take 88 us
+// forward (411 MB, 4.7 TB/s; 72 where the last call left part in the cache) and
+// 156 us backward (679 MB, 4.4 TB/s; 135; x, gate and dy are read once, h comes
+// from the saved states); a lane that goes through all steps alone takes 2,627 and 5,664 us. A tile's loads have to be under way
 // for the whole of the tile before it: nothing in the loop may wait for memory
 // (a state loaded before the loop is waited for there, no value goes through
 // scratch, the odd channel's block has a loop of its own), and the two channels
@@ -657,11 +657,11 @@ Spans spans_of(const msamp_recurrence& a, void* ws, bool backward) {
   const int64_t each = (tiles + count - 1) / count;
   s.count = (int32_t)((tiles + each - 1) / each);
   s.steps = (int32_t)(each * tile);
-  // Whole lines (steps that start on 128 bytes): 4 to a die spread a sequence's channels over all dies; with all of
-  // them on one, 8 x 4,096 x 4,096 took 341 us backward instead of 298. Lines that neighbours share: all of them (2 x
-  // 16,411 x 1,000: 73 us backward, with 4 of them 86, in turn 103).
+  // Lines that neighbours share (steps that do not start on 128 bytes): all of a die's workgroups side by side. 2 x
+  // 16,411 x 1,000: 40 us forward and 73 backward, in turn 55 and 103. Whole lines: in turn (4 x 4,096 x
+  // 4,096: 88 us and 156; four to a die 92 and 164).
   const int64_t all = s.blocks * s.count * a.batch;
-  s.run = whole_lines(a, backward) ? 4 : (int32_t)((all + 7) / 8);
+  s.run = whole_lines(a, backward) ? 1 : (int32_t)((all + 7) / 8);
   s.joined = (float4*)ws;
   s.first = (float2*)(s.joined + a.batch * s.count * s.pairs);
   return s;
