@@ -14,7 +14,7 @@ namespace msamp {
 namespace {
 
 constexpr int kChunk = MSAMP_RECURRENCE_CHUNK;
-constexpr int kPastCaches = 2;  // nt
+constexpr int kPastCaches = 2, kThroughCaches = 0;  // nt, or not
 
 // Two consecutive channels as they lie in memory; n (1 or 2) of them are the
 // tensor's.
@@ -41,8 +41,9 @@ struct Pair<float> {
     return raw{__builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0), 0u};
   }
   static __device__ __forceinline__ raw second(raw r) { return raw{r.y, 0u}; }
+  template <int CACHES>
   static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, uint32_t at, float2 v) {
-    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v.x), __float_as_uint(v.y)}, b, at, 0, kPastCaches);
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v.x), __float_as_uint(v.y)}, b, at, 0, CACHES);
   }
   static __device__ __forceinline__ void store_one(__amdgpu_buffer_rsrc_t b, uint32_t at, float2 v) {
     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v.x), b, at, 0, 0);
@@ -76,8 +77,9 @@ struct Pair {
     return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, at, 0, 0);
   }
   static __device__ __forceinline__ raw second(raw r) { return r >> 16; }
+  template <int CACHES>
   static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, uint32_t at, float2 v) {
-    __builtin_amdgcn_raw_buffer_store_b32(packed(v), b, at, 0, kPastCaches);
+    __builtin_amdgcn_raw_buffer_store_b32(packed(v), b, at, 0, CACHES);
   }
   static __device__ __forceinline__ void store_one(__amdgpu_buffer_rsrc_t b, uint32_t at, float2 v) {
     __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(packed(v) & 0xFFFFu), b, at, 0, 0);
@@ -210,6 +212,7 @@ struct Spans {
   int32_t steps;   // of a span, a multiple of the tile's
   int32_t count;
   int32_t run;     // neighbouring blocks on a die
+  bool whole;      // every step starts on 128 bytes
   float4* joined;  // [batch][count][pairs]: (A, S) of each span
   float2* first;   // [batch][pairs]: the state before all spans, which the last state may go over
   int64_t pairs;
@@ -317,11 +320,17 @@ __device__ __forceinline__ float2 own(const Place& p, typename Pair<T>::raw v) {
   return Pair<T>::values(ODD && p.ends ? Pair<T>::second(v) : v);
 }
 template <typename T, int R, bool ODD>
-__device__ __forceinline__ void store_steps(__amdgpu_buffer_rsrc_t b, const Steps& s, const Place& p, const float2* v) {
+__device__ __forceinline__ void store_steps(__amdgpu_buffer_rsrc_t b, const Steps& s, const Place& p, bool whole,
+                                            const float2* v) {
   const uint32_t row = (uint32_t)(s.stride * (int64_t)sizeof(T));
   const uint32_t at = once(ODD && p.n < 2 ? kOutside : s.lane);
+  if (whole) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) Pair<T>::store(b, at + r * row, v[r]);
+    for (int r = 0; r < R; ++r) Pair<T>::template store<kPastCaches>(b, at + r * row, v[r]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) Pair<T>::template store<kThroughCaches>(b, at + r * row, v[r]);
+  }
   if (ODD && p.n == 1) {
     const uint32_t one = once(s.lane);
 #pragma unroll
@@ -457,7 +466,7 @@ __device__ __forceinline__ void forward_tiles(const msamp_recurrence& a, const S
       v = fma2(av[r], v, bv[r]);
       bv[r] = v;
     }
-    store_steps<T, R, ODD>(buffer_of(y, sy, t, steps_at(t), a.channels), sy, p, bv);
+    store_steps<T, R, ODD>(buffer_of(y, sy, t, steps_at(t), a.channels), sy, p, sp.whole, bv);
   }
   if (p.n == 0 || threadIdx.x >= K::kLanes) return;
   if (PASS == 1) {
@@ -600,8 +609,8 @@ __device__ __forceinline__ void backward_tiles(const msamp_recurrence& a, const 
     }
     if (more) load_steps<T, R, ODD>(buffer_of(dy, sd, t - K::kTile, K::kTile, a.channels), sd, p, dr);
     if (PASS == 0) {
-      store_steps<T, R, ODD>(buffer_of(dx, ox, t, steps_at(t), a.channels), ox, p, keep);
-      store_steps<T, R, ODD>(buffer_of(dg, og, t, steps_at(t), a.channels), og, p, slope);
+      store_steps<T, R, ODD>(buffer_of(dx, ox, t, steps_at(t), a.channels), ox, p, sp.whole, keep);
+      store_steps<T, R, ODD>(buffer_of(dg, og, t, steps_at(t), a.channels), og, p, sp.whole, slope);
     }
   }
   if (p.n == 0 || threadIdx.x >= K::kLanes) return;
@@ -659,9 +668,12 @@ Spans spans_of(const msamp_recurrence& a, void* ws, bool backward) {
   s.steps = (int32_t)(each * tile);
   // Lines that neighbours share (steps that do not start on 128 bytes): all of a die's workgroups side by side. 2 x
   // 16,411 x 1,000: 40 us forward and 73 backward, in turn 55 and 103. Whole lines: in turn (4 x 4,096 x
-  // 4,096: 88 us and 156; four to a die 92 and 164).
+  // 4,096: 88 us and 156; four to a die 92 and 164). Outputs go past the caches where lines are whole (there 88 and
+  // 156, through them 90 and 159) and through them where the cache can join a line's parts (2 x 16,411 x 999
+  // backward: 138 us past them, 127 through).
   const int64_t all = s.blocks * s.count * a.batch;
-  s.run = whole_lines(a, backward) ? 1 : (int32_t)((all + 7) / 8);
+  s.whole = whole_lines(a, backward);
+  s.run = s.whole ? 1 : (int32_t)((all + 7) / 8);
   s.joined = (float4*)ws;
   s.first = (float2*)(s.joined + a.batch * s.count * s.pairs);
   return s;
