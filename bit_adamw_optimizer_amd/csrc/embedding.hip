@@ -260,7 +260,8 @@ __device__ __forceinline__ void store4(float* p, int n, const float* f) {
 
 // Adds dy's columns col[c] of sorted rows [p0, p1), in their order, U rows'
 // loads under way at a time. WAVE: p0 and p1 are the whole wave's, whose lanes
-// load 64 rows' numbers at once.
+// load 64 rows' numbers at once and read them from each other: all 64 have to
+// come here, those without columns (n <= 0, nothing is loaded for them) too.
 template <typename T, int CH, int U, bool WAVE>
 __device__ __forceinline__ void sum_rows(const EmbeddingArgs& a, const int32_t* order, int64_t p0, int64_t p1,
                                          int64_t col, int step, const int* n, float (*f)[4]) {
@@ -359,7 +360,10 @@ __global__ __launch_bounds__(kBlock) void k_embedding_backward(EmbeddingArgs a, 
   if (kWave) q0 = __builtin_amdgcn_readfirstlane(q0), q1 = __builtin_amdgcn_readfirstlane(q1);
   const int64_t p0 = q0, p1 = q1;
   float* out = a.dweight + v * a.ld_dweight;
-  for (int64_t col = lane * 4; col < a.cols; col += CH * kStep) {
+  // a wave stays together while it has columns, its lanes behind the last one too (sum_rows)
+  const int in_wave = kWave ? lane & 63 : lane;
+  for (int64_t first = lane - in_wave; first * 4 < a.cols; first += CH * LANES) {
+    const int64_t col = (first + in_wave) * 4;
     int n[CH];
     float f[CH][4] = {};
 #pragma unroll

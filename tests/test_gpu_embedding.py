@@ -163,3 +163,24 @@ def test_another_stream_and_replays():
         for y, dw in outs:
             assert torch.equal(y, want_y) and torch.equal(dw, want_dw)
         backward(dy, ids, vocab)  # eager work between the replays
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows,vocab,cols", [
+    (40, 3, 4100), (40, 3, 4157), (45, 3, 5000), (30, 2, 8196), (40000, 700, 132), (40000, 700, 190), (40000, 700, 252),
+    (140000, 1100, 131)])
+def test_ids_of_several_rows_whose_last_columns_do_not_fill_a_wave(rows, vocab, cols, dtype):
+    """A wave reads its rows' numbers from all of its lanes, those without columns among them: as many rows of an id as
+    a piece has (16, 64 of 40,000 rows, 256 of 140,000) and fewer, and ids of more than a piece."""
+    g = torch.Generator().manual_seed(cols)
+    ids = torch.randint(0, vocab, (rows,), generator=g)
+    ids[rows // 2] = -1
+    if rows > 1000:
+        ids[ids >= vocab - 2] = 0
+        ids[:64], ids[64:64 + 50] = vocab - 1, vocab - 2
+    ids = ids.cuda()
+    dy, base = rows_of(rows, cols, 1, DT[dtype], 7, 0.1), rows_of(vocab, cols, 0, torch.float32, 8)
+    got = backward(dy, ids, vocab, 0.5)
+    check_backward(dy, ids, vocab, 0.5, got)
+    check_backward(dy, ids, vocab, 0.5, backward(dy, ids, vocab, 0.5, base), base)
+    assert torch.equal(got, backward(dy, ids, vocab, 0.5))
