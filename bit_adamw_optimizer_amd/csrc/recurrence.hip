@@ -570,6 +570,11 @@ __device__ __forceinline__ void backward_tiles(const msamp_recurrence& a, const 
         load_state(t - K::kTile);
       }
     }
+    if (cut) {  // a dy that repeats its steps is within its bounds behind the end too
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (at + r >= p.t1) dr[r] = typename Pair<T>::raw{};
+    }
     Affine f = {av[R - 1], mul2(av[R - 1], own<T, ODD>(p, again(dr[R - 1])))}, before, all;
 #pragma unroll
     for (int r = R - 2; r >= 0; --r) {

@@ -334,3 +334,39 @@ def test_another_stream_and_replays(shape):
         for _, o in runs:
             assert all(torch.equal(p, q) for p, q in zip(want, o))
         go(other)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("shape", [(2, 3, 6), (2, 33, 10), (3, 100, 33), (2, 300, 40), (1, 9001, 6)])
+def test_backward_from_repeated_and_overlapping_steps(shape, dtype):
+    """Gradients of a sum over time (one dy for all steps), inputs repeated over time or sequences, and steps that
+    share elements, with and without lengths: what is behind the last step is not added again."""
+    b, t, c = shape
+    dt = DT[dtype]
+    full = [cube(shape, dt, i, 0.5, offset=i % 2) for i in (1, 2, 3)]
+    gen = torch.Generator().manual_seed(4)
+    h0, dl = (torch.randn(b, c, generator=gen).cuda() for _ in range(2))
+    shifted = cube((1, 1, b * c + 3 * t), dt, 5, 0.5).as_strided(shape, (c, 3, 1))
+    for n in (None, torch.tensor([t - 1, t // 2 + 1, 1][:b], device="cuda")):
+        check(full[0], full[1], h0, n, full[2][:, :1].expand(shape), dl)
+        for which in (0, 1, 2, None):
+            for v in ([p[:, :1].expand(shape) for p in full], [p[:1].expand(shape) for p in full], [shifted] * 3):
+                args = [v[i] if which in (i, None) else full[i] for i in range(3)]
+                outs = []
+                for x, g, dy in (args, [p.contiguous() for p in args]):
+                    st, y = M.new_recurrence_states(*shape).fill_(7), torch.full(shape, 7.0, dtype=dt, device="cuda")
+                    M.recurrence_forward(x, g, y, h0=h0, states=st, lengths=n)
+                    dx, dg, dh0 = torch.full_like(y, 7.0), torch.full_like(y, 7.0), torch.full_like(h0, 7.0)
+                    M.recurrence_backward(dy, x, g, st, dx, dg, dh_last=dl, dh0=dh0, lengths=n)
+                    outs.append((y, st, dx, dg, dh0))
+                assert all(torch.equal(p, q) for p, q in zip(*outs)), (which, n)
+
+
+def test_the_gradient_of_a_mean_over_time():
+    """Open gates (a = 1/2) and dy = 1: l_t = 2 - 2^-(T - 1 - t), so that dx at the last step is 1/2."""
+    for t in (33, 100, 300):
+        x = torch.zeros(1, t, 2, device="cuda")
+        dy, dx, dg = torch.ones(1, 1, 2, device="cuda").expand(1, t, 2), torch.empty_like(x), torch.empty_like(x)
+        M.recurrence_backward(dy, x, x, M.new_recurrence_states(1, t, 2).zero_(), dx, dg)
+        want = 1 - 0.5 ** (t - torch.arange(t, dtype=torch.float64))
+        R.assert_near(dx[0, :, 0], want, 16 * R.U * want, "dx")
