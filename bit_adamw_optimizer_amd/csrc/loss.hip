@@ -26,7 +26,7 @@ struct LossArgs {
   float inv_tau;             // 1 / tau
   double inv_tau64;
   double log_low, log_high;  // logarithms of the clip's bounds
-  float low, high, kl;
+  double low, high, kl;
 };
 
 __device__ __forceinline__ float wave_max(float v) {
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
       if (KIND == kPolicy) {
         old = a.old_logp[row];
         adv = a.advantages[row];
-        if (l.kl != 0.0f) ref = a.ref_logp[row];
+        if (l.kl != 0.0) ref = a.ref_logp[row];
       }
     }
     if (a.dlogits != nullptr && a.dloss != nullptr) dloss = a.dloss[row];
@@ -387,22 +387,22 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
   float c = 0.0f, at = 0.0f;
   if constexpr (KIND == kPolicy) {
     if (wave == 0) {
-      const float zv = zc - s.largest;
-      const double lp = (double)zv * l.inv_tau64 - log((double)s.sum);
-      const double d = lp - (double)old;
-      const float r = expf((float)d);
+      // binary64 from the row's binary32 sum on: one lane's work, while near the reference policy e^d - d - 1 is d^2 / 2
+      // and would keep no digits of binary32
+      const double lp = ((double)zc - (double)s.largest) * l.inv_tau64 - log((double)s.sum);
+      const double d = lp - (double)old, r = exp(d);
       const bool over = adv > 0.0f && d > l.log_high, under = adv < 0.0f && d < l.log_low;
-      const float away = l.kl != 0.0f ? (float)((double)ref - lp) : 0.0f;
-      const float more = expm1f(away);
+      const double away = l.kl != 0.0 ? (double)ref - lp : 0.0, more = expm1(away);
       if (first && lane == 0) {
-        const float won = adv == 0.0f ? 0.0f : (over ? l.high : under ? l.low : r) * adv;
-        a.loss[row] = l.kl * (more - away) - won;
+        const double won = adv == 0.0f ? 0.0 : (over ? l.high : under ? l.low : r) * (double)adv;
+        const double apart = away == INFINITY ? away : more - away;  // the reference allows what the mask does not
+        a.loss[row] = (float)(l.kl * apart - won);
         if (a.logp != nullptr) a.logp[row] = (float)lp;
       }
-      const float g = -l.kl * more - (over || under || adv == 0.0f ? 0.0f : r * adv);
-      c = -dloss * g * l.inv_tau;
+      const double g = -l.kl * more - (over || under || adv == 0.0f ? 0.0 : r * (double)adv);
+      c = (float)(-(double)dloss * g * l.inv_tau64);
       if (kWaves > 1 && lane == 0) factor = c;
-      at = (__builtin_amdgcn_exp2f(zv * scale) * inv - 1.0f) * c;
+      at = (__builtin_amdgcn_exp2f((zc - s.largest) * scale) * inv - 1.0f) * c;
       if (kWaves > 1 && lane == 0) part_of_loss[0] = at;
     }
     if (a.dlogits != nullptr && kWaves > 1) {
@@ -533,9 +533,9 @@ LossArgs loss_args(const msamp_vocab_loss& a) {
   l.inv_tau64 = 1.0 / a.temperature;
   l.log_low = std::log(1.0 - a.clip_low);
   l.log_high = std::log1p(a.clip_high);
-  l.low = (float)(1.0 - a.clip_low);
-  l.high = (float)(1.0 + a.clip_high);
-  l.kl = (float)a.kl;
+  l.low = 1.0 - a.clip_low;
+  l.high = 1.0 + a.clip_high;
+  l.kl = (float)a.kl != 0.0f ? a.kl : 0.0;  // as the check of ref_logp takes it
   return l;
 }
 

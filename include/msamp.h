@@ -823,9 +823,11 @@ msamp_status msamp_recurrence_backward(const msamp_recurrence* args, void* works
  *     g = kl (1 - e^d) - (0 where r is beyond the bound that the minimum
  *         takes: A > 0 and r > 1 + clip_high, or A < 0 and r < 1 - clip_low;
  *         else r A)
- *   A row with A = 0 has no first term. lp and the clip's comparison are
- *   formed in binary64 from binary32 sums, so that a ratio next to a bound
- *   falls on its side.
+ *   A row with A = 0 has no first term. lp and all that follows from it (the
+ *   clip's comparison, r, e^d - d - 1, g) are formed in binary64 from the
+ *   row's binary32 sum, so that a ratio next to a bound falls on its side and
+ *   a small d keeps its digits. An action with a logit of -Inf is infinitely
+ *   far from a reference that allows it (kl times Inf).
  *
  * Everything else is binary32; loss and logp are binary32, dlogits is rounded
  * once to dtype (with MSAMP_F16, values of 2^-25 or less become 0: dloss has

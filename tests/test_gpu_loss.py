@@ -323,3 +323,36 @@ def test_another_stream_and_replays():
         for _, o in runs:
             assert all(torch.equal(p, q) for p, q in zip(want, o))
         go(other)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("vocab", [512, 1 << 15, 1 << 17])
+def test_the_kl_term_next_to_the_reference_policy(vocab, dtype):
+    """e^d - d - 1 is about d^2 / 2: every digit of it, where lp is exact (equal logits, a power of two of them: sums
+    of ones, and a logarithm in binary64, off by less than 2^-49). One rounding, the binary64 logarithm's 2^-49 as
+    a part of d, expm1's last place as a part of d / 2; the gradient's exact q leaves the factor and two products."""
+    d = torch.tensor([0.3, -0.3, 1e-2, -1e-2, 1e-3, -1e-3, 1e-4, -1e-4, 1e-5, -1e-5, 1e-6, 0.0], dtype=torch.float64)
+    rows, lp = len(d), -math.log(vocab)
+    z = torch.full((rows, vocab), 1.5, dtype=DT[dtype], device="cuda")
+    ref = (lp + d).float()
+    d = ref.double() - lp
+    act, old, adv = torch.arange(rows, device="cuda"), torch.full((rows,), lp, device="cuda"), torch.zeros(rows, device="cuda")
+    for tau in (1.0, 2.0):
+        loss, dz = torch.empty(rows, device="cuda"), torch.empty_like(z)
+        M.policy_loss_forward(z, act, old, adv, loss, ref_logp=ref.cuda(), kl=0.5, dlogits=dz, temperature=tau)
+        want = 0.5 * (torch.expm1(d) - d)
+        R.assert_near(loss, want, 2 ** -47 * d.abs() + 2 ** -96, "loss")
+        q = torch.full((rows, vocab), -1.0 / vocab, dtype=torch.float64)
+        q[torch.arange(rows), torch.arange(rows)] += 1
+        want = (-0.5 * torch.expm1(d) / tau)[:, None] * q
+        R.assert_near(dz, want, 4 * R.U * want.abs() + 2 ** -48, "dlogits")
+
+
+def test_a_masked_action_is_infinitely_far_from_a_reference_that_allows_it():
+    z = matrix(3, 700, torch.float32, 0, 1)
+    z[1, 5] = -INF
+    act, v, adv = torch.full((3,), 5, device="cuda"), torch.full((3,), -6.0, device="cuda"), torch.ones(3, device="cuda")
+    loss, logp = torch.empty(3, device="cuda"), torch.empty(3, device="cuda")
+    for kl, want in ((0.1, INF), (-0.1, -INF), (0.0, 0.0)):
+        M.policy_loss_forward(z, act, v, adv, loss, logp=logp, ref_logp=v, kl=kl)
+        assert loss[1] == want and logp[1] == -INF and torch.isfinite(loss[[0, 2]]).all()
