@@ -1176,9 +1176,11 @@ def embedding_forward(ids: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, 
 def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, dweight: torch.Tensor, *, scale: float = 1.0,
                        accumulate: bool = False) -> None:
     """dweight <- the gradient of embedding_forward's weight from dy: for every
-    id scale times the sum of its rows, in their order; float32 [vocab, cols],
-    what amax takes. accumulate adds it to what is there (a tied output
-    projection's gradient) and leaves the rows of absent ids alone."""
+    id scale times the sum of its rows; float32 [vocab, cols], what amax takes.
+    Rows are added in their order, those of an id with many in pieces (16 rows
+    sorted by id, more of many rows) joined in order: the same ids give the same
+    bits. accumulate adds it to what is there (a tied output projection's
+    gradient) and leaves the rows of absent ids alone."""
     dev, d, shape = _leading(dy, "dy")
     rows, cols = shape
     pdy, lddy = _matrix(dy, "dy", dev, dy.dtype, shape)

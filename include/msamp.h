@@ -708,7 +708,12 @@ msamp_status msamp_embedding_forward(int64_t rows, int64_t vocab, int64_t cols, 
 /*
  * msamp_embedding_backward -- dweight [vocab, cols], binary32 (what msamp_amax
  * takes): dweight[v] = scale * (sum of dy[r] over the rows r with ids[r] = v,
- * in binary32, in the rows' order); zeros where there is no such row. With
+ * in binary32); zeros where there is no such row. The sum goes through the rows
+ * in their order; with more than P of them (P = 16, doubled while P * 1024 <
+ * rows) it is cut into pieces, summed in order each and then joined in order.
+ * They are cut at every P-th of all rows sorted by id, so the last bits of an
+ * id's sum depend on how many rows smaller ids have, but on nothing that
+ * changes from call to call. With
  * accumulate the products are added to what is there (the gradient of an
  * output projection tied to the embedding), and a dweight row without rows of
  * its id is neither read nor written.

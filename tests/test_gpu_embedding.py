@@ -184,3 +184,26 @@ def test_ids_of_several_rows_whose_last_columns_do_not_fill_a_wave(rows, vocab, 
     check_backward(dy, ids, vocab, 0.5, got)
     check_backward(dy, ids, vocab, 0.5, backward(dy, ids, vocab, 0.5, base), base)
     assert torch.equal(got, backward(dy, ids, vocab, 0.5))
+
+
+@pytest.mark.parametrize("rows,vocab,cols", [(300, 4, 7), (1000, 50, 260), (20000, 9, 3)])
+def test_the_order_of_the_sum(rows, vocab, cols):
+    """In the rows' order up to a piece of them; beyond it pieces of the rows sorted by id, joined in order."""
+    ids, dy = ids_of(rows, vocab, 3), rows_of(rows, cols, 0, torch.float32, 4)
+    piece = 16
+    while piece * 1024 < rows:
+        piece *= 2
+    i, v = ids.cpu(), dy.cpu()
+    order = torch.argsort(torch.where((i < 0) | (i >= vocab), vocab, i), stable=True)
+    want, at = torch.zeros(vocab, cols), 0
+    for k in range(vocab):
+        n = int((i == k).sum())
+        cuts = [at, at + n] if n <= piece else [at, *range(at // piece * piece + piece, at + n, piece), at + n]
+        total = torch.zeros(cols)
+        for p0, p1 in zip(cuts, cuts[1:]):
+            part = torch.zeros(cols)
+            for r in order[p0:p1]:
+                part += v[r]
+            total = part if len(cuts) == 2 else total + part
+        want[k], at = total, at + n
+    assert torch.equal(backward(dy, ids, vocab).cpu(), want)
