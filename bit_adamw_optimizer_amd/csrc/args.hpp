@@ -70,14 +70,16 @@ class Regions {
            int in_place = 0, int64_t outer = 0) {
     if (p == nullptr || rows == 0 || cols == 0) return;
     r_[n_++] = {(uintptr_t)p, (uintptr_t)p + (uintptr_t)(((rows - 1) * ld + cols) * size), cols * size,
-                rows == 1 ? cols * size : ld * size, outer, rows == 1, written, in_place, role};
+                rows == 1 ? cols * size : ld * size, outer, rows == 1, written, in_place, role, {}};
   }
   // [batch, time, cols] with distances sb and st: the rows of a matrix where
   // one distance is a multiple of the other (with the rows between them, which
   // may be nobody's), otherwise all that lies between the first and the last.
+  // Two of the same distances, one of them beyond all that the other spans, are
+  // compared row by row (rows_meet).
   void cube(const void* p, int64_t batch, int64_t time, int64_t cols, int64_t sb, int64_t st, int64_t size,
             bool written, const char* role, int in_place) {
-    if (batch == 0 || time == 0) return;
+    if (p == nullptr || batch == 0 || time == 0 || cols == 0) return;
     if (batch == 1) sb = 0;
     if (time == 1) st = 0;
     const int64_t small = batch == 1 ? st : time == 1 ? sb : st < sb ? st : sb, large = st < sb ? sb : st;
@@ -86,6 +88,9 @@ class Regions {
     else if (small >= cols && (small == large || batch == 1 || time == 1 || large % small == 0))
       add(p, last / small + 1, cols, small, size, written, role, in_place, sb);
     else add(p, 1, last + cols, last + cols, size, written, role, in_place, sb);
+    const int64_t n = small == st ? time : batch;  // rows 'small' apart
+    if (batch > 1 && time > 1 && small >= cols && large >= (n - 1) * small + cols)
+      r_[n_ - 1].rows = {cols * size, small * size, large * size, n, batch * time / n};
   }
   void vector(const void* p, int64_t n, int64_t size, bool written, const char* role) {
     add(p, 1, n, n, size, written, role);
@@ -104,18 +109,42 @@ class Regions {
   }
 
  private:
+  struct Rows {  // of a cube, in bytes: runs of 'count' rows 'small' apart, 'large' apart; bytes 0: not such a cube
+    int64_t bytes, small, large, count, runs;
+  };
   struct Region {
     uintptr_t lo, hi;
     int64_t row, ld, outer;
     bool one, written;
     int in_place;
     const char* role;
+    Rows rows;
   };
+  // Whether a row of one cube touches a row of another of the same distances:
+  // rows i runs and j rows apart do where the starts' distance less i large and
+  // j small is less than a row, which only the nearest two i and j can make it.
+  static bool rows_meet(const Region& a, const Region& b) {
+    const Rows& r = a.rows;
+    const int64_t d = (int64_t)(b.lo - a.lo);
+    auto below = [](int64_t v, int64_t by) { return v / by - (v % by < 0 ? 1 : 0); };
+    const int64_t i0 = below(d, r.large);
+    for (int64_t i = i0; i <= i0 + 1; ++i) {
+      const int64_t left = d - i * r.large, j0 = below(left, r.small);
+      for (int64_t j = j0; j <= j0 + 1; ++j) {
+        const int64_t apart = left - j * r.small;
+        if (i > -r.runs && i < r.runs && j > -r.count && j < r.count && apart > -r.bytes && apart < r.bytes) return true;
+      }
+    }
+    return false;
+  }
   static bool overlap(const Region& a, const Region& b) {
     if (a.hi <= b.lo || b.hi <= a.lo) return false;
     if (a.in_place != 0 && a.in_place == b.in_place && !(a.written && b.written) && a.lo == b.lo && a.hi == b.hi &&
         a.row == b.row && a.outer == b.outer && (a.ld == b.ld || a.one))
       return false;
+    if (a.rows.bytes != 0 && a.rows.bytes == b.rows.bytes && a.rows.small == b.rows.small &&
+        a.rows.large == b.rows.large && a.rows.count == b.rows.count && a.rows.runs == b.rows.runs)
+      return rows_meet(a, b);
     // rows side by side at the same distance (columns of one buffer)
     const int64_t ld = a.one ? b.ld : a.ld;
     if ((a.one && b.one) || (!a.one && !b.one && a.ld != b.ld) || ld == 0) return true;

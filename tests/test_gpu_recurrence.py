@@ -370,3 +370,24 @@ def test_the_gradient_of_a_mean_over_time():
         M.recurrence_backward(dy, x, x, M.new_recurrence_states(1, t, 2).zero_(), dx, dg)
         want = 1 - 0.5 ** (t - torch.arange(t, dtype=torch.float64))
         R.assert_near(dx[0, :, 0], want, 16 * R.U * want, "dx")
+
+
+@pytest.mark.parametrize("pad", [0, 5])
+def test_parts_of_one_buffer_that_are_apart(pad):
+    """Time halves, and column halves of sequences that start anywhere: inputs and outputs share no element."""
+    B, T, C = 3, 70, 24
+    x, g, dy = (cube((B, T, C), torch.float32, i, offset=i % 2) for i in (1, 2, 3))
+    y, st, dx, dg = torch.empty_like(x), M.new_recurrence_states(B, T, C), torch.empty_like(x), torch.empty_like(x)
+    M.recurrence_forward(x, g, y, states=st)
+    M.recurrence_backward(dy, x, g, st, dx, dg)
+    for make in (lambda: torch.zeros(B, 2 * T * C + pad, device="cuda")[:, :2 * T * C].view(B, 2 * T, C).split(T, 1),
+                 lambda: torch.zeros(B, 2 * T * C + pad, device="cuda")[:, :2 * T * C].view(B, T, 2 * C).split(C, 2),
+                 lambda: torch.zeros(T, 2 * B * C + pad, device="cuda")[:, :2 * B * C].view(T, 2 * B, C).transpose(0, 1).split(B)):
+        for src in (x, g):
+            a, b = make()
+            a.copy_(src)
+            M.recurrence_forward(a if src is x else x, a if src is g else g, b)
+            assert torch.equal(b, y) and torch.equal(a, src)
+        a, b = make()
+        M.recurrence_backward(dy, x, g, st, a, b)
+        assert torch.equal(a, dx) and torch.equal(b, dg)

@@ -124,6 +124,27 @@ def test_recurrence_memory_that_is_shared():
     refused("forward", "x and h_last", time=1, dtype=F32, h0=0, h_last=0x100000, ld_h_last=64, x_batch=64, y_batch=64, gate_batch=64)
 
 
+def test_recurrence_parts_of_one_buffer_that_share_a_step_or_an_element():
+    def refused(**kw):
+        for which, what in (("forward", "x and y"), ("backward", "dx and dgate")):
+            a, b = ("x", "y") if which == "forward" else ("dx", "dgate")
+            args = {a + "_batch": kw["batch"], b + "_batch": kw["batch"], a + "_time": kw["time"], b + "_time": kw["time"],
+                    a: 0x400000, b: 0x400000 + kw["apart"]}
+            assert _rrun(which, **args) == 1 and what + " overlap" in _err(), (kw, _err())
+
+    step, seq = 64 * 2, 40 * 64 * 2
+    for pad in (0, 3):  # time halves
+        long = 80 * 64 + pad
+        for apart in (2, step, seq - step, seq - 2, 2 * long + seq - 2, 2 * long + step):
+            refused(batch=long, time=64, apart=apart)
+        # column halves of sequences that start anywhere
+        for apart in (2, step - 2, 39 * 2 * step + step - 2, 2 * long + step - 2):
+            refused(batch=long, time=128, apart=apart)
+    # time-major halves
+    refused(batch=64, time=8 * 64, apart=4 * step - 2)
+    refused(batch=64, time=8 * 64, apart=3 * step)
+
+
 # ------------------------------------------------------------------ losses ---
 
 def _loss(**kw):
