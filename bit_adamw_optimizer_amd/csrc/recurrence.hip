@@ -645,7 +645,13 @@ constexpr int64_t kEnoughGroups = 192;  // workgroups from which sequences are l
 constexpr int64_t kSpanGroups = 256;    // of sequences that are cut
 constexpr int64_t kMostSpans = 64;
 
-int waves_of(int64_t time) { return time <= kChunk ? 1 : time <= 2 * kChunk ? 2 : time <= 4 * kChunk ? 4 : 8; }
+// A launch has less than 2^32 threads: 2^22 sequences of up to 64 binary32 channels, two workgroups each, take 4 waves.
+int waves_of(const msamp_recurrence& a) {
+  const int64_t channels = a.dtype == MSAMP_F32 ? 32 : 64;  // of a workgroup
+  if (a.time <= kChunk) return 1;
+  if (a.time <= 2 * kChunk) return 2;
+  return a.time <= 4 * kChunk || a.batch * ((a.channels + channels - 1) / channels) > (1 << 22) ? 4 : 8;
+}
 
 bool whole_lines(const msamp_recurrence& a, bool backward) {
   const int64_t size = a.dtype == MSAMP_F32 ? 4 : 2;
@@ -663,7 +669,7 @@ Spans spans_of(const msamp_recurrence& a, void* ws, bool backward) {
   const int64_t lanes = a.dtype == MSAMP_F32 ? lanes_of<float>() : lanes_of<f16>();
   s.pairs = (a.channels + 1) / 2;
   s.blocks = (s.pairs + lanes - 1) / lanes;
-  const int64_t tile = kChunk * waves_of(a.time), tiles = (a.time + tile - 1) / tile;
+  const int64_t tile = kChunk * waves_of(a), tiles = (a.time + tile - 1) / tile;
   const int64_t groups = s.blocks * a.batch;
   int64_t count = groups >= kEnoughGroups ? 1 : (kSpanGroups + groups - 1) / groups;
   if (count > kMostSpans) count = kMostSpans;
@@ -704,7 +710,7 @@ hipError_t tiles(const msamp_recurrence& a, const Spans& sp, hipStream_t s) {
 bool lane_alone(const msamp_recurrence& a, bool backward) {
   if (a.time <= (backward ? kFewBackward : kFewForward)) return true;
   const int64_t most = ((int64_t)1 << 31) / (a.dtype == MSAMP_F32 ? 4 : 2) - a.channels;
-  const int64_t tile = kChunk * waves_of(a.time);
+  const int64_t tile = kChunk * waves_of(a);
   auto far = [&](int64_t stride) { return stride >= most / tile; };
   if (far(a.x_time) || far(a.gate_time)) return true;
   return backward ? far(a.dy_time) || far(a.dx_time) || far(a.dgate_time) : far(a.y_time);
@@ -720,7 +726,7 @@ hipError_t run(const msamp_recurrence& a, void* ws, hipStream_t s) {
     return hipGetLastError();
   }
   const Spans sp = spans_of(a, ws, BACKWARD);
-  switch (waves_of(a.time)) {
+  switch (waves_of(a)) {
     case 1: return tiles<T, 1, BACKWARD>(a, sp, s);
     case 2: return tiles<T, 2, BACKWARD>(a, sp, s);
     case 4: return tiles<T, 4, BACKWARD>(a, sp, s);

@@ -391,3 +391,21 @@ def test_parts_of_one_buffer_that_are_apart(pad):
         a, b = make()
         M.recurrence_backward(dy, x, g, st, a, b)
         assert torch.equal(a, dx) and torch.equal(b, dg)
+
+
+def test_the_largest_number_of_sequences():
+    """2^22 sequences of 33 binary32 channels, in place: 2^23 workgroups."""
+    B, T, C = 1 << 22, 129, 33
+    g = cube((1, T, C), torch.float32, 1, offset=2.0)
+    first, last = cube((1, T, C), torch.float32, 2), cube((1, T, C), torch.float32, 3)
+    x = torch.ones(B, T, C, device="cuda")
+    x[0], x[-1] = first[0], last[0]
+    M.recurrence_forward(x, g.expand(B, T, C), x)
+    y = torch.empty(3, T, C, device="cuda")
+    M.recurrence_forward(torch.cat([first, torch.ones_like(first), last]), g.expand(3, T, C), y)
+    # fewer waves side by side join their steps in another order: both within the bound
+    for i, (at, v) in enumerate(((0, first), (B // 2 + 1, torch.ones_like(first)), (B - 1, last))):
+        hs, errs = R.recurrence_forward(v.cpu(), g.cpu())
+        R.assert_near(x[at:at + 1], hs[:, 1:], errs[:, 1:], "y")
+        R.assert_near(y[i:i + 1], hs[:, 1:], errs[:, 1:], "y of three")
+    assert torch.equal(x[1], x[B // 2 + 1]) and (x[1:-1].amax(0) == x[1]).all() and (x[1:-1].amin(0) == x[1]).all()
