@@ -418,7 +418,7 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
         const float zv = zc - s.largest, p = own * teacher_inv;
         float loss = p != 0.0f ? p * ((t - teacher_log) - (zv * l.inv_tau - log_sum)) : 0.0f;
         loss = wave_sum(loss);
-        if (first && lane == 0) a.loss[row] = tau * tau * loss;
+        if (first && lane == 0) a.loss[row] = tau * (tau * loss);
         at = (__builtin_amdgcn_exp2f(zv * scale) * inv - mine * teacher_inv) * c;
       }
       // these logits are read before the gradient, which may go over them, is written (the barrier of the sums does
@@ -444,7 +444,7 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
         loss = part_of_loss[0];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) loss += part_of_loss[w];
-        a.loss[row] = tau * tau * loss;
+        a.loss[row] = tau * (tau * loss);
       }
     }
   }

@@ -356,3 +356,12 @@ def test_a_masked_action_is_infinitely_far_from_a_reference_that_allows_it():
     for kl, want in ((0.1, INF), (-0.1, -INF), (0.0, 0.0)):
         M.policy_loss_forward(z, act, v, adv, loss, logp=logp, ref_logp=v, kl=kl)
         assert loss[1] == want and logp[1] == -INF and torch.isfinite(loss[[0, 2]]).all()
+
+
+@pytest.mark.parametrize("tau", [1e-25, 1e-12, 0.01, 20.0])
+def test_temperatures_far_from_one(tau):
+    """temperature^2 leaves binary32 before temperature times a logit does."""
+    rows, vocab = 3, 900
+    z, t = matrix(rows, vocab, torch.float32, 0, 1), matrix(rows, 5, torch.float32, 0, 2)
+    loss, _, _ = check_distill(z, classes(rows, vocab, 5, 3), t, tau, torch.full((rows,), 8.0, device="cuda"))
+    assert (loss > 0).all()
