@@ -18,12 +18,12 @@
 namespace msamp {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896341f;
+constexpr double kLog2e = 1.44269504088896341;
 
 struct LossArgs {
   msamp_vocab_loss a;
   int64_t row0;              // of the launch's first workgroup
-  float inv_tau;             // 1 / tau
+  float inv_tau, scale;      // 1 / tau, log2(e) / tau, rounded once each
   double inv_tau64;
   double log_low, log_high;  // logarithms of the clip's bounds
   double low, high, kl;
@@ -77,6 +77,11 @@ __device__ __forceinline__ void again(u32x4& r) { asm volatile("" : "+v"(r)); }
 // A row's softmax while it is formed: the largest logit and the sum of
 // exp2((z - largest) scale). Logits of -Inf alone leave the largest at -Inf
 // and the sum at 0; a NaN makes the sum NaN.
+// Both are binary32, as the stats that the backward pass takes are: terms are
+// added as trees of 8 over pieces, lanes and waves, and an exponent is off by
+// 2^-23 of itself, that is least where a term has weight. log(sum) is off by
+// 3e-8 at the median (rows of 512 binary32 logits), half a step of the stored
+// sum.
 struct Soft {
   float largest, sum;
 };
@@ -275,7 +280,7 @@ __global__ __launch_bounds__(BLOCK) void k_loss(LossArgs l, Parts parts) {
   const int top = KIND == kPolicy ? 1 : (int)a.top;
   const Entries e = {(int32_t*)lds, (float*)lds + top, (float*)lds + 2 * top};
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const float scale = l.inv_tau * kLog2e;
+  const float scale = l.scale;
   const bool first = FROM != kGivenSums && blockIdx.y == 0;  // writes the loss
   const int64_t row = l.row0 + blockIdx.x;
   const T* z = (const T*)a.logits + row * a.ld_logits;
@@ -501,7 +506,7 @@ __global__ __launch_bounds__(BLOCK) void k_parts(LossArgs l, Parts parts) {
   const msamp_vocab_loss& a = l.a;
   const int top = KIND == kPolicy ? 1 : (int)a.top;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const float scale = l.inv_tau * kLog2e;
+  const float scale = l.scale;
   const int64_t row = l.row0 + blockIdx.x;
   const T* z = (const T*)a.logits + row * a.ld_logits;
   Held<T, BLOCK, NCH> held;
@@ -530,6 +535,7 @@ LossArgs loss_args(const msamp_vocab_loss& a) {
   l.a = a;
   l.row0 = 0;
   l.inv_tau = (float)(1.0 / a.temperature);
+  l.scale = (float)(kLog2e / a.temperature);
   l.inv_tau64 = 1.0 / a.temperature;
   l.log_low = std::log(1.0 - a.clip_low);
   l.log_high = std::log1p(a.clip_high);

@@ -123,9 +123,9 @@ msamp_status check_loss(const msamp_vocab_loss* a, bool policy, bool backward) {
   if (V > MSAMP_LOSS_MAX_VOCAB) return invalid("vocab exceeds 2^29");
   MSAMP_TRY(check_dtype(a->dtype, "dtype"));
   MSAMP_TRY(check_int_bytes(a->id_bytes, "id_bytes"));
-  const float tau = (float)a->temperature, inv = (float)(1.0 / a->temperature);
+  const float tau = (float)a->temperature, inv = (float)(1.44269504088896341 / a->temperature);
   if (!(tau > 0.0f) || !std::isfinite(tau) || !(inv > 0.0f) || !std::isfinite(inv))
-    return invalid("temperature must be above 0, it and its inverse finite in binary32");
+    return invalid("temperature must be above 0, it and log2(e) / temperature finite in binary32");
   const int64_t size = elem_size(a->dtype);
   MSAMP_TRY(check_matrix(a->logits, R, V, a->ld_logits, size, false, "logits"));
   if (policy) {

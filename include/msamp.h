@@ -834,9 +834,10 @@ msamp_status msamp_recurrence_backward(const msamp_recurrence* args, void* works
  *   a small d keeps its digits. An action with a logit of -Inf is infinitely
  *   far from a reference that allows it (kl times Inf).
  *
- * Everything else is binary32; loss and logp are binary32, dlogits is rounded
- * once to dtype (with MSAMP_F16, values of 2^-25 or less become 0: dloss has
- * to carry a loss scale that keeps them above).
+ * Everything else is binary32 (so the distillation's KL is off by some 2^-23,
+ * and its loss by temperature^2 times that); loss and logp are binary32,
+ * dlogits is rounded once to dtype (with MSAMP_F16, values of 2^-25 or less
+ * become 0: dloss has to carry a loss scale that keeps them above).
  *
  * A row is left out (loss, logp 0, dlogits 0) when its teacher has no entry of
  * an id in [0, vocab) and above -Inf, when its action is outside [0, vocab),
@@ -867,7 +868,7 @@ typedef struct {
   int64_t ld_logits;
   const void* ids; /* distillation: [rows, top], rows ld_ids apart; policy: the actions [rows] */
   int64_t ld_ids;
-  double temperature; /* > 0; it and its inverse finite in binary32 */
+  double temperature; /* > 0; it and log2(e) / temperature finite in binary32 */
   float* loss;
   float* stats;
   const float* dloss;

@@ -193,6 +193,12 @@ def test_losses_refuse(which):
                  advantages=0, logp=0) == 0
 
 
+@pytest.mark.parametrize("which", ("distill", "policy"))
+def test_losses_refuse_a_temperature_whose_exponents_are_infinite(which):
+    for back in (False, True):  # 1 / 4e-39 is finite in binary32, log2(e) / 4e-39 is not
+        assert _lrun(which, back, temperature=4e-39) == 1 and "temperature" in _err()
+
+
 def test_losses_refuse_their_own():
     for bad in (dict(top=-1), dict(top=1025, ld_ids=1025, ld_teacher=1025), dict(teacher=0), dict(teacher_dtype=3), dict(ld_teacher=-1)):
         assert _lrun("distill", **bad) == 1, bad
