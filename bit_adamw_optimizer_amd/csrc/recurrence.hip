@@ -705,15 +705,16 @@ hipError_t tiles(const msamp_recurrence& a, const Spans& sp, hipStream_t s) {
   return hipGetLastError();
 }
 
-// A lane goes through all steps of few, and where a tile's steps do not lie
-// within the 2^31 bytes of a buffer.
+// A lane goes through all steps of few, where a tile's steps do not lie within
+// the 2^31 bytes of a buffer, and where steps share elements: the bounds of
+// such a buffer end inside a pair of a step behind it, which is read as a whole.
 bool lane_alone(const msamp_recurrence& a, bool backward) {
   if (a.time <= (backward ? kFewBackward : kFewForward)) return true;
   const int64_t most = ((int64_t)1 << 31) / (a.dtype == MSAMP_F32 ? 4 : 2) - a.channels;
   const int64_t tile = kChunk * waves_of(a);
-  auto far = [&](int64_t stride) { return stride >= most / tile; };
-  if (far(a.x_time) || far(a.gate_time)) return true;
-  return backward ? far(a.dy_time) || far(a.dx_time) || far(a.dgate_time) : far(a.y_time);
+  auto alone = [&](int64_t stride) { return stride >= most / tile || (stride > 0 && stride < a.channels); };
+  if (alone(a.x_time) || alone(a.gate_time)) return true;
+  return backward ? alone(a.dy_time) || alone(a.dx_time) || alone(a.dgate_time) : alone(a.y_time);
 }
 
 template <typename T, bool BACKWARD>

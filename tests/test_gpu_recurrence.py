@@ -349,8 +349,12 @@ def test_backward_from_repeated_and_overlapping_steps(shape, dtype):
     shifted = cube((1, 1, b * c + 3 * t), dt, 5, 0.5).as_strided(shape, (c, 3, 1))
     for n in (None, torch.tensor([t - 1, t // 2 + 1, 1][:b], device="cuda")):
         check(full[0], full[1], h0, n, full[2][:, :1].expand(shape), dl)
+        check(shifted, shifted, h0, n, shifted, dl)
+        for i in range(3) if t < 1000 else ():
+            args = [shifted if j == i else full[j] for j in range(3)]
+            check(args[0], args[1], h0, n, args[2], dl)
         for which in (0, 1, 2, None):
-            for v in ([p[:, :1].expand(shape) for p in full], [p[:1].expand(shape) for p in full], [shifted] * 3):
+            for v in ([p[:, :1].expand(shape) for p in full], [p[:1].expand(shape) for p in full]):
                 args = [v[i] if which in (i, None) else full[i] for i in range(3)]
                 outs = []
                 for x, g, dy in (args, [p.contiguous() for p in args]):
