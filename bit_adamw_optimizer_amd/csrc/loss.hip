@@ -261,7 +261,7 @@ struct Entries {
 // 366 us for the first. The arithmetic, two exponentials and about ten other
 // operations a logit, is 60% of the vector units' time at that rate, so several
 // rows have to be in different stages on a compute unit: that takes few
-// registers (64 for 32,000 16-bit logits, four workgroups a compute unit), for
+// registers (70 for 32,000 16-bit logits, three workgroups a compute unit), for
 // which there is no loop over rows (its constants would stay in registers: 112)
 // and the logits are unpacked again in each pass (145). Rows that start
 // anywhere are cut at their first 16 bytes (4,096 x 50,257: 178 us from the
@@ -568,7 +568,9 @@ hipError_t launch(const LossArgs& l, const Parts& parts, int count, hipStream_t 
 }
 
 // Rows that one workgroup does not hold in registers are cut into parts of
-// 32,768 16-bit or 16,384 binary32 logits.
+// 32,768 16-bit or 16,384 binary32 logits. Loss and gradient in one call read
+// such rows twice: 4,096 x 128,256 bfloat16, 2.1 GB, take 207 + 380 us, 2,048 x
+// 50,257 binary32, 823 MB, 75 + 136.
 constexpr int kPartBlock = 512, kPartPieces = 8;
 int64_t bytes_of(const msamp_vocab_loss& a) { return a.vocab * (a.dtype == MSAMP_F32 ? 4 : 2); }
 int64_t parts_of(const msamp_vocab_loss& a) {
@@ -578,7 +580,11 @@ bool in_parts(const msamp_vocab_loss& a) { return bytes_of(a) > 512 * 16 * 16; }
 
 // The smallest workgroup that holds a row in registers. Rows fit where their
 // pieces do: those logits behind the last whole piece have a register of their
-// own.
+// own. Each size against the next one, distillation of 2^27 bfloat16 logits with
+// their gradient, us: 512 a row 213 and 248, 1,024 132 and 177, 2,048 113 and
+// 187 (256 threads of one piece), 4,096 111 and 151, 8,192 91 and 139, 16,384 89
+// and 121, 32,768 97 and 106; 13 pieces and 16 at 34,000 108 and 121, at 45,000
+// 103 and 107, at 50,257 105 and 108.
 template <typename T, int KIND, int FROM>
 hipError_t whole(const LossArgs& l, hipStream_t s) {
   const int64_t pieces = (bytes_of(l.a) + 15) / 16;
@@ -607,7 +613,8 @@ hipError_t forward(const LossArgs& l, void* ws, hipStream_t s) {
 }
 
 // Parts read the logits at every class, so in place a long row stays with one
-// workgroup, which reads them before it writes.
+// workgroup, which reads them before it writes: 500 x 131,072 binary32 take 106
+// us (96 in parts, the gradient apart), 4,096 x 128,256 bfloat16 418 (393).
 template <typename T, int KIND>
 hipError_t backward(const LossArgs& l, hipStream_t s) {
   if (!in_parts(l.a)) return whole<T, KIND, kGivenSums>(l, s);

@@ -748,8 +748,10 @@ msamp_status msamp_embedding_backward(int64_t rows, int64_t vocab, int64_t cols,
  * elements of one step consecutive, *_batch and *_time the distances between
  * sequences and between steps in elements (any order of the two; x and gate
  * may be column ranges of one projection's output, and a step that is read
- * may be repeated by a distance of 0). y may be x or gate, dx and dgate may
- * each be one of dy, x and gate (the same tensor).
+ * may be repeated by a distance of 0, or share elements with the next one,
+ * which is slow). y may be x or gate, dx and dgate may each be one of dy, x
+ * and gate (the same tensor). Tensors of the same distances may otherwise lie
+ * in one buffer where they share no element (halves of its steps or channels).
  *   lengths    NULL, or device [batch] of length_bytes 4 or 8: the steps of
  *              each sequence, taken as 0 below 0 and as time above it. What
  *              lies behind them is neither read nor written.

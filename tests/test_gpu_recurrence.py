@@ -413,3 +413,21 @@ def test_the_largest_number_of_sequences():
         R.assert_near(x[at:at + 1], hs[:, 1:], errs[:, 1:], "y")
         R.assert_near(y[i:i + 1], hs[:, 1:], errs[:, 1:], "y of three")
     assert torch.equal(x[1], x[B // 2 + 1]) and (x[1:-1].amax(0) == x[1]).all() and (x[1:-1].amin(0) == x[1]).all()
+
+
+@pytest.mark.parametrize("time", [1, 17])
+def test_every_gate_keeps_its_digits(time):
+    """y = 1 - a from x = 1 and no state, and y = a from h0 = 1 and x = 0. e^-|g| comes from a power of 2 (two units of
+    U), its product with what the exponent's rounding left (one), ln 2's own rounding (|g| U / 21); 1 + e, a reciprocal
+    and a product (four) follow. The larger of the two is 1 less the smaller."""
+    g = torch.cat([torch.linspace(-86, 86, 4001), torch.linspace(-1, 1, 1001)])[None, None].cuda()
+    want = torch.sigmoid(-g.double())
+    bound = (8 + g.double().abs() / 16) * R.U * torch.minimum(want, 1 - want) + torch.where(want > 0.5, R.U / 2, 0.0)
+    shape = (1, time, g.shape[2])
+    one = (torch.arange(time, device="cuda") == 0)[None, :, None].expand(shape)
+    open_behind = torch.where(one, g, torch.full_like(g, 200.0)).contiguous()  # the later steps keep the state
+    x, y = torch.where(one, 1.0, 0.0).contiguous(), torch.empty(shape, device="cuda")
+    M.recurrence_forward(x, open_behind, y)
+    assert ((y[:, -1:].double() - want).abs() <= bound).all()
+    M.recurrence_forward(torch.zeros_like(x), torch.where(one, -g, open_behind).contiguous(), y, h0=torch.ones(1, shape[2], device="cuda"))
+    assert ((y[:, -1:].double() - want).abs() <= bound).all()
