@@ -44,6 +44,9 @@ __global__ __launch_bounds__(kBlock) void k_embedding_forward(EmbeddingArgs a) {
   }
 }
 
+// The fewest lanes that hold a row, up to 64 with 8 columns each; measured, us, against the neighbouring sizes
+// (2^26 bfloat16 elements, ids spread evenly): 64 columns 12 with 8 lanes, 23 with 32; 256 columns 40 with 32, 50 with
+// 64; 512 columns 40 with 64, 54 with 256; 1,024 columns 43 with 256, 40 with 64; 4,096 columns 40 and 42.
 template <typename T>
 hipError_t forward(const EmbeddingArgs& a, hipStream_t s) {
   auto run = [&](auto lanes) -> hipError_t {
@@ -442,6 +445,11 @@ hipError_t backward(const EmbeddingArgs& a, void* ws, hipStream_t s) {
     }
     return hipSuccess;
   };
+  // lanes and columns a lane that hold a row, up to 4,096 columns at a time; us against the neighbouring sizes (the
+  // forward rows' gradient into 2^27 elements): 32 columns 202 with 8 lanes, 301 with 32; 128 columns 288 with 32, 279
+  // with 64; 256 columns 319, with 64 x 2 303; 512 columns 243 with 64 x 2, 332 x 1, 337 x 4; 1,024 columns 182 with 64
+  // x 4, 166 x 2, 267 with 128 x 4; 2,048 columns 160 with 128 x 4, 156 with 64, 227 with 256; 4,096 columns 143 with
+  // 256 x 4, 145 with 128
   const int64_t units = (a.cols + 3) / 4;
   using std::integral_constant;
   if (units <= 8) return run(integral_constant<int, 8>(), integral_constant<int, 1>());

@@ -569,7 +569,7 @@ hipError_t launch(const LossArgs& l, const Parts& parts, int count, hipStream_t 
 
 // Rows that one workgroup does not hold in registers are cut into parts of
 // 32,768 16-bit or 16,384 binary32 logits. Loss and gradient in one call read
-// such rows twice: 4,096 x 128,256 bfloat16, 2.1 GB, take 207 + 380 us, 2,048 x
+// such rows twice: 4,096 x 128,256 bfloat16, 2.1 GB, take 208 + 390 us, 2,048 x
 // 50,257 binary32, 823 MB, 75 + 136.
 constexpr int kPartBlock = 512, kPartPieces = 8;
 int64_t bytes_of(const msamp_vocab_loss& a) { return a.vocab * (a.dtype == MSAMP_F32 ? 4 : 2); }

@@ -200,9 +200,9 @@ __global__ __launch_bounds__(kBlock) void k_backward_lane(msamp_recurrence a, in
 // then go through their steps with the state they start from. The next tile's
 // loads are under way meanwhile.
 //
-// Bound by memory: 4 x 4,096 steps of 4,096 bfloat16 channels take 88 us
-// forward (411 MB, 4.7 TB/s; 72 where the last call left part in the cache) and
-// 156 us backward (679 MB, 4.4 TB/s; 135; x, gate and dy are read once, h comes
+// Bound by memory: 4 x 4,096 steps of 4,096 bfloat16 channels take 91 us
+// forward (411 MB, 4.5 TB/s; 72 where the last call left part in the cache) and
+// 159 us backward (679 MB, 4.3 TB/s; 135; x, gate and dy are read once, h comes
 // from the saved states); a lane that goes through all steps alone takes 2,627 and 5,664 us. A tile's loads have to be under way
 // for the whole of the tile before it: nothing in the loop may wait for memory
 // (a state loaded before the loop is waited for there, no value goes through
@@ -652,6 +652,9 @@ constexpr int64_t kEnoughGroups = 192;  // workgroups from which sequences are l
 constexpr int64_t kSpanGroups = 256;    // of sequences that are cut
 constexpr int64_t kMostSpans = 64;
 
+// The waves side by side that a sequence fills, up to 8. Measured (4,096 bfloat16 channels, us forward): 64 x 32 steps 11
+// with 1 wave, 19 with 2; 64 x 64 21 with 2, 20 with 1, 34 with 4; 32 x 128 21 with 4, 46 with 8; 4 x 256 7.9 with 8, 8.4
+// with 4, 17 with 1; 16 x 256 26 with 8, 21 with 4.
 // A launch has less than 2^32 threads: 2^22 sequences of up to 64 binary32 channels, two workgroups each, take 4 waves.
 int waves_of(const msamp_recurrence& a) {
   const int64_t channels = a.dtype == MSAMP_F32 ? 32 : 64;  // of a workgroup
@@ -684,6 +687,7 @@ Spans spans_of(const msamp_recurrence& a, void* ws, bool backward) {
   const int64_t each = (tiles + count - 1) / count;
   s.count = (int32_t)((tiles + each - 1) / each);
   s.steps = (int32_t)(each * tile);
+  // (Times here are of gates two operations shorter, 1 to 2% less.)
   // Lines that neighbours share (steps that do not start on 128 bytes): all of a die's workgroups side by side. 2 x
   // 16,411 x 1,000: 40 us forward and 73 backward, in turn 55 and 103. Whole lines: in turn (4 x 4,096 x
   // 4,096: 88 us and 156; four to a die 92 and 164). Outputs go past the caches where lines are whole (there 88 and
