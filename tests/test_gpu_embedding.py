@@ -207,3 +207,22 @@ def test_the_order_of_the_sum(rows, vocab, cols):
             total = part if len(cuts) == 2 else total + part
         want[k], at = total, at + n
     assert torch.equal(backward(dy, ids, vocab).cpu(), want)
+
+
+def test_more_rows_than_a_launch_has():
+    """More than 2^20 workgroups: looked up in turns, gradients in slices of the vocabulary or of the rows."""
+    n = (1 << 20) + 3
+    ids = torch.arange(n, device="cuda") % 7
+    w = rows_of(7, 520, 0, torch.float16, 1)
+    y = torch.zeros(n, 520, dtype=torch.float16, device="cuda")
+    M.embedding_forward(ids, w, y)
+    assert torch.equal(y, w[ids])
+    del y
+    dw = torch.full((n, 2049), 7.0, device="cuda")
+    few = torch.tensor([n - 1, 0, n - 1], device="cuda")
+    M.embedding_backward(torch.ones(3, 2049, dtype=torch.float16, device="cuda"), few, dw)
+    assert (dw[0] == 1).all() and (dw[-1] == 2).all() and not dw[1:-1].any()
+    del dw
+    dw = torch.ones(7, 2049, device="cuda")
+    M.embedding_backward(torch.ones(n, 2049, dtype=torch.float16, device="cuda"), ids, dw, accumulate=True)
+    assert torch.equal(dw[:, 0].cpu(), 1.0 + torch.bincount(ids.cpu(), minlength=7)) and (dw == dw[:, :1]).all()

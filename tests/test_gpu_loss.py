@@ -365,3 +365,34 @@ def test_temperatures_far_from_one(tau):
     z, t = matrix(rows, vocab, torch.float32, 0, 1), matrix(rows, 5, torch.float32, 0, 2)
     loss, _, _ = check_distill(z, classes(rows, vocab, 5, 3), t, tau, torch.full((rows,), 8.0, device="cuda"))
     assert (loss > 0).all()
+
+
+def test_more_rows_than_a_launch_has():
+    """Rows in slices of 2^20."""
+    rows, vocab = (1 << 20) + 3, 5
+    z = matrix(rows, vocab, torch.float32, 0, 1)
+    act, old, ref, adv = rollout(z, 1.0, 2)
+    act[7::11] = -1
+    lp = torch.log_softmax(z.double(), 1).gather(1, act.clamp_min(0)[:, None])[:, 0]
+    near_bound = torch.minimum(((lp - old).exp() / 1.2 - 1).abs(), ((lp - old).exp() - 0.8).abs()) < 1e-4
+    act[near_bound] = -1
+    check_policy(z, act, old, adv, 1.0, ref, 0.1, dloss=torch.full((rows,), 64.0, device="cuda"))
+    check_distill(z, torch.stack([act, act + 1], 1), z[:, :2].contiguous(), 2.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_longest_row(dtype):
+    """2^29 logits, all but two equal: sums of a power of two and exact exponentials."""
+    vocab = 1 << 29
+    z = torch.zeros(1, vocab, dtype=DT[dtype], device="cuda")
+    act = torch.tensor([vocab - 1], device="cuda")
+    old, adv = torch.full((1,), -20.0, device="cuda"), torch.ones(1, device="cuda")
+    loss, logp, stats = torch.empty(1, device="cuda"), torch.empty(1, device="cuda"), torch.empty(1, 2, device="cuda")
+    want = -math.log(vocab)
+    M.policy_loss_forward(z, act, old, adv, loss, logp=logp, stats=stats, clip_high=INF, dlogits=z,
+                          dloss=torch.full((1,), float(vocab), device="cuda"))
+    assert stats.tolist() == [[0.0, float(vocab)]] and abs(logp.item() - want) <= R.U * abs(want)
+    r = math.exp(want + 20.0)
+    # dlogits = -dloss r (onehot - q): r elsewhere, within the roundings of r, the factor, the product and the type
+    tol = (8 * R.U + R.half(DT[dtype])) * r
+    assert ((z[0, :-1].float() - r).abs().amax() <= tol) and abs(z[0, -1].double().item() / (-r * (vocab - 1)) - 1) <= tol / r
